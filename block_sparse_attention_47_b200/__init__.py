@@ -487,3 +487,8 @@ __all__ = ["Problem", "Sizes", "BSAError", "BlockSparseAttention", "lib", "keep_
            "window_attn_fwd_raster", "select_topk_gated", "sparse_attn_fwd_lse",
            "bwd_workspace_bytes", "sparse_attn_bwd",
            "FIXED_444", "DYNAMIC_888", "LIB_PATH"]
+
+from . import seq  # noqa: E402  (uses the loader above)
+from .seq import *  # noqa: E402,F401,F403
+
+__all__ += seq.__all__

@@ -11,6 +11,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "bsa_internal.cuh"
+#include "seq_internal.cuh"
 
 namespace bsa {
 size_t select_smem_bytes(const Geo& g);
@@ -279,6 +280,34 @@ bsa_status check_raster_kv(const Geo& g, int64_t sh, const char* name) {
 }
 
 }  // namespace
+
+// the host-side checks above, for the token-sequence entry points
+namespace bsa {
+void clear_error() { g_last_error[0] = 0; }
+bsa_status cuda_error(cudaError_t e, const char* what) { return cuda_fail(e, what); }
+bsa_status require_device() { return check_device(); }
+bsa_status resolve_status(int32_t** status) { return status_word(status); }
+bool stall_enabled() { return g_stall_pv != 0; }
+void range_push(const char* name) { nvtxRangePushA(name); }
+void range_pop() { nvtxRangePop(); }
+
+bsa_status make_rows_map(CUtensorMap* m, const void* ptr, int64_t rows, int heads, int d,
+                         int64_t stride_n, int64_t stride_h, int box_rows, bool fp16) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(BSA_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  cuuint64_t dims[3] = {cuuint64_t(d), cuuint64_t(heads), cuuint64_t(rows)};
+  cuuint64_t strides[2] = {cuuint64_t(stride_h) * 2, cuuint64_t(stride_n) * 2};
+  cuuint32_t box[3] = {64, 1, cuuint32_t(box_rows)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                  const_cast<void*>(ptr), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(BSA_ERR_CUDA, "cuTensorMapEncodeTiled (packed rows) failed (%d)", int(r));
+  return BSA_OK;
+}
+}  // namespace bsa
 
 extern "C" {
 

@@ -1,0 +1,152 @@
+"""Host-side checks of the token-sequence entry points that need no GPU: the
+library exports what include/bsa_seq.h declares, the header is strict C99,
+and invalid arguments are refused before any launch."""
+import ctypes
+import os
+import re
+import shutil
+import subprocess
+
+import pytest
+import torch
+
+import block_sparse_attention_47_b200 as bsa
+from block_sparse_attention_47_b200 import seq
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+INVALID, SHAPE, UNSUPPORTED, WORKSPACE = 1, 2, 3, 4
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from block_sparse_attention_47_b200 import build
+    build.build()
+    return bsa.lib()
+
+
+def test_exports_every_declared_symbol():
+    text = open(os.path.join(ROOT, "include", "bsa_seq.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    names = set(re.findall(r"\b(bsa_[a-z_0-9]+)\s*\(", text))
+    assert names == set(seq._SIGS), "binding and header disagree"
+    for n in names:
+        assert hasattr(bsa.lib(), n), n
+
+
+@pytest.mark.skipif(shutil.which("gcc") is None, reason="no C compiler")
+def test_header_is_strict_c99(tmp_path):
+    src = tmp_path / "client.c"
+    src.write_text('#include "bsa_seq.h"\n'
+                   "int main(void) { bsa_seq_problem p = {8, 2, 96, BSA_DTYPE_FP16, 1, 0.1f};\n"
+                   "  size_t n; return bsa_query_decode_workspace(&p, &n) == BSA_ERR_UNSUPPORTED "
+                   "? 0 : 1; }\n")
+    exe = tmp_path / "client"
+    libdir = os.path.dirname(bsa.LIB_PATH)
+    cc = subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-pedantic", "-Werror",
+                         "-I", os.path.join(ROOT, "include"), str(src), "-L", libdir, "-lbsa",
+                         "-Wl,-rpath," + libdir, "-o", str(exe)], capture_output=True, text=True)
+    assert cc.returncode == 0, cc.stderr
+    assert subprocess.run([str(exe)], timeout=60).returncode == 0
+
+
+def prob(**kw):
+    d = dict(heads=8, kv_heads=2, head_dim=64)
+    d.update(kw)
+    return bsa.SeqProblem.make(**d)
+
+
+@pytest.mark.parametrize("field,value,status", [
+    ("head_dim", 96, UNSUPPORTED), ("head_dim", 0, UNSUPPORTED), ("heads", 0, SHAPE),
+    ("kv_heads", 0, SHAPE), ("kv_heads", 3, SHAPE), ("heads", 65536, SHAPE), ("dtype", 2, INVALID),
+    ("causal", 2, INVALID), ("softmax_scale", 0.0, INVALID),
+    ("softmax_scale", float("nan"), INVALID)])
+def test_invalid_problems_are_refused(field, value, status):
+    p = prob()
+    setattr(p, field, value)
+    with pytest.raises(bsa.BSAError) as e:
+        bsa.decode_workspace_bytes(p)
+    assert e.value.status == status
+
+
+def test_dtype_of_the_problem():
+    with pytest.raises(ValueError):
+        prob(dtype=torch.float32)
+    assert prob(dtype=torch.float16).torch_dtype == torch.float16
+
+
+def decode_args(**kw):
+    """Arguments of bsa_paged_attn_decode that pass every host check."""
+    a = dict(prob=ctypes.byref(prob()), n_seqs=2, q=16, q_sn=512, q_sh=64, k=16, v=16, n_pages=4,
+             page_size=16, sp=2048, st=128, sh=64, table=16, table_stride=4, table_width=4, lens=16,
+             o=16, o_sn=512, o_sh=64, ws=16, ws_bytes=1 << 30, status=None, stream=None)
+    a.update(kw)
+    return list(a.values())
+
+
+DECODE_BAD = [
+    (dict(prob=None), INVALID, b"problem"), (dict(n_seqs=-1), SHAPE, b"n_seqs"),
+    (dict(n_seqs=1 << 25), SHAPE, b"n_seqs"), (dict(q=None), INVALID, b"q is NULL"),
+    (dict(q=24), INVALID, b"aligned"), (dict(q_sh=60), INVALID, b"strides"),
+    (dict(q_sn=-512), INVALID, b"strides"), (dict(k=None), INVALID, b"k_cache"),
+    (dict(v=8), INVALID, b"v_cache"), (dict(n_pages=0), SHAPE, b"n_pages"),
+    (dict(page_size=0), SHAPE, b"page_size"), (dict(sp=2052), INVALID, b"cache strides"),
+    (dict(st=8), INVALID, b"cache strides"), (dict(sh=0), INVALID, b"cache strides"),
+    (dict(table=None), INVALID, b"block_table"), (dict(table=18), INVALID, b"block_table"),
+    (dict(table_width=0), SHAPE, b"block_table"), (dict(table_stride=3), SHAPE, b"block_table"),
+    (dict(lens=None), INVALID, b"seq_lens"), (dict(o=None), INVALID, b"o is NULL"),
+    (dict(o_sh=0), INVALID, b"o is written"), (dict(ws=None), INVALID, b"workspace"),
+    (dict(ws_bytes=16), WORKSPACE, b"workspace"), (dict(status=2), INVALID, b"dev_status"),
+]
+
+
+@pytest.mark.parametrize("kw,status,word", DECODE_BAD, ids=[str(k) for k, _, _ in DECODE_BAD])
+def test_decode_refuses(kw, status, word):
+    rc = seq._fn("bsa_paged_attn_decode")(*decode_args(**kw))
+    assert rc == status, (rc, bsa.lib().bsa_last_error())
+    assert word in bsa.lib().bsa_last_error()
+
+
+def test_empty_batches_need_no_device():
+    assert seq._fn("bsa_paged_attn_decode")(*decode_args(n_seqs=0)) == 0
+    assert seq._fn("bsa_kv_append")(*append_args(n=0)) == 0
+
+
+def append_args(**kw):
+    a = dict(prob=ctypes.byref(prob()), n_seqs=2, n=5, k=16, k_sn=128, k_sh=64, v=16, v_sn=128,
+             v_sh=64, kc=16, vc=16, n_pages=4, page_size=16, sp=2048, st=128, sh=64, table=16,
+             table_stride=4, table_width=4, cu=16, lens=16, rope=16, rope_n=100, rot=64,
+             interleaved=0, rope_rows=None, q=16, q_sn=512, q_sh=64, qo=16, qo_sn=512, qo_sh=64,
+             ko=16, ko_sn=128, ko_sh=64, status=None, stream=None)
+    a.update(kw)
+    return list(a.values())
+
+
+APPEND_BAD = [
+    (dict(n=-1), SHAPE, b"n_tokens"), (dict(n=1 << 31), SHAPE, b"n_tokens"),
+    (dict(k=None), INVALID, b"k is NULL"), (dict(v=4), INVALID, b"v is not"),
+    (dict(k_sn=4), INVALID, b"k strides"), (dict(kc=None), INVALID, b"k_cache"),
+    (dict(cu=None), INVALID, b"cu_new"), (dict(cu=2), INVALID, b"cu_new"),
+    (dict(lens=6), INVALID, b"seq_lens"), (dict(rope=8), INVALID, b"rope"),
+    (dict(rope_n=0), SHAPE, b"rope_n"), (dict(rot=24), SHAPE, b"rot_dim"),
+    (dict(rot=80), SHAPE, b"rot_dim"), (dict(rot=0), SHAPE, b"rot_dim"),
+    (dict(rope_rows=3), INVALID, b"rope_rows"), (dict(q=None), INVALID, b"q and q_out"),
+    (dict(qo=None), INVALID, b"q and q_out"), (dict(qo_sn=0), INVALID, b"q_out is written"),
+    (dict(ko=8), INVALID, b"k_out"), (dict(ko_sh=0), INVALID, b"k_out is written"),
+    (dict(status=1), INVALID, b"dev_status"),
+]
+
+
+@pytest.mark.parametrize("kw,status,word", APPEND_BAD, ids=[str(k) for k, _, _ in APPEND_BAD])
+def test_append_refuses(kw, status, word):
+    rc = seq._fn("bsa_kv_append")(*append_args(**kw))
+    assert rc == status, (rc, bsa.lib().bsa_last_error())
+    assert word in bsa.lib().bsa_last_error()
+
+
+def test_binding_refuses_host_tensors():
+    t = torch.zeros(3, 8, 64, dtype=torch.bfloat16)
+    i = torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        bsa.paged_attn_decode(prob(), t, None, None, None, i, t, None)
+    with pytest.raises(ValueError, match="CUDA"):
+        bsa.kv_append(prob(), t, t, None, None, None, i, i)
