@@ -18,8 +18,6 @@
 // with the head group as M: K and V are read from shared memory once for all
 // heads of the group, which plain FMAs could not keep up with for more than
 // a few heads; the wide (tcgen05) form would need 128 rows.
-#include <type_traits>
-
 #include "seq_internal.cuh"
 
 namespace bsa {

@@ -121,10 +121,32 @@ bsa_status check_counts(int32_t n_seqs, int64_t rows, const char* what) {
   return BSA_OK;
 }
 
+// one CTA per 128-row tile and head at most
+bsa_status check_grid(int64_t rows, int32_t n_seqs, int heads) {
+  if ((rows / 128 + (n_seqs < rows ? n_seqs : rows)) * heads > INT32_MAX)
+    return fail(BSA_ERR_SHAPE, "too many (tile, head) pairs for one call");
+  return BSA_OK;
+}
+
 bsa_status check_status(const int32_t* p) {
   if (p && (reinterpret_cast<uintptr_t>(p) & 3u))
     return fail(BSA_ERR_INVALID_ARG, "dev_status is not 4-byte aligned");
   return BSA_OK;
+}
+
+// a tensor read by TMA boxes: broadcast views have no tensor map
+bsa_status check_tma_rows(bsa::Rows* r, const SeqGeo& g, const void* p, int64_t sn, int64_t sh,
+                          int64_t rows, int heads, const char* name) {
+  SEQ_TRY(check_rows(r, p, sn, sh, rows, heads, g.d, false, name));
+  if (r->sn == 0 || r->sh == 0)
+    return fail(BSA_ERR_INVALID_ARG, "%s: strides of 0 (broadcast views) are not supported", name);
+  return BSA_OK;
+}
+
+// its map of 128-row boxes (zeros for an empty tensor, which is not read)
+bsa_status rows_map(CUtensorMap* m, const SeqGeo& g, const bsa::Rows& r, int64_t rows, int heads) {
+  std::memset(m, 0, sizeof(*m));
+  return rows ? bsa::make_rows_map(m, r.p, rows, heads, g.d, r.sn, r.sh, 128, g.fp16) : BSA_OK;
 }
 
 bsa_status done(cudaError_t e, const char* what) {
@@ -191,6 +213,50 @@ bsa_status bsa_kv_append(const bsa_seq_problem* prob, int32_t n_seqs, int64_t n_
   io.status = dev_status;
   return done(bsa::launch_kv_append(g, c, io, static_cast<cudaStream_t>(stream)),
               "bsa_kv_append launch");
+}
+
+bsa_status bsa_packed_attn_fwd(const bsa_seq_problem* prob, int32_t n_seqs, int64_t total_q,
+                               int64_t total_k, const void* q, int64_t q_stride_n,
+                               int64_t q_stride_h, const void* k, int64_t k_stride_n,
+                               int64_t k_stride_h, const void* v, int64_t v_stride_n,
+                               int64_t v_stride_h, const int32_t* cu_q, const int32_t* cu_k,
+                               void* o, int64_t o_stride_n, int64_t o_stride_h, float* lse,
+                               int32_t* dev_status, void* stream) {
+  SEQ_RANGE();
+  SeqGeo g;
+  SEQ_TRY(make_geo(prob, &g));
+  SEQ_TRY(check_counts(n_seqs, total_q, "total_q"));
+  SEQ_TRY(check_counts(n_seqs, total_k, "total_k"));
+  if (total_q == 0 || n_seqs == 0) return BSA_OK;
+  SEQ_TRY(check_grid(total_q, n_seqs, g.heads));
+  bsa::PackedIO io{};
+  bsa::Rows rq, rk{}, rv{};
+  SEQ_TRY(check_ptr(cu_q, "cu_q", 4));
+  SEQ_TRY(check_ptr(cu_k, "cu_k", 4));
+  SEQ_TRY(check_rows(&io.o, o, o_stride_n, o_stride_h, total_q, g.heads, g.d, true, "o"));
+  if (lse) SEQ_TRY(check_ptr(lse, "lse", 4));
+  SEQ_TRY(check_status(dev_status));
+  SEQ_TRY(check_tma_rows(&rq, g, q, q_stride_n, q_stride_h, total_q, g.heads, "q"));
+  if (total_k > 0) {  // else no row sees a key
+    SEQ_TRY(check_tma_rows(&rk, g, k, k_stride_n, k_stride_h, total_k, g.kv_heads, "k"));
+    SEQ_TRY(check_tma_rows(&rv, g, v, v_stride_n, v_stride_h, total_k, g.kv_heads, "v"));
+  }
+  SEQ_TRY(bsa::require_device());
+  CUtensorMap maps[3];
+  SEQ_TRY(rows_map(&maps[0], g, rq, total_q, g.heads));
+  SEQ_TRY(rows_map(&maps[1], g, rk, total_k, g.kv_heads));
+  SEQ_TRY(rows_map(&maps[2], g, rv, total_k, g.kv_heads));
+  SEQ_TRY(bsa::resolve_status(&dev_status));
+  io.cu_q = cu_q;
+  io.cu_k = cu_k;
+  io.n_seqs = n_seqs;
+  io.total_q = total_q;
+  io.total_k = total_k;
+  io.lse = lse;
+  io.status = dev_status;
+  io.stall = bsa::stall_enabled();
+  return done(bsa::launch_packed_fwd(g, maps, io, static_cast<cudaStream_t>(stream)),
+              "bsa_packed_attn_fwd launch");
 }
 
 bsa_status bsa_query_decode_workspace(const bsa_seq_problem* prob, size_t* bytes) {

@@ -5,6 +5,8 @@
 
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "../../include/bsa_seq.h"
 #include "bsa_internal.cuh"
 
@@ -66,6 +68,20 @@ struct DecodeIO {
   void* workspace;
   int32_t* status;
 };
+// Pointers of one packed forward; maps: Q, K, V (128-row boxes; K and V are
+// not read when total_k is 0).
+struct PackedIO {
+  const int32_t *cu_q, *cu_k;
+  int n_seqs;
+  int64_t total_q, total_k;
+  Rows o;
+  float* lse;  // [heads, total_q], exp2 domain, or null
+  int32_t* status;
+  int stall;   // test hook: no PV is issued
+};
+cudaError_t launch_packed_fwd(const SeqGeo& g, const CUtensorMap* maps, const PackedIO& io,
+                              cudaStream_t st);
+
 cudaError_t launch_paged_decode(const SeqGeo& g, const PagedCache& c, const DecodeIO& io,
                                 cudaStream_t st);
 
@@ -95,6 +111,97 @@ __device__ __forceinline__ float2 unpack2<__half>(uint32_t u) {
 
 __device__ __forceinline__ void report_invalid(int32_t* status) {
   atomicCAS(status, 0, int32_t(BSA_ERR_INVALID_ARG));
+}
+
+// Instruction descriptor of kind::f16 with fp16 or bf16 A and B, fp32 D.
+template <typename T>
+__host__ __device__ constexpr uint32_t idesc_f32(int M, int N, bool b_mn_major) {
+  return idesc_bf16_f32(M, N, b_mn_major) &
+         (std::is_same<T, __half>::value ? ~((1u << 7) | (1u << 10)) : ~0u);
+}
+
+// 128 columns of this thread's tensor-memory lane
+#define BSA_TMEM_LD128(taddr, r)  \
+  asm volatile(  \
+      "tcgen05.ld.sync.aligned.32x32b.x128.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63,%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95,%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%128];\n\t"  \
+      "tcgen05.wait::ld.sync.aligned;"  \
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]), "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]), "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]), "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]), "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]), "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]), "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]), "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]), "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])  \
+      : "r"(taddr)  \
+      : "memory")
+
+// ---- packed sequences ------------------------------------------------------------
+// One sequence of a packed call; offsets that descend or leave the tensor are
+// reported and read as an empty sequence.
+struct Span {
+  int start, len;
+};
+__device__ __forceinline__ Span span_of(const int32_t* __restrict__ cu, int b, int64_t total,
+                                        int32_t* status) {
+  const int a = __ldg(cu + b), z = __ldg(cu + b + 1);
+  if (a < 0 || z < a || z > total) {
+    report_invalid(status);
+    return {0, 0};
+  }
+  return {a, z - a};
+}
+
+// The tile `target` of the list of all sequences' tiles of `rows` rows, last
+// sequence and last tile first (in causal order the longest walks come
+// first), by a whole warp.  False when the list is shorter.
+__device__ __forceinline__ bool find_tile(const int32_t* __restrict__ cu, int n_seqs, int64_t total,
+                                          int rows, int64_t target, int lane, int32_t* status,
+                                          int& seq, int& tile) {
+  int64_t before = 0;
+  for (int base = 0; base < n_seqs; base += 32) {
+    const int b = n_seqs - 1 - base - lane;
+    const int n = b >= 0 ? (span_of(cu, b, total, status).len + rows - 1) / rows : 0;
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const bool here = before + incl > target;
+    const uint32_t m = __ballot_sync(0xffffffffu, here);
+    if (m) {
+      const int l = __ffs(m) - 1;
+      const int n_l = __shfl_sync(0xffffffffu, n, l), incl_l = __shfl_sync(0xffffffffu, incl, l);
+      seq = n_seqs - 1 - base - l;
+      tile = n_l - 1 - int(target - (before + incl_l - n_l));
+      return true;
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return false;
+}
+
+__device__ __forceinline__ void report_timeout(volatile int* abort_flag, int32_t* status) {
+  *abort_flag = 1;
+  atomicCAS(status, 0, int32_t(BSA_ERR_TIMEOUT));
+}
+
+// 2^x for two lanes on the FMA pipe: 2^n * 2^f, n the nearest integer (from
+// adding 1.5 * 2^23), 2^f on [-0.5, 0.5] by a degree-4 polynomial fitted for
+// the least largest relative error (2.7e-6).  x is clamped at -125 so that
+// the result stays a normal number.
+__device__ __forceinline__ void exp2_fma_x2(float& y0, float& y1, float x0, float x1) {
+  constexpr float kRound = 12582912.f;  // 1.5 * 2^23
+  constexpr float c0 = 0.99999928f, c1 = 0.69312179f, c2 = 0.24024744f, c3 = 0.05591786f,
+                  c4 = 0.00957010f;
+  x0 = fmaxf(x0, -125.f);
+  x1 = fmaxf(x1, -125.f);
+  float t0, t1, n0, n1, f0, f1, p0, p1;
+  add_f32x2(t0, t1, x0, x1, kRound, kRound);
+  add_f32x2(n0, n1, t0, t1, -kRound, -kRound);
+  add_f32x2(f0, f1, x0, x1, -n0, -n1);
+  fma_f32x2(p0, p1, f0, f1, c4, c4, c3, c3);
+  fma_f32x2(p0, p1, p0, p1, f0, f1, c2, c2);
+  fma_f32x2(p0, p1, p0, p1, f0, f1, c1, c1);
+  fma_f32x2(p0, p1, p0, p1, f0, f1, c0, c0);
+  // the low bits of t hold n (two's complement); shifted into the exponent
+  // field, the constant's own bits fall off the top
+  y0 = __int_as_float(__float_as_int(p0) + int(uint32_t(__float_as_int(t0)) << 23));
+  y1 = __int_as_float(__float_as_int(p1) + int(uint32_t(__float_as_int(t1)) << 23));
 }
 #endif
 

@@ -52,6 +52,8 @@ _PROB = ctypes.POINTER(SeqProblem)
 _ROWS = [_P, _I64, _I64]
 _CACHE = [_P, _P, _I32, _I32, _I64, _I64, _I64, _P, _I64, _I32]
 _SIGS = {
+    "bsa_packed_attn_fwd": [_PROB, _I32, _I64, _I64, *_ROWS, *_ROWS, *_ROWS, _P, _P, *_ROWS, _P,
+                            _P, _P],
     "bsa_kv_append": [_PROB, _I32, _I64, *_ROWS, *_ROWS, *_CACHE, _P, _P, _P, _I32, _I32, _I32, _P,
                       *_ROWS, *_ROWS, *_ROWS, _P, _P],
     "bsa_query_decode_workspace": [_PROB, ctypes.POINTER(ctypes.c_size_t)],
@@ -141,7 +143,29 @@ def _call(name, dev, stream, *args):
             _check(f(*args, stream.cuda_stream))
 
 
+def _lse_ptr(prob, t, rows, dev):
+    if t.device != dev or t.dtype != torch.float32 or tuple(t.shape) != (prob.heads, rows) or \
+            not t.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 [%d, %d] on %s" % (prob.heads, rows, dev))
+    return t.data_ptr()
+
+
 # ---- entry points ----------------------------------------------------------------
+def packed_attn_fwd(prob, q, k, v, cu_q, cu_k, out, lse=None, dev_status=None, stream=None):
+    """Attention over packed sequences (bsa_packed_attn_fwd): q and out
+    [total_q, heads, head_dim], k and v [total_k, kv_heads, head_dim], cu_q
+    and cu_k [n_seqs + 1] row offsets.  prob.causal aligns the last query
+    with the last key.  lse, float32 [heads, total_q], receives the rows'
+    log-sum-exp (exp2 domain) for packed_attn_bwd."""
+    dev = _device(q, "q")
+    tq, tk, n_seqs = q.shape[0], k.shape[0], cu_q.shape[0] - 1
+    _call("bsa_packed_attn_fwd", dev, stream, ctypes.byref(prob), n_seqs, tq, tk,
+          *_rows(prob, q, tq, prob.heads, dev, "q"), *_rows(prob, k, tk, prob.kv_heads, dev, "k"),
+          *_rows(prob, v, tk, prob.kv_heads, dev, "v"), _ints(cu_q, n_seqs + 1, dev, "cu_q"),
+          _ints(cu_k, n_seqs + 1, dev, "cu_k"), *_rows(prob, out, tq, prob.heads, dev, "out"),
+          None if lse is None else _lse_ptr(prob, lse, tq, dev), _status_ptr(dev_status, dev))
+
+
 def kv_append(prob, k, v, k_cache, v_cache, block_table, cu_new, seq_lens, rope=None,
               interleaved=False, rope_rows=None, q=None, q_out=None, k_out=None, dev_status=None,
               stream=None):
@@ -201,4 +225,4 @@ def paged_attn_decode(prob, q, k_cache, v_cache, block_table, seq_lens, out, wor
           *_workspace(workspace, dev), _status_ptr(dev_status, dev))
 
 
-__all__ = ["SeqProblem", "kv_append", "decode_workspace_bytes", "paged_attn_decode"]
+__all__ = ["SeqProblem", "packed_attn_fwd", "kv_append", "decode_workspace_bytes", "paged_attn_decode"]

@@ -59,6 +59,29 @@ typedef struct bsa_seq_problem {
   float softmax_scale;  /* finite and > 0 */
 } bsa_seq_problem;
 
+/* Attention over packed sequences: row i of sequence b (Lq queries, Lk keys)
+ * sees keys j < lim,
+ *   causal      lim = min(Lk, max(0, i + 1 + Lk - Lq)): the last query sees
+ *               every key, so queries may be the last part of a longer text
+ *   otherwise   lim = Lk (cross attention, or an encoder when cu_q == cu_k)
+ * and o = sum_j softmax_j(softmax_scale q.k_j) v_j; a row that sees nothing
+ * gives 0.
+ *   q, o        [total_q, heads, head_dim];  k, v [total_k, kv_heads, head_dim];
+ *               the strides of q, k and v must not be 0 (no broadcast views)
+ *   cu_q, cu_k  int32 [n_seqs + 1]
+ *   lse         fp32 [heads, total_q] or NULL: each row's log-sum-exp in the
+ *               exp2 domain, log2 sum_j exp2(softmax_scale log2(e) q.k_j)
+ *               (-inf for a row that sees nothing), for the backward
+ * Scores, statistics and outputs accumulate in fp32; the probabilities are
+ * rounded to the element type for their product with V. */
+bsa_status bsa_packed_attn_fwd(const bsa_seq_problem* prob, int32_t n_seqs, int64_t total_q,
+                               int64_t total_k, const void* q, int64_t q_stride_n,
+                               int64_t q_stride_h, const void* k, int64_t k_stride_n,
+                               int64_t k_stride_h, const void* v, int64_t v_stride_n,
+                               int64_t v_stride_h, const int32_t* cu_q, const int32_t* cu_k,
+                               void* o, int64_t o_stride_n, int64_t o_stride_h, float* lse,
+                               int32_t* dev_status, void* stream);
+
 /* Append new keys and values to a paged cache, rotating keys (and queries)
  * on the way.  Token t of the packed [n_tokens, ...] inputs belongs to the
  * sequence b with cu_new[b] <= t < cu_new[b+1]; its position is

@@ -33,7 +33,7 @@ def attention64(q, k, v, lim, scale):
     seen = torch.arange(k.shape[0], device=q.device)[None] < lim.to(q.device)[:, None]
     z = z.masked_fill(~seen, -math.inf)
     none = ~seen.any(dim=1)
-    m = z.amax(dim=1, keepdim=True) if k.shape[0] else torch.zeros(q.shape[0], 1).double()
+    m = z.amax(dim=1, keepdim=True) if k.shape[0] else z.new_zeros(q.shape[0], 1)
     m = torch.where(torch.isinf(m), torch.zeros_like(m), m)
     e = torch.exp(z - m)
     s = e.sum(dim=1, keepdim=True)

@@ -1,0 +1,204 @@
+"""Attention over packed sequences on the GPU against 64-bit oracles with
+derived bounds."""
+import math
+
+import pytest
+import torch
+
+import block_sparse_attention_47_b200 as bsa
+from seq_helpers import assert_within, attention64, cu_of, limits, output_bound
+
+pytestmark = pytest.mark.gpu
+BF, FP = torch.bfloat16, torch.float16
+
+
+def status_word():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+def inputs(lq, lk, H, K, d, dt, seed=11, gain=2.0, tail=2):
+    """q, k, v as slices of wider tensors; the rows behind the last sequence
+    are NaN."""
+    gen = torch.Generator().manual_seed(seed)
+    wide_q = torch.randn(sum(lq) + tail, H + 1, d, generator=gen) * gain
+    wide_kv = torch.randn(sum(lk) + tail, 2 * K, d, generator=gen)
+    wide_q[sum(lq):], wide_kv[sum(lk):] = math.nan, math.nan
+    wide_q, wide_kv = wide_q.to(dt).cuda(), wide_kv.to(dt).cuda()
+    return wide_q[:, :H], wide_kv[:, :K], wide_kv[:, K:]
+
+
+def check_fwd(q, k, v, lq, lk, causal, out, lse, scale):
+    H, K = q.shape[1], k.shape[1]
+    q0 = k0 = 0
+    for a, b in zip(lq, lk):
+        lim = limits(a, b, causal)
+        for h in range(H):
+            kk, vv = k[k0:k0 + b, h // (H // K)], v[k0:k0 + b, h // (H // K)]
+            o, lse2, p, g = attention64(q[q0:q0 + a, h], kk, vv, lim, scale)
+            what = "%d x %d, head %d" % (a, b, h)
+            assert_within(out[q0:q0 + a, h], o, output_bound(o, p, vv, g, q.dtype), what)
+            if lse is not None and a:
+                got, want = lse[h, q0:q0 + a].double().cpu(), lse2.cpu()
+                none = lim == 0
+                assert bool((got[none] == -math.inf).all())
+                # the scores' error, the exponentials' (4e-6 on a quarter of
+                # them) and a few fp32 roundings of values up to |lse|
+                tol = (g + 4e-6) / math.log(2.0) + 2.0 ** -22 * (1 + want[~none].abs())
+                assert bool(((got - want)[~none].abs() <= tol).all()), what
+        q0, k0 = q0 + a, k0 + b
+
+
+FWD = [
+    # lens_q, lens_k, heads, kv, d, dtype, causal
+    ([1], [1], 1, 1, 64, BF, True),
+    ([1], [1], 2, 1, 128, FP, False),
+    ([37], [37], 2, 2, 64, FP, True),
+    ([127, 128, 129], [127, 128, 129], 4, 2, 128, BF, True),
+    ([255, 256, 257, 1], [255, 256, 257, 1], 3, 1, 64, BF, True),
+    ([0, 300, 0, 5, 0], [0, 300, 7, 5, 0], 6, 2, 128, FP, True),
+    ([64, 511, 3], [640, 700, 130], 8, 1, 64, BF, True),       # the last part of longer texts
+    ([300, 129, 40], [100, 1, 0], 4, 4, 128, BF, True),         # rows that see nothing
+    ([300, 40, 9], [77, 0, 513], 3, 3, 128, FP, False),         # cross attention
+    ([1500], [1500], 2, 1, 128, BF, True),
+    ([1000, 700], [1000, 700], 5, 5, 64, FP, False),
+    ([5] * 70 + [200], [5] * 70 + [200], 4, 4, 64, BF, True),    # more sequences than a warp
+    ([2, 129] * 40, [129, 2] * 40, 2, 1, 128, FP, True),
+]
+
+
+@pytest.mark.parametrize("case", FWD, ids=[str(i) for i in range(len(FWD))])
+def test_fwd(cuda_ok, case):
+    lq, lk, H, K, d, dt, causal = case
+    q, k, v = inputs(lq, lk, H, K, d, dt)
+    prob = bsa.SeqProblem.make(H, K, d, dt, causal=causal)
+    wide = torch.full((q.shape[0], H + 1, d + 8), 5.0, dtype=dt, device="cuda")
+    out, st = wide[:, :H, :d], status_word()
+    lse = torch.full((H, q.shape[0]), 5.0, device="cuda")
+    bsa.packed_attn_fwd(prob, q, k, v, cu_of(lq), cu_of(lk), out, lse, dev_status=st)
+    assert int(st) == 0
+    check_fwd(q, k, v, lq, lk, causal, out, lse, 1 / math.sqrt(d))
+    # what no sequence owns is as it was
+    n = sum(lq)
+    assert bool((wide[n:] == 5.0).all()) and bool((lse[:, n:] == 5.0).all())
+    assert bool((wide[:, H] == 5.0).all()) and bool((wide[:, :, d:] == 5.0).all())
+    again = torch.empty_like(out)
+    bsa.packed_attn_fwd(prob, q, k, v, cu_of(lq), cu_of(lk), again)
+    assert torch.equal(again[:n], out[:n])
+
+
+def test_fwd_large_and_growing_scores(cuda_ok):
+    """Row maxima that grow from key tile to key tile force the rescale."""
+    lens = [900]
+    q, k, v = inputs(lens, lens, 2, 1, 128, BF, gain=8.0)
+    k = k * torch.linspace(0.1, 4.0, k.shape[0], device="cuda", dtype=BF)[:, None, None]
+    prob = bsa.SeqProblem.make(2, 1, 128)
+    out, lse = torch.empty_like(q), torch.empty(2, q.shape[0], device="cuda")
+    bsa.packed_attn_fwd(prob, q, k, v, cu_of(lens), cu_of(lens), out, lse)
+    check_fwd(q, k, v, lens, lens, True, out, lse, 1 / math.sqrt(128))
+
+
+def test_fwd_one_dead_value_stays_where_it_is(cuda_ok):
+    """A NaN in one sequence reaches no other one."""
+    lens = [200, 130, 64]
+    q, k, v = inputs(lens, lens, 2, 2, 64, BF)
+    prob = bsa.SeqProblem.make(2, 2, 64)
+    a, b = torch.empty_like(q), torch.empty_like(q)
+    bsa.packed_attn_fwd(prob, q, k, v, cu_of(lens), cu_of(lens), a)
+    for t in (q, k, v):
+        t[200:330] = math.nan
+    bsa.packed_attn_fwd(prob, q, k, v, cu_of(lens), cu_of(lens), b)
+    for s in (slice(0, 200), slice(330, 394)):
+        assert torch.equal(a[s], b[s])
+    assert bool(b[200:330].isnan().all())
+
+
+def test_fwd_long_sequence_sampled(cuda_ok):
+    """A long walk: sampled rows against the oracle."""
+    n, H, K, d = 20000, 2, 1, 128
+    q, k, v = inputs([n], [n], H, K, d, BF, tail=0)
+    prob = bsa.SeqProblem.make(H, K, d)
+    out, lse = torch.empty_like(q), torch.empty(H, n, device="cuda")
+    bsa.packed_attn_fwd(prob, q, k, v, cu_of([n]), cu_of([n]), out, lse)
+    rows = torch.tensor([0, 1, 127, 128, 9999, 10000, 15487, n - 129, n - 1])
+    for h in range(H):
+        o, lse2, p, g = attention64(q[rows.cuda(), h], k[:, 0], v[:, 0], rows + 1, 1 / math.sqrt(d))
+        assert_within(out[rows.cuda(), h], o, output_bound(o, p, v[:, 0], g, BF))
+        assert bool(((lse[h, rows.cuda()].double() - lse2).abs() <= 2e-3).all())
+
+
+def test_fwd_reports_bad_offsets(cuda_ok):
+    """Offsets that descend or leave the tensor: reported, read as empty; the
+    other sequences are right."""
+    lens = [100, 50, 70]
+    q, k, v = inputs(lens, lens, 4, 2, 64, BF, tail=0)
+    prob = bsa.SeqProblem.make(4, 2, 64)
+    for bad_q, bad_k in (([0, 100, 150, 221], None), ([0, 100, 90, 90], None), (None, [0, 100, 150, 9999]),
+                         ([-5, 100, 150, 220], None)):
+        cq, ck = cu_of(lens), cu_of(lens)
+        if bad_q:
+            cq = torch.tensor(bad_q, dtype=torch.int32, device="cuda")
+        if bad_k:
+            ck = torch.tensor(bad_k, dtype=torch.int32, device="cuda")
+        out, st = torch.full_like(q, 5.0), status_word()
+        bsa.packed_attn_fwd(prob, q, k, v, cq, ck, out, dev_status=st)
+        assert int(st) == 1
+        good = slice(100, 150) if (bad_q or [0, 0, 150])[2] == 150 else slice(0, 100)
+        b = 1 if good.start else 0
+        n = lens[b]
+        check_fwd(q[good], k[good], v[good], [n], [n], True, out[good], None, 1 / 8)
+
+
+def test_fwd_captured_and_replayed(cuda_ok):
+    lens = [130, 257]
+    q, k, v = inputs(lens, lens, 4, 2, 128, FP, tail=0)
+    prob = bsa.SeqProblem.make(4, 2, 128, FP)
+    out, cu = torch.empty_like(q), cu_of(lens)
+    bsa.packed_attn_fwd(prob, q, k, v, cu, cu, out)
+    want = out.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        bsa.packed_attn_fwd(prob, q, k, v, cu, cu, out)
+    out.zero_()
+    g.replay()
+    assert torch.equal(out, want)
+    cu.copy_(torch.tensor([0, 300, 387], dtype=torch.int32))
+    g.replay()
+    check_fwd(q, k, v, [300, 87], [300, 87], True, out, None, 1 / math.sqrt(128))
+
+
+def test_fwd_timeout_path(cuda_ok):
+    """With the products held back the waits run out, the status says so and
+    the next call is right."""
+    lens = [300]
+    q, k, v = inputs(lens, lens, 2, 1, 64, BF, tail=0)
+    prob, st = bsa.SeqProblem.make(2, 1, 64), status_word()
+    out, cu = torch.empty_like(q), cu_of(lens)
+    bsa.debug_stall_pv(True)
+    try:
+        bsa.packed_attn_fwd(prob, q, k, v, cu, cu, out, dev_status=st)
+        torch.cuda.synchronize()
+    finally:
+        bsa.debug_stall_pv(False)
+    assert int(st) == 6
+    bsa.packed_attn_fwd(prob, q, k, v, cu, cu, out)
+    check_fwd(q, k, v, lens, lens, True, out, None, 1 / 8)
+
+
+def test_fwd_binding_refuses(cuda_ok):
+    lens = [40]
+    q, k, v = inputs(lens, lens, 4, 2, 64, BF, tail=0)
+    prob, cu = bsa.SeqProblem.make(4, 2, 64), cu_of(lens)
+    out, lse = torch.empty_like(q), torch.empty(4, 40, device="cuda")
+    ok = [prob, q, k, v, cu, cu, out, lse]
+    for i, bad in [(1, q.float()), (1, q[:, :3]), (2, k.cpu()), (2, k[..., ::2]), (3, v[:39]),
+                   (4, cu.long()), (5, cu[:1]), (6, out.half()), (6, out[:, :2]), (7, lse.double()),
+                   (7, lse[:3])]:
+        a = list(ok)
+        a[i] = bad
+        with pytest.raises(ValueError):
+            bsa.packed_attn_fwd(*a)
+    a = list(ok)
+    a[2] = k[:, :1].expand(40, 2, 64)  # a broadcast view
+    with pytest.raises(bsa.BSAError, match="broadcast"):
+        bsa.packed_attn_fwd(*a)
+    bsa.packed_attn_fwd(*ok)

@@ -107,6 +107,7 @@ def test_decode_refuses(kw, status, word):
 
 
 def test_empty_batches_need_no_device():
+    assert seq._fn("bsa_packed_attn_fwd")(*fwd_args(tq=0)) == 0
     assert seq._fn("bsa_paged_attn_decode")(*decode_args(n_seqs=0)) == 0
     assert seq._fn("bsa_kv_append")(*append_args(n=0)) == 0
 
@@ -139,6 +140,36 @@ APPEND_BAD = [
 @pytest.mark.parametrize("kw,status,word", APPEND_BAD, ids=[str(k) for k, _, _ in APPEND_BAD])
 def test_append_refuses(kw, status, word):
     rc = seq._fn("bsa_kv_append")(*append_args(**kw))
+    assert rc == status, (rc, bsa.lib().bsa_last_error())
+    assert word in bsa.lib().bsa_last_error()
+
+
+def fwd_args(**kw):
+    a = dict(prob=ctypes.byref(prob()), n_seqs=2, tq=100, tk=100, q=16, q_sn=512, q_sh=64, k=16,
+             k_sn=128, k_sh=64, v=16, v_sn=128, v_sh=64, cu_q=16, cu_k=16, o=16, o_sn=512, o_sh=64,
+             lse=None, status=None, stream=None)
+    a.update(kw)
+    return list(a.values())
+
+
+FWD_BAD = [
+    (dict(n_seqs=-1), SHAPE, b"n_seqs"), (dict(tq=-1), SHAPE, b"total_q"),
+    (dict(tk=1 << 31), SHAPE, b"total_k"), (dict(tq=(1 << 31) - 1, n_seqs=1 << 24, prob="wide"), SHAPE, b"pairs"),
+    (dict(q=None), INVALID, b"q is NULL"), (dict(q=18), INVALID, b"aligned"),
+    (dict(q_sn=516), INVALID, b"q strides"), (dict(k_sh=0), INVALID, b"broadcast"),
+    (dict(v_sn=0), INVALID, b"broadcast"), (dict(cu_q=None), INVALID, b"cu_q"),
+    (dict(cu_k=2), INVALID, b"cu_k"), (dict(o=None), INVALID, b"o is NULL"),
+    (dict(o_sn=0), INVALID, b"o is written"), (dict(lse=2), INVALID, b"lse"),
+    (dict(status=1), INVALID, b"dev_status"),
+]
+
+
+@pytest.mark.parametrize("kw,status,word", FWD_BAD, ids=[str(k) for k, _, _ in FWD_BAD])
+def test_packed_fwd_refuses(kw, status, word):
+    kw = dict(kw)
+    if kw.get("prob") == "wide":
+        kw["prob"] = ctypes.byref(prob(heads=4096, kv_heads=2))
+    rc = seq._fn("bsa_packed_attn_fwd")(*fwd_args(**kw))
     assert rc == status, (rc, bsa.lib().bsa_last_error())
     assert word in bsa.lib().bsa_last_error()
 
