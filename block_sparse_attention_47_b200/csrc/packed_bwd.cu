@@ -1,0 +1,994 @@
+// Backward of the packed-sequence attention on sm_100a.  With P recomputed
+// from the forward's row statistics, P = exp2(s scale log2(e) - lse2), and
+// D = rowsum(dO * O):
+//     dP = dO V^T,  dS = P * (dP - D),
+//     dQ = scale dS K,  dK = scale sum_h dS_h^T Q_h,  dV = sum_h P_h^T dO_h,
+// the sums over the query heads h of a kv head.
+//
+// Bound by the tensor cores: 10 d flops per (query head, seen pair), 14 with
+// the scores and dP formed in both kernels.  Two kernels rather than one with
+// atomic dQ sums, so that gradients do not vary from run to run:
+//   dQ     CTA = 128 query rows of a head, walking the key tiles they see.
+//   dK/dV  CTA = 128 keys of a kv head, walking the query tiles that see them
+//          of every head of the group, so shared heads are summed in the
+//          accumulators.
+// Both follow the block-sparse backward's scheme: per step the two score-like
+// products are one N=128 burst each, two row groups of 128 threads take 64
+// of the 128 columns each, and the results return to tensor memory as A
+// operands of the accumulations, which run while the next step is loaded.
+//
+// Preparation: lse2 and D are written per 128-row tile of a sequence (rows
+// behind its end get lse2 = +inf, D = 0, so that P = 0 there), sequence b at
+// row 128 (cu[b] / 128 + b), which keeps tiles apart and 512-byte aligned for
+// bulk copies.
+//
+// Tiles that run into a neighbour's rows: as the B operand of an accumulation
+// (K in dQ; Q and dO in dK/dV) their foreign rows are zeroed in shared
+// memory, since 0 times a NaN would reach the sums; as rows of the CTA's own
+// tile they only reach results that are not stored.
+//
+// fp16.  P and dS enter the accumulations as 16-bit values.  P <= 1 is scaled
+// by 2^13.  dS is scaled by the power of two that puts its largest possible
+// value, 2 max_i |dO_i| max_j |V_j| (2-norms over the rows of a kv head), at
+// 2^15, so that it neither overflows nor sinks below fp16's range whatever
+// the scale of the loss.  bf16 needs neither.
+#include "seq_internal.cuh"
+
+namespace bsa {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kPShift = 13.f;
+
+#define BSA_TMEM_ST16(taddr, r)                                                               \
+  asm volatile(                                                                               \
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "                                        \
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n\t"                         \
+      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),                                          \
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), \
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),       \
+      "r"(r[15])                                                                              \
+      : "memory")
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// rows of the padded statistics, and where sequence b's begin
+__host__ __device__ inline int64_t stat_rows(int64_t total_q, int64_t n_seqs) {
+  return 128 * (total_q / 128 + n_seqs + 1);
+}
+__device__ __forceinline__ int64_t stat_start(int cu, int b) {
+  return 128 * (int64_t(cu >> 7) + b);
+}
+
+// the power of two of dS for one kv head (fp16), from the largest squared norms
+__device__ __forceinline__ float ds_factor(const float* __restrict__ norms, int kvh, int kv_heads) {
+  const float bound = 2.f * sqrtf(__ldg(norms + kvh)) * sqrtf(__ldg(norms + kv_heads + kvh));
+  if (!(bound > 0.f) || isinf(bound)) return 1.f;
+  return exp2f(fminf(fmaxf(floorf(15.f - log2f(bound)), -60.f), 60.f));
+}
+
+// zero the rows from r0 on of a 128-row tile of KB boxes (a whole warp)
+__device__ __forceinline__ void zero_rows(uint32_t tile, int boxes, int r0, int lane) {
+  for (int bx = 0; bx < boxes; ++bx)
+    for (int o = r0 * 128 + lane * 16; o < 128 * 128; o += 512)
+      st_shared_v4(tile + bx * 128 * 128 + o, make_uint4(0u, 0u, 0u, 0u));
+}
+
+// one 32-column chunk of an accumulator row, scaled, to 64 bytes of a gradient row
+template <typename T>
+__device__ __forceinline__ void store_chunk(T* dst, const uint32_t (&a)[32], float f, bool live) {
+  uint4* d4 = reinterpret_cast<uint4*>(dst);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      w[x] = live ? pack2<T>(__uint_as_float(a[8 * i + 2 * x]) * f,
+                             __uint_as_float(a[8 * i + 2 * x + 1]) * f)
+                  : 0u;
+    d4[i] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// ============================================================================
+// D = rowsum(dO * O), the statistics' layout, and the norms for fp16
+// ============================================================================
+template <typename T, int D>
+__global__ void __launch_bounds__(256) bwd_prepare_kernel(SeqGeo g, const PackedBwdIO io) {
+  constexpr int TPR = D / 8;  // threads per row, 16 bytes each
+  __shared__ int where[3];    // any, sequence, tile
+  __shared__ float top[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (warp == 0) {
+    int b = 0, t = 0;
+    const bool any = find_tile(io.cu_q, io.n_seqs, io.total_q, 128, blockIdx.x, lane, io.status, b, t);
+    if (lane == 0) where[0] = any, where[1] = b, where[2] = t;
+  }
+  __syncthreads();
+  if (!where[0]) return;
+  const int b = where[1], t = where[2], head = blockIdx.y;
+  const Span q = span_of(io.cu_q, b, io.total_q, io.status);
+  const int64_t stats = stat_rows(io.total_q, io.n_seqs);
+  const int64_t out0 = int64_t(head) * stats + stat_start(q.start, b) + int64_t(t) * 128;
+  float most = 0.f;
+#pragma unroll 4
+  for (int r = threadIdx.x / TPR; r < 128; r += 256 / TPR) {
+    const int row = t * 128 + r;
+    float acc = 0.f, sq = 0.f;
+    if (row < q.len) {
+      const int64_t at = q.start + row;
+      const int c = (threadIdx.x % TPR) * 8;
+      const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const T*>(io.o.p) + at * io.o.sn +
+                                                      int64_t(head) * io.o.sh + c);
+      const uint4 z = *reinterpret_cast<const uint4*>(static_cast<const T*>(io.dout.p) +
+                                                      at * io.dout.sn + int64_t(head) * io.dout.sh + c);
+      const uint32_t av[4] = {a.x, a.y, a.z, a.w}, zv[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 x = unpack2<T>(av[i]), y = unpack2<T>(zv[i]);
+        acc = fmaf(x.x, y.x, acc);
+        acc = fmaf(x.y, y.y, acc);
+        sq = fmaf(y.x, y.x, sq);
+        sq = fmaf(y.y, y.y, sq);
+      }
+    }
+#pragma unroll
+    for (int o = TPR / 2; o > 0; o >>= 1) {
+      acc += __shfl_xor_sync(0xffffffffu, acc, o);
+      sq += __shfl_xor_sync(0xffffffffu, sq, o);
+    }
+    most = fmaxf(most, sq);
+    if (threadIdx.x % TPR == 0) {
+      float lse = INFINITY;
+      if (row < q.len) {
+        lse = __ldg(io.lse + int64_t(head) * io.total_q + q.start + row);
+        if (lse == -INFINITY) lse = INFINITY;  // the row saw nothing: P = 0
+      }
+      io.stat_lse[out0 + r] = lse;
+      io.stat_delta[out0 + r] = row < q.len ? acc : 0.f;
+    }
+  }
+  if constexpr (std::is_same<T, __half>::value) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if (lane == 0) top[warp] = most;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int w = 1; w < 8; ++w) most = fmaxf(most, top[w]);
+      // non-negative floats order as their bits; a maximum has no order of arrival
+      atomicMax(reinterpret_cast<int*>(io.norms) + head / g.group, __float_as_int(most));
+    }
+  }
+}
+
+// largest squared norm of a V row per kv head (fp16)
+template <int D>
+__global__ void __launch_bounds__(256) bwd_vnorm_kernel(SeqGeo g, const PackedBwdIO io) {
+  constexpr int TPR = D / 8;
+  const int lane = threadIdx.x & 31, kvh = blockIdx.y;
+  // rows that a sequence owns, taking the offsets' ends (gaps do not occur)
+  const int64_t lo = max(0, __ldg(io.cu_k)), hi = min(int64_t(__ldg(io.cu_k + io.n_seqs)), io.total_k);
+  float most = 0.f;
+  const int64_t step = int64_t(gridDim.x) * (256 / TPR);
+  const int64_t first = lo + int64_t(blockIdx.x) * (256 / TPR);
+  for (int64_t r0 = first; r0 < hi; r0 += step) {
+    const int64_t r = r0 + threadIdx.x / TPR;
+    float sq = 0.f;
+    if (r < hi) {
+      const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const __half*>(io.v.p) + r * io.v.sn +
+                                                      int64_t(kvh) * io.v.sh + (threadIdx.x % TPR) * 8);
+      const uint32_t av[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 x = unpack2<__half>(av[i]);
+        sq = fmaf(x.x, x.x, sq);
+        sq = fmaf(x.y, x.y, sq);
+      }
+    }
+#pragma unroll
+    for (int o = TPR / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+    most = fmaxf(most, sq);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  if (lane == 0)
+    atomicMax(reinterpret_cast<int*>(io.norms) + g.kv_heads + kvh, __float_as_int(most));
+}
+
+// ============================================================================
+// dQ: CTA = 128 query rows of a head
+// ============================================================================
+template <int D>
+struct DqCfg {
+  // warps 0-3 / 4-7: row groups 0 / 1 (64 key columns of a step each);
+  // 8: S/dP issuer; 9: finds the tile, copies, the K tail; 10: accumulations
+  static constexpr int kThreads = 352;
+  static constexpr int KB = D / 64;
+  static constexpr int NK = 3, NV = 2;       // K / V ring slots
+  static constexpr int BOX = 128 * 128;
+  static constexpr int TILE = KB * BOX;      // 128 rows
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = TILE;
+  static constexpr int OFF_V = OFF_K + NK * TILE;
+  static constexpr int OFF_BAR = OFF_V + NV * TILE;
+  // kfull[NK] kempty[NK] vfull[NV] vempty[NV] sd_ready read x_ready[2]
+  // x_free own q fix_go fixed done drain[2]
+  static constexpr int N_BARS = 2 * NK + 2 * NV + 12;
+  static constexpr int OFF_MISC = OFF_BAR + 8 * N_BARS;
+  static constexpr int SMEM = OFF_MISC + 64 + 1024;
+  static constexpr uint32_t TMEM_COLS = 512;
+  // dO (A of dP) at 0, S at 64 (group w's half at 64 + 64 w), dP at 192, dS
+  // at 320 (32 packed columns per group), dQ at 384
+  static constexpr uint32_t COL_DO = 0, COL_S = 64, COL_DP = 192, COL_DS = 320, COL_ACC = 384;
+  static_assert(SMEM <= 227 * 1024, "shared memory budget");
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(352, 1)
+    packed_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                     const __grid_constant__ CUtensorMap mv, SeqGeo g, const PackedBwdIO io) {
+  using C = DqCfg<D>;
+  constexpr bool kHalf = std::is_same<T, __half>::value;
+  constexpr int NK = C::NK, NV = C::NV;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  unsigned char* sm = smem_raw + (base - raw);
+  const uint32_t sQ = base + C::OFF_Q;
+  const uint32_t kfull = base + C::OFF_BAR, kempty = kfull + 8 * NK;
+  const uint32_t vfull = kempty + 8 * NK, vempty = vfull + 8 * NV;
+  const uint32_t sd_ready = vempty + 8 * NV, read = sd_ready + 8, x_ready = read + 8;
+  const uint32_t x_free = x_ready + 16, own = x_free + 8, bar_q = own + 8;
+  const uint32_t fix_go = bar_q + 8, fixed = fix_go + 8, done = fixed + 8, drain = done + 8;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 4);
+  int* found = reinterpret_cast<int*>(sm + C::OFF_MISC + 8);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int head = int(blockIdx.x % uint32_t(g.heads)), kvh = head / g.group;
+  auto kslot = [&](int p) { return base + C::OFF_K + (p % NK) * C::TILE; };
+  auto vslot = [&](int p) { return base + C::OFF_V + (p % NV) * C::TILE; };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NK; ++s) {
+      mbar_init(kfull + 8 * s, 1);
+      mbar_init(kempty + 8 * s, 1);
+    }
+    for (int s = 0; s < NV; ++s) {
+      mbar_init(vfull + 8 * s, 1);
+      mbar_init(vempty + 8 * s, 1);
+    }
+    mbar_init(sd_ready, 1);
+    mbar_init(read, 8);
+    mbar_init(x_ready, 4);
+    mbar_init(x_ready + 8, 4);
+    mbar_init(x_free, 1);
+    mbar_init(own, 4);
+    mbar_init(bar_q, 1);
+    mbar_init(fix_go, 1);
+    mbar_init(fixed, 1);
+    mbar_init(done, 2);
+    mbar_init(drain, 1);
+    mbar_init(drain + 8, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_u32(tmem_holder), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  if (warp == 9) {
+    int b = 0, t = 0;
+    const bool any = find_tile(io.cu_q, io.n_seqs, io.total_q, 128, blockIdx.x / uint32_t(g.heads),
+                               lane, io.status, b, t);
+    if (lane == 0) {
+      found[0] = any;
+      if (any) {
+        const Span q = span_of(io.cu_q, b, io.total_q, io.status);
+        const Span k = span_of(io.cu_k, b, io.total_k, io.status);
+        found[1] = q.start, found[2] = q.len, found[3] = k.start, found[4] = k.len;
+        found[5] = t, found[6] = b;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const bool any = found[0] != 0;
+  const int q0 = found[1], Lq = found[2], k0 = found[3], Lk = found[4];
+  const int first = any ? found[5] * 128 : 0, seq = found[6];
+  int np = 0;  // key tiles that the tile's last row sees
+  if (any) {
+    const int last = min(first + 128, Lq) - 1;
+    np = ((g.causal ? min(Lk, max(0, last + 1 + Lk - Lq)) : Lk) + 127) >> 7;
+  }
+  const bool has_tail = np > 0 && np * 128 > Lk;
+
+  if (warp == 9) {
+    // ---- the copies: Q, then K and V tiles into their rings
+    if (lane == 0 && np > 0) {
+      tma_prefetch_desc(&mk);
+      tma_prefetch_desc(&mv);
+      mbar_arrive_expect_tx(bar_q, C::TILE);
+      for (int bx = 0; bx < C::KB; ++bx)
+        tma_load_3d(sQ + bx * C::BOX, &mq, bar_q, 64 * bx, head, q0 + first);
+      bool ok = true;
+      int kl = 0, vl = 0;  // tiles whose K / V copies have been issued
+      for (int p = 0; p < np; ++p) {
+        if (p >= NK && !mbar_wait(kempty + 8 * (p % NK), ((p - NK) / NK) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        mbar_arrive_expect_tx(kfull + 8 * (p % NK), C::TILE);
+        for (int bx = 0; bx < C::KB; ++bx)
+          tma_load_3d(kslot(p) + bx * C::BOX, &mk, kfull + 8 * (p % NK), 64 * bx, kvh,
+                      k0 + p * 128);
+        kl = p + 1;
+        if (p >= NV && !mbar_wait(vempty + 8 * (p % NV), ((p - NV) / NV) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        mbar_arrive_expect_tx(vfull + 8 * (p % NV), C::TILE);
+        for (int bx = 0; bx < C::KB; ++bx)
+          tma_load_3d(vslot(p) + bx * C::BOX, &mv, vfull + 8 * (p % NV), 64 * bx, kvh,
+                      k0 + p * 128);
+        vl = p + 1;
+      }
+      if (!ok) report_timeout(abort_flag, io.status);
+      if (!ok || *abort_flag) {
+        // the newest copies may still be landing
+        mbar_wait(bar_q, 0, nullptr, 200000000ull);
+        for (int p = kl > NK ? kl - NK : 0; p < kl; ++p)
+          mbar_wait(kfull + 8 * (p % NK), (p / NK) & 1, nullptr, 200000000ull);
+        for (int p = vl > NV ? vl - NV : 0; p < vl; ++p)
+          mbar_wait(vfull + 8 * (p % NV), (p / NV) & 1, nullptr, 200000000ull);
+      }
+    }
+    __syncwarp();
+    // ---- the last tile's foreign K rows, once it has landed
+    if (has_tail) {
+      if (__all_sync(0xffffffffu, mbar_wait(fix_go, 0, abort_flag))) {
+        zero_rows(kslot(np - 1), C::KB, Lk - (np - 1) * 128, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(fixed);
+      } else if (lane == 0) {
+        report_timeout(abort_flag, io.status);
+      }
+    }
+  } else if (warp == 8) {
+    // ---- S and dP of each step, once its tiles are in and both groups have
+    // read the previous step's
+    if (lane == 0 && np > 0) {
+      constexpr uint32_t idesc_s = idesc_f32<T>(128, 128, false);
+      bool ok = mbar_wait(own, 0, abort_flag) && mbar_wait(bar_q, 0, abort_flag);
+      for (int p = 0; ok && p < np; ++p) {
+        if (!mbar_wait(kfull + 8 * (p % NK), (p / NK) & 1, abort_flag) ||
+            !mbar_wait(vfull + 8 * (p % NV), (p / NV) & 1, abort_flag) ||
+            (p > 0 && !mbar_wait(read, (p - 1) & 1, abort_flag))) {
+          ok = false;
+          break;
+        }
+        if (has_tail && p == np - 1) {
+          mbar_arrive(fix_go);
+          if (!mbar_wait(fixed, 0, abort_flag)) {
+            ok = false;
+            break;
+          }
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk / 4) * C::BOX + (kk % 4) * 32;
+          tc_mma_ss(tmem + C::COL_S, sdesc_sw128(sQ + off, 16, 1024),
+                    sdesc_sw128(kslot(p) + off, 16, 1024), idesc_s, kk > 0);
+          tc_mma_ts(tmem + C::COL_DP, tmem + C::COL_DO + 8u * kk,
+                    sdesc_sw128(vslot(p) + off, 16, 1024), idesc_s, kk > 0);
+        }
+        tc_commit(sd_ready);
+        tc_commit(vempty + 8 * (p % NV));
+      }
+      if (!ok) report_timeout(abort_flag, io.status);
+      tc_commit(done);
+      tc_commit(drain);
+      mbar_wait(drain, 0, nullptr, 200000000ull);
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    // ---- dQ += dS_w K_w as each group's dS is in; B = its 64 K rows, N-major
+    if (lane == 0 && np > 0) {
+      constexpr uint32_t idesc_acc = idesc_f32<T>(128, D, true);
+      bool ok = true;
+      // test hook: with `stall` set no accumulation is issued (the timeout path)
+      for (int p = 0; ok && p < np && !io.stall; ++p) {
+        for (int h = 0; h < 2; ++h) {
+          if (!mbar_wait(x_ready + 8 * h, p & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_ts(tmem + C::COL_ACC, tmem + C::COL_DS + 32u * h + 8u * kk,
+                      sdesc_sw128(kslot(p) + h * 8192 + kk * 2048, C::BOX, 1024), idesc_acc,
+                      (p > 0 || h > 0 || kk > 0) ? 1u : 0u);
+        }
+        if (!ok) break;
+        tc_commit(x_free);
+        tc_commit(kempty + 8 * (p % NK));
+      }
+      if (!ok) report_timeout(abort_flag, io.status);
+      tc_commit(done);
+      tc_commit(drain + 8);
+      mbar_wait(drain + 8, 0, nullptr, 200000000ull);
+    }
+    __syncwarp();
+  } else {
+    // ---- row groups: group grp takes key columns 64 grp .. of every step;
+    // thread r of a group owns query row r = TMEM lane r
+    const int grp = warp >> 2, quad = warp & 3;
+    const int row = quad * 32 + lane, r = first + row;
+    const uint32_t lane_base = uint32_t(quad * 32) << 16;
+    const bool exists = any && r < Lq;
+    const int lim = !exists ? 0 : (g.causal ? min(Lk, max(0, r + 1 + Lk - Lq)) : Lk);
+    if (grp == 1 && np > 0) {
+      // dO rows into tensor memory: the A operand of dP
+      const T* src = static_cast<const T*>(io.dout.p) + int64_t(q0 + r) * io.dout.sn +
+                     int64_t(head) * io.dout.sh;
+      uint32_t rw[D / 2];
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 u = exists ? __ldg(reinterpret_cast<const uint4*>(src) + i)
+                               : make_uint4(0u, 0u, 0u, 0u);
+        rw[4 * i] = u.x;
+        rw[4 * i + 1] = u.y;
+        rw[4 * i + 2] = u.z;
+        rw[4 * i + 3] = u.w;
+      }
+      if constexpr (D == 128) {
+        BSA_TMEM_ST64(tmem + C::COL_DO + lane_base, rw);
+      } else {
+        BSA_TMEM_ST32(tmem + C::COL_DO + lane_base, rw);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(own);
+    }
+    float lse2 = INFINITY, dlt = 0.f, fac = 1.f;
+    if (exists && np > 0) {
+      const int64_t at = int64_t(head) * stat_rows(io.total_q, io.n_seqs) + stat_start(q0, seq) + r;
+      lse2 = __ldg(io.stat_lse + at);
+      dlt = __ldg(io.stat_delta + at);
+      if constexpr (kHalf) fac = ds_factor(io.norms, kvh, g.kv_heads);
+    }
+    const float dlt_f = dlt * fac;
+    const float sl2 = g.scale * kLog2e;
+    const uint32_t tS = tmem + C::COL_S + 64u * grp + lane_base;
+    const uint32_t tDP = tmem + C::COL_DP + 64u * grp + lane_base;
+    const uint32_t tDS = tmem + C::COL_DS + 32u * grp + lane_base;
+    bool ok = true;
+    for (int p = 0; p < np; ++p) {
+      ok = __all_sync(0xffffffffu, mbar_wait(sd_ready, p & 1, abort_flag));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t sv[64], dp[64];
+      BSA_TMEM_LD64(tS, sv);
+      BSA_TMEM_LD64(tDP, dp);
+      // S and dP read: the issuer may start the next step's
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(read);
+      const int seen = lim - 128 * p - 64 * grp;
+      uint32_t pk[32];
+      if (__all_sync(0xffffffffu, !exists || seen >= 64)) {
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          float x0, x1, t0, t1, d0, d1;
+          fma_f32x2(x0, x1, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]), sl2, sl2, -lse2,
+                    -lse2);
+          const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+          if constexpr (kHalf)
+            fma_f32x2(t0, t1, __uint_as_float(dp[c]), __uint_as_float(dp[c + 1]), fac, fac, -dlt_f,
+                      -dlt_f);
+          else
+            add_f32x2(t0, t1, __uint_as_float(dp[c]), __uint_as_float(dp[c + 1]), -dlt, -dlt);
+          fma_f32x2(d0, d1, p0, p1, t0, t1, 0.f, 0.f);
+          pk[c / 2] = pack2<T>(d0, d1);
+        }
+      } else {
+        // masked scores and dP may be anything: both are selected away
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          const float p0 = ex2_approx(fmaf(__uint_as_float(sv[c]), sl2, -lse2));
+          const float p1 = ex2_approx(fmaf(__uint_as_float(sv[c + 1]), sl2, -lse2));
+          const float t0 = fmaf(__uint_as_float(dp[c]), fac, -dlt_f);
+          const float t1 = fmaf(__uint_as_float(dp[c + 1]), fac, -dlt_f);
+          pk[c / 2] = pack2<T>(c < seen ? p0 * t0 : 0.f, c + 1 < seen ? p1 * t1 : 0.f);
+        }
+      }
+      // the group's columns are free once the previous accumulation has read them
+      if (p > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(x_free, (p - 1) & 1, abort_flag));
+        if (!ok) break;
+      }
+      tc_fence_after();
+      BSA_TMEM_ST32(tDS, pk);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(x_ready + 8 * grp);
+    }
+    if (ok && np > 0) ok = __all_sync(0xffffffffu, mbar_wait(done, 0, abort_flag));
+    if (!ok) {
+      if (lane == 0) report_timeout(abort_flag, io.status);
+    } else {
+      // group grp writes channels grp * D/2 ..; no step: the gradient is 0
+      tc_fence_after();
+      T* dst = static_cast<T*>(io.dq.p) + int64_t(q0 + r) * io.dq.sn + int64_t(head) * io.dq.sh;
+      const float f = g.scale / fac;
+#pragma unroll 1
+      for (int ch = grp * (D / 64); ch < (grp + 1) * (D / 64); ++ch) {
+        uint32_t a[32];
+        BSA_TMEM_LD32(tmem + C::COL_ACC + 32u * ch + lane_base, a);
+        if (exists) store_chunk<T>(dst + 32 * ch, a, f, np > 0);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// ============================================================================
+// dK, dV: CTA = 128 keys of a kv head
+// ============================================================================
+template <int D>
+struct DkdvCfg {
+  // warps 0-3 / 4-7: row groups 0 / 1 (64 query columns of a step each);
+  // 8: S^T/dP^T issuer and copies; 9: finds the tile, the Q/dO tails; 10:
+  // accumulations
+  static constexpr int kThreads = 352;
+  static constexpr int KB = D / 64;
+  static constexpr int NR = 2;                 // Q/dO ring slots
+  static constexpr int BOX = 128 * 128;
+  static constexpr int TILE = KB * BOX;
+  static constexpr int OFF_K = 0, OFF_V = TILE;
+  static constexpr int OFF_STG = 2 * TILE;     // [slot][Q | dO]
+  static constexpr int OFF_VEC = OFF_STG + NR * 2 * TILE;  // [slot][lse2 128 | D 128] fp32
+  static constexpr int OFF_BAR = OFF_VEC + NR * 1024;
+  // full[NR] s_ready dp_ready st_issued p_ready[2] ds_ready[2] xv_free
+  // xk_free own fix_go fixed done drain[2]
+  static constexpr int N_BARS = NR + 15;
+  static constexpr int OFF_MISC = OFF_BAR + 8 * N_BARS;
+  static constexpr int SMEM = OFF_MISC + 64 + 1024;
+  static constexpr uint32_t TMEM_COLS = 512;
+  // S^T at 0 (group w's half at 64 w, P^T over it), dP^T at 128 (dS^T over
+  // it), dV at 256, dK at 256 + D
+  static constexpr uint32_t COL_ST = 0, COL_DPT = 128, COL_DV = 256, COL_DK = 256 + D;
+  static_assert(SMEM <= 227 * 1024, "shared memory budget");
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(352, 1)
+    packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq,
+                       const __grid_constant__ CUtensorMap mk,
+                       const __grid_constant__ CUtensorMap mv,
+                       const __grid_constant__ CUtensorMap mdo, SeqGeo g, const PackedBwdIO io) {
+  using C = DkdvCfg<D>;
+  constexpr bool kHalf = std::is_same<T, __half>::value;
+  constexpr int NR = C::NR;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  unsigned char* sm = smem_raw + (base - raw);
+  const uint32_t sK = base + C::OFF_K, sV = base + C::OFF_V;
+  const uint32_t full = base + C::OFF_BAR, s_ready = full + 8 * NR, dp_ready = s_ready + 8;
+  const uint32_t st_issued = dp_ready + 8, p_ready = st_issued + 8, ds_ready = p_ready + 16;
+  const uint32_t xv_free = ds_ready + 16, xk_free = xv_free + 8, own = xk_free + 8;
+  const uint32_t fix_go = own + 8, fixed = fix_go + 8, done = fixed + 8, drain = done + 8;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 4);
+  int* found = reinterpret_cast<int*>(sm + C::OFF_MISC + 8);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kvh = int(blockIdx.x % uint32_t(g.kv_heads));
+  auto qslot = [&](int p) { return base + C::OFF_STG + (p % NR) * 2 * C::TILE; };
+  auto doslot = [&](int p) { return qslot(p) + C::TILE; };
+  auto vecslot = [&](int p) { return base + C::OFF_VEC + (p % NR) * 1024; };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NR; ++s) mbar_init(full + 8 * s, 1);
+    mbar_init(s_ready, 1);
+    mbar_init(dp_ready, 1);
+    mbar_init(st_issued, 1);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(p_ready + 8 * w, 4);
+      mbar_init(ds_ready + 8 * w, 4);
+    }
+    mbar_init(xv_free, 1);
+    mbar_init(xk_free, 1);
+    mbar_init(own, 1);
+    mbar_init(fix_go, 1);
+    mbar_init(fixed, 1);
+    mbar_init(done, 2);
+    mbar_init(drain, 1);
+    mbar_init(drain + 8, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_u32(tmem_holder), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  if (warp == 9) {
+    int b = 0, t = 0;
+    const bool any = find_tile(io.cu_k, io.n_seqs, io.total_k, 128,
+                               blockIdx.x / uint32_t(g.kv_heads), lane, io.status, b, t);
+    if (lane == 0) {
+      found[0] = any;
+      if (any) {
+        const Span q = span_of(io.cu_q, b, io.total_q, io.status);
+        const Span k = span_of(io.cu_k, b, io.total_k, io.status);
+        found[1] = q.start, found[2] = q.len, found[3] = k.start, found[4] = k.len;
+        // in causal order a sequence's first keys are seen by the most
+        // queries: the longest walks first
+        found[5] = g.causal ? (k.len + 127) / 128 - 1 - t : t;
+        found[6] = b;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const bool any = found[0] != 0;
+  const int q0 = found[1], Lq = found[2], k0 = found[3], Lk = found[4];
+  const int first = any ? found[5] * 128 : 0, seq = found[6];
+  // query tiles qt0 .. n_qt-1 of each of the group's heads, head after head
+  int qt0 = 0, per = 0;
+  if (any && Lq > 0) {
+    if (g.causal) qt0 = max(0, first + Lq - Lk) >> 7;
+    per = ((Lq + 127) >> 7) - qt0;
+  }
+  const int np = per * g.group;
+  const bool has_tail = np > 0 && (Lq & 127) != 0;  // every per-th step's tile is partial
+
+  if (warp == 9) {
+    // ---- the foreign rows of the heads' last Q and dO tiles
+    if (has_tail) {
+      for (int h = 0; h < g.group; ++h) {
+        const int p = (h + 1) * per - 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(fix_go, h & 1, abort_flag,
+                                               2000000000ull + uint64_t(np) * 10000ull))) {
+          if (lane == 0) report_timeout(abort_flag, io.status);
+          break;
+        }
+        zero_rows(qslot(p), C::KB, Lq & 127, lane);
+        zero_rows(doslot(p), C::KB, Lq & 127, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(fixed);
+      }
+    }
+  } else if (warp == 8) {
+    // ---- S^T and dP^T of each step, and the copies
+    if (lane == 0 && np > 0) {
+      constexpr uint32_t idesc_s = idesc_f32<T>(128, 128, false);
+      tma_prefetch_desc(&mq);
+      tma_prefetch_desc(&mdo);
+      mbar_arrive_expect_tx(own, 2 * C::TILE);
+      for (int bx = 0; bx < C::KB; ++bx) {
+        tma_load_3d(sK + bx * C::BOX, &mk, own, 64 * bx, kvh, k0 + first);
+        tma_load_3d(sV + bx * C::BOX, &mv, own, 64 * bx, kvh, k0 + first);
+      }
+      const int64_t stats = stat_rows(io.total_q, io.n_seqs), at0 = stat_start(q0, seq);
+      // Q and dO tiles of step p with their rows' lse2 and D
+      int lh = kvh * g.group, lt = qt0;  // head and query tile of the next load
+      auto load = [&](int p) {
+        const uint32_t bar = full + 8 * (p % NR);
+        mbar_arrive_expect_tx(bar, 2 * C::TILE + 1024);
+        for (int bx = 0; bx < C::KB; ++bx) {
+          tma_load_3d(qslot(p) + bx * C::BOX, &mq, bar, 64 * bx, lh, q0 + lt * 128);
+          tma_load_3d(doslot(p) + bx * C::BOX, &mdo, bar, 64 * bx, lh, q0 + lt * 128);
+        }
+        const int64_t at = lh * stats + at0 + lt * 128;
+        bulk_load(vecslot(p), io.stat_lse + at, 512, bar);
+        bulk_load(vecslot(p) + 512, io.stat_delta + at, 512, bar);
+        if (++lt == qt0 + per) {
+          lt = qt0;
+          ++lh;
+        }
+      };
+      int loaded = 0, in_head = 0, tails = 0;
+      for (; loaded < np && loaded < NR; ++loaded) load(loaded);
+      bool ok = mbar_wait(own, 0, abort_flag);
+      for (int p = 0; ok && p < np; ++p) {
+        // S^T of step p once dV has read P^T of step p-1 from its columns
+        if (!mbar_wait(full + 8 * (p % NR), (p / NR) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (++in_head == per) {
+          in_head = 0;
+          if (has_tail) {
+            mbar_arrive(fix_go);
+            if (!mbar_wait(fixed, tails & 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            ++tails;
+          }
+        }
+        if (p > 0 && !mbar_wait(xv_free, (p - 1) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk / 4) * C::BOX + (kk % 4) * 32;
+          tc_mma_ss(tmem + C::COL_ST, sdesc_sw128(sK + off, 16, 1024),
+                    sdesc_sw128(qslot(p) + off, 16, 1024), idesc_s, kk > 0);
+        }
+        tc_commit(s_ready);
+        mbar_arrive(st_issued);
+        // dP^T once dK has read dS^T of step p-1; step p+1 goes into the slot
+        // of step p-1 as soon as both its accumulations have finished
+        if (p > 0 && !mbar_wait(xk_free, (p - 1) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (p >= 1 && p + 1 < np) {
+          load(p + 1);
+          loaded = p + 2;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk / 4) * C::BOX + (kk % 4) * 32;
+          tc_mma_ss(tmem + C::COL_DPT, sdesc_sw128(sV + off, 16, 1024),
+                    sdesc_sw128(doslot(p) + off, 16, 1024), idesc_s, kk > 0);
+        }
+        tc_commit(dp_ready);
+      }
+      if (!ok) {
+        report_timeout(abort_flag, io.status);
+        // the newest copies may still be landing
+        mbar_wait(own, 0, nullptr, 200000000ull);
+        for (int pp = loaded > NR ? loaded - NR : 0; pp < loaded; ++pp)
+          mbar_wait(full + 8 * (pp % NR), (pp / NR) & 1, nullptr, 200000000ull);
+      }
+      tc_commit(done);
+      tc_commit(drain);
+      mbar_wait(drain, 0, nullptr, 200000000ull);
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    // ---- dV += P^T_w dO_w as each group's P^T is in, then (after the next
+    // step's S^T, so that the groups' next P^T is not held up) dK += dS^T_w
+    // Q_w; B read N-major
+    if (lane == 0 && np > 0) {
+      constexpr uint32_t idesc_acc = idesc_f32<T>(128, D, true);
+      bool ok = true;
+      // test hook: with `stall` set no accumulation is issued (the timeout path)
+      for (int p = 0; ok && p < np && !io.stall; ++p) {
+        for (int h = 0; h < 2; ++h) {
+          if (!mbar_wait(p_ready + 8 * h, p & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_ts(tmem + C::COL_DV, tmem + C::COL_ST + 64u * h + 8u * kk,
+                      sdesc_sw128(doslot(p) + h * 8192 + kk * 2048, C::BOX, 1024), idesc_acc,
+                      (p > 0 || h > 0 || kk > 0) ? 1u : 0u);
+        }
+        if (!ok) break;
+        tc_commit(xv_free);
+        if (p + 1 < np && !mbar_wait(st_issued, (p + 1) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        for (int h = 0; h < 2; ++h) {
+          if (!mbar_wait(ds_ready + 8 * h, p & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_ts(tmem + C::COL_DK, tmem + C::COL_DPT + 64u * h + 8u * kk,
+                      sdesc_sw128(qslot(p) + h * 8192 + kk * 2048, C::BOX, 1024), idesc_acc,
+                      (p > 0 || h > 0 || kk > 0) ? 1u : 0u);
+        }
+        if (!ok) break;
+        tc_commit(xk_free);
+      }
+      if (!ok) report_timeout(abort_flag, io.status);
+      tc_commit(done);
+      tc_commit(drain + 8);
+      mbar_wait(drain + 8, 0, nullptr, 200000000ull);
+    }
+    __syncwarp();
+  } else {
+    // ---- row groups: key row r of the tile = TMEM lane r
+    const int grp = warp >> 2, quad = warp & 3;
+    const int row = quad * 32 + lane, kr = first + row;
+    const uint32_t lane_base = uint32_t(quad * 32) << 16;
+    const bool exists = any && kr < Lk;
+    const float sl2 = g.scale * kLog2e;
+    const float fac = kHalf && np > 0 ? ds_factor(io.norms, kvh, g.kv_heads) : 1.f;
+    const float fac_p = kHalf ? fac * exp2f(-kPShift) : 1.f;
+    const float shift = kHalf ? kPShift : 0.f;
+    const uint32_t tS = tmem + C::COL_ST + 64u * grp + lane_base;
+    const uint32_t tDP = tmem + C::COL_DPT + 64u * grp + lane_base;
+    bool ok = true;
+    int qt = qt0;
+    for (int p = 0; p < np; ++p) {
+      ok = __all_sync(0xffffffffu, mbar_wait(s_ready, p & 1, abort_flag));
+      if (!ok) break;
+      tc_fence_after();
+      // query columns from `from` on see this key (rows behind Lq have P = 0)
+      const int from = g.causal ? kr + Lq - Lk - 128 * qt - 64 * grp : 0;
+      if (++qt == qt0 + per) qt = qt0;
+      const bool dense = __all_sync(0xffffffffu, !exists || from <= 0);
+      uint32_t sv[64], dp[64];
+      BSA_TMEM_LD64(tS, sv);
+      const float* lse = reinterpret_cast<const float*>(sm + C::OFF_VEC + (p % NR) * 1024) + 64 * grp;
+      const float* dlt = lse + 128;
+      // P^T over S^T first, so that dV starts while dS^T is computed; the
+      // probabilities stay in sv.  32 query columns at a time.
+#pragma unroll
+      for (int h2 = 0; h2 < 2; ++h2) {
+        uint32_t pk[16];
+        float4 l4[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) l4[i] = reinterpret_cast<const float4*>(lse)[8 * h2 + i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int c = 32 * h2 + 4 * i;
+          float x0, x1, x2, x3;
+          fma_f32x2(x0, x1, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]), sl2, sl2,
+                    shift - l4[i].x, shift - l4[i].y);
+          fma_f32x2(x2, x3, __uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]), sl2, sl2,
+                    shift - l4[i].z, shift - l4[i].w);
+          float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+          float p2 = ex2_approx(x2), p3 = ex2_approx(x3);
+          if (!dense) {
+            p0 = c >= from ? p0 : 0.f;
+            p1 = c + 1 >= from ? p1 : 0.f;
+            p2 = c + 2 >= from ? p2 : 0.f;
+            p3 = c + 3 >= from ? p3 : 0.f;
+          }
+          sv[c] = __float_as_uint(p0);
+          sv[c + 1] = __float_as_uint(p1);
+          sv[c + 2] = __float_as_uint(p2);
+          sv[c + 3] = __float_as_uint(p3);
+          pk[2 * i] = pack2<T>(p0, p1);
+          pk[2 * i + 1] = pack2<T>(p2, p3);
+        }
+        BSA_TMEM_ST16(tS + 16u * h2, pk);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_ready + 8 * grp);
+      // dS^T = P^T * (dP^T - D) over dP^T, 32 columns at a time
+      ok = __all_sync(0xffffffffu, mbar_wait(dp_ready, p & 1, abort_flag));
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int h2 = 0; h2 < 2; ++h2) {
+        BSA_TMEM_LD32(tDP + 32u * h2, (dp + 32 * h2));
+        uint32_t pk[16];
+#pragma unroll
+        for (int c4 = 8 * h2; c4 < 8 * h2 + 8; ++c4) {
+          const float4 t4 = reinterpret_cast<const float4*>(dlt)[c4];
+          const float dv[4] = {t4.x, t4.y, t4.z, t4.w};
+#pragma unroll
+          for (int u = 0; u < 4; u += 2) {
+            const int c = 4 * c4 + u;
+            float t0, t1, d0, d1;
+            add_f32x2(t0, t1, __uint_as_float(dp[c]), __uint_as_float(dp[c + 1]), -dv[u],
+                      -dv[u + 1]);
+            if constexpr (kHalf) fma_f32x2(t0, t1, t0, t1, fac_p, fac_p, 0.f, 0.f);
+            fma_f32x2(d0, d1, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]), t0, t1, 0.f,
+                      0.f);
+            pk[(c - 32 * h2) / 2] = pack2<T>(d0, d1);
+          }
+        }
+        BSA_TMEM_ST16(tDP + 16u * h2, pk);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ds_ready + 8 * grp);
+    }
+    if (ok && np > 0) ok = __all_sync(0xffffffffu, mbar_wait(done, 0, abort_flag));
+    if (!ok) {
+      if (lane == 0) report_timeout(abort_flag, io.status);
+    } else {
+      // group 0 writes dV, group 1 dK; keys no query saw have zero gradients
+      tc_fence_after();
+      const Rows& out = grp ? io.dk : io.dv;
+      T* dst = static_cast<T*>(out.p) + int64_t(k0 + kr) * out.sn + int64_t(kvh) * out.sh;
+      const float f = grp ? g.scale / fac : (kHalf ? exp2f(-kPShift) : 1.f);
+#pragma unroll 1
+      for (int ch = 0; ch < D / 32; ++ch) {
+        uint32_t a[32];
+        BSA_TMEM_LD32(tmem + (grp ? C::COL_DK : C::COL_DV) + 32u * ch + lane_base, a);
+        if (exists) store_chunk<T>(dst + 32 * ch, a, f, np > 0);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch_t(const SeqGeo& g, const CUtensorMap* maps, const PackedBwdIO& io,
+                     cudaStream_t st) {
+  auto tiles = [&](int64_t rows) {
+    return rows / 128 + (io.n_seqs < rows ? io.n_seqs : rows);
+  };
+  cudaError_t e;
+  if (io.total_q > 0) {
+    if (std::is_same<T, __half>::value) {
+      e = cudaMemsetAsync(io.norms, 0, 2 * sizeof(float) * g.kv_heads, st);
+      if (e != cudaSuccess) return e;
+      if (io.total_k > 0) {
+        int64_t blocks = (io.total_k + 255) / 256;
+        blocks = blocks < 256 ? blocks : 256;
+        bwd_vnorm_kernel<D><<<dim3(unsigned(blocks), g.kv_heads), 256, 0, st>>>(g, io);
+      }
+    }
+    bwd_prepare_kernel<T, D><<<dim3(unsigned(tiles(io.total_q)), g.heads), 256, 0, st>>>(g, io);
+    auto dq = packed_dq_kernel<T, D>;
+    e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, DqCfg<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    dq<<<unsigned(tiles(io.total_q) * g.heads), DqCfg<D>::kThreads, DqCfg<D>::SMEM, st>>>(
+        maps[0], maps[1], maps[2], g, io);
+  }
+  if (io.total_k > 0) {
+    auto dkdv = packed_dkdv_kernel<T, D>;
+    e = cudaFuncSetAttribute(dkdv, cudaFuncAttributeMaxDynamicSharedMemorySize, DkdvCfg<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    dkdv<<<unsigned(tiles(io.total_k) * g.kv_heads), DkdvCfg<D>::kThreads, DkdvCfg<D>::SMEM, st>>>(
+        maps[0], maps[1], maps[2], maps[3], g, io);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t packed_bwd_workspace_bytes(const SeqGeo& g, int64_t total_q, int64_t n_seqs) {
+  // statistics (lse2 and D per head and padded row) and the norms
+  return sizeof(float) * (2 * size_t(g.heads) * stat_rows(total_q, n_seqs) + 2 * size_t(g.kv_heads));
+}
+
+void packed_bwd_workspace_split(const SeqGeo& g, PackedBwdIO* io, void* workspace) {
+  const size_t n = size_t(g.heads) * stat_rows(io->total_q, io->n_seqs);
+  io->stat_lse = static_cast<float*>(workspace);
+  io->stat_delta = io->stat_lse + n;
+  io->norms = io->stat_delta + n;
+}
+
+cudaError_t launch_packed_bwd(const SeqGeo& g, const CUtensorMap* maps, const PackedBwdIO& io,
+                              cudaStream_t st) {
+  if (g.d == 128)
+    return g.fp16 ? launch_t<__half, 128>(g, maps, io, st) : launch_t<__nv_bfloat16, 128>(g, maps, io, st);
+  return g.fp16 ? launch_t<__half, 64>(g, maps, io, st) : launch_t<__nv_bfloat16, 64>(g, maps, io, st);
+}
+
+}  // namespace bsa

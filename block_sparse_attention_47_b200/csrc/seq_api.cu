@@ -259,6 +259,79 @@ bsa_status bsa_packed_attn_fwd(const bsa_seq_problem* prob, int32_t n_seqs, int6
               "bsa_packed_attn_fwd launch");
 }
 
+bsa_status bsa_query_packed_bwd_workspace(const bsa_seq_problem* prob, int32_t n_seqs,
+                                          int64_t total_q, size_t* bytes) {
+  SEQ_RANGE();
+  SeqGeo g;
+  SEQ_TRY(make_geo(prob, &g));
+  SEQ_TRY(check_counts(n_seqs, total_q, "total_q"));
+  if (!bytes) return fail(BSA_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = bsa::packed_bwd_workspace_bytes(g, total_q, n_seqs);
+  return BSA_OK;
+}
+
+bsa_status bsa_packed_attn_bwd(const bsa_seq_problem* prob, int32_t n_seqs, int64_t total_q,
+                               int64_t total_k, const void* q, int64_t q_stride_n,
+                               int64_t q_stride_h, const void* k, int64_t k_stride_n,
+                               int64_t k_stride_h, const void* v, int64_t v_stride_n,
+                               int64_t v_stride_h, const void* o, int64_t o_stride_n,
+                               int64_t o_stride_h, const void* dout, int64_t do_stride_n,
+                               int64_t do_stride_h, const float* lse, const int32_t* cu_q,
+                               const int32_t* cu_k, void* dq, int64_t dq_stride_n,
+                               int64_t dq_stride_h, void* dk, int64_t dk_stride_n,
+                               int64_t dk_stride_h, void* dv, int64_t dv_stride_n,
+                               int64_t dv_stride_h, void* workspace, size_t ws_bytes,
+                               int32_t* dev_status, void* stream) {
+  SEQ_RANGE();
+  SeqGeo g;
+  SEQ_TRY(make_geo(prob, &g));
+  SEQ_TRY(check_counts(n_seqs, total_q, "total_q"));
+  SEQ_TRY(check_counts(n_seqs, total_k, "total_k"));
+  if (n_seqs == 0 || (total_q == 0 && total_k == 0)) return BSA_OK;
+  SEQ_TRY(check_grid(total_q, n_seqs, g.heads));
+  SEQ_TRY(check_grid(total_k, n_seqs, g.kv_heads));
+  bsa::PackedBwdIO io{};
+  bsa::Rows rq{}, rk{};
+  SEQ_TRY(check_ptr(cu_q, "cu_q", 4));
+  SEQ_TRY(check_ptr(cu_k, "cu_k", 4));
+  if (total_q > 0) {
+    SEQ_TRY(check_tma_rows(&rq, g, q, q_stride_n, q_stride_h, total_q, g.heads, "q"));
+    SEQ_TRY(check_rows(&io.o, o, o_stride_n, o_stride_h, total_q, g.heads, g.d, false, "o"));
+    SEQ_TRY(check_tma_rows(&io.dout, g, dout, do_stride_n, do_stride_h, total_q, g.heads, "dout"));
+    SEQ_TRY(check_ptr(lse, "lse", 4));
+    SEQ_TRY(check_rows(&io.dq, dq, dq_stride_n, dq_stride_h, total_q, g.heads, g.d, true, "dq"));
+  }
+  if (total_k > 0) {
+    SEQ_TRY(check_tma_rows(&rk, g, k, k_stride_n, k_stride_h, total_k, g.kv_heads, "k"));
+    SEQ_TRY(check_tma_rows(&io.v, g, v, v_stride_n, v_stride_h, total_k, g.kv_heads, "v"));
+    SEQ_TRY(check_rows(&io.dk, dk, dk_stride_n, dk_stride_h, total_k, g.kv_heads, g.d, true, "dk"));
+    SEQ_TRY(check_rows(&io.dv, dv, dv_stride_n, dv_stride_h, total_k, g.kv_heads, g.d, true, "dv"));
+  }
+  SEQ_TRY(check_ptr(workspace, "workspace"));
+  if (ws_bytes < bsa::packed_bwd_workspace_bytes(g, total_q, n_seqs))
+    return fail(BSA_ERR_WORKSPACE, "workspace of %zu bytes; %zu are needed", ws_bytes,
+                bsa::packed_bwd_workspace_bytes(g, total_q, n_seqs));
+  SEQ_TRY(check_status(dev_status));
+  SEQ_TRY(bsa::require_device());
+  CUtensorMap maps[4];
+  SEQ_TRY(rows_map(&maps[0], g, rq, total_q, g.heads));
+  SEQ_TRY(rows_map(&maps[1], g, rk, total_k, g.kv_heads));
+  SEQ_TRY(rows_map(&maps[2], g, io.v, total_k, g.kv_heads));
+  SEQ_TRY(rows_map(&maps[3], g, io.dout, total_q, g.heads));
+  SEQ_TRY(bsa::resolve_status(&dev_status));
+  io.cu_q = cu_q;
+  io.cu_k = cu_k;
+  io.n_seqs = n_seqs;
+  io.total_q = total_q;
+  io.total_k = total_k;
+  io.lse = lse;
+  io.status = dev_status;
+  io.stall = bsa::stall_enabled();
+  bsa::packed_bwd_workspace_split(g, &io, workspace);
+  return done(bsa::launch_packed_bwd(g, maps, io, static_cast<cudaStream_t>(stream)),
+              "bsa_packed_attn_bwd launch");
+}
+
 bsa_status bsa_query_decode_workspace(const bsa_seq_problem* prob, size_t* bytes) {
   SEQ_RANGE();
   SeqGeo g;

@@ -82,6 +82,24 @@ struct PackedIO {
 cudaError_t launch_packed_fwd(const SeqGeo& g, const CUtensorMap* maps, const PackedIO& io,
                               cudaStream_t st);
 
+// Pointers of one packed backward; maps: Q, K, V, dO (128-row boxes).
+struct PackedBwdIO {
+  const int32_t *cu_q, *cu_k;
+  int n_seqs;
+  int64_t total_q, total_k;
+  Rows o, dout, v, dq, dk, dv;
+  const float* lse;    // [heads, total_q] from the forward
+  // workspace: statistics per head and padded row, the largest squared norms
+  // of dO and V rows per kv head (fp16)
+  float *stat_lse, *stat_delta, *norms;
+  int32_t* status;
+  int stall;
+};
+size_t packed_bwd_workspace_bytes(const SeqGeo& g, int64_t total_q, int64_t n_seqs);
+void packed_bwd_workspace_split(const SeqGeo& g, PackedBwdIO* io, void* workspace);
+cudaError_t launch_packed_bwd(const SeqGeo& g, const CUtensorMap* maps, const PackedBwdIO& io,
+                              cudaStream_t st);
+
 cudaError_t launch_paged_decode(const SeqGeo& g, const PagedCache& c, const DecodeIO& io,
                                 cudaStream_t st);
 

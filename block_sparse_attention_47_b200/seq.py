@@ -54,6 +54,9 @@ _CACHE = [_P, _P, _I32, _I32, _I64, _I64, _I64, _P, _I64, _I32]
 _SIGS = {
     "bsa_packed_attn_fwd": [_PROB, _I32, _I64, _I64, *_ROWS, *_ROWS, *_ROWS, _P, _P, *_ROWS, _P,
                             _P, _P],
+    "bsa_query_packed_bwd_workspace": [_PROB, _I32, _I64, ctypes.POINTER(ctypes.c_size_t)],
+    "bsa_packed_attn_bwd": [_PROB, _I32, _I64, _I64, *_ROWS, *_ROWS, *_ROWS, *_ROWS, *_ROWS, _P,
+                            _P, _P, *_ROWS, *_ROWS, *_ROWS, _P, ctypes.c_size_t, _P, _P],
     "bsa_kv_append": [_PROB, _I32, _I64, *_ROWS, *_ROWS, *_CACHE, _P, _P, _P, _I32, _I32, _I32, _P,
                       *_ROWS, *_ROWS, *_ROWS, _P, _P],
     "bsa_query_decode_workspace": [_PROB, ctypes.POINTER(ctypes.c_size_t)],
@@ -143,6 +146,12 @@ def _call(name, dev, stream, *args):
             _check(f(*args, stream.cuda_stream))
 
 
+def _workspace(t, dev):
+    if t.device != dev or not t.is_contiguous():
+        raise ValueError("workspace must be contiguous on %s" % dev)
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def _lse_ptr(prob, t, rows, dev):
     if t.device != dev or t.dtype != torch.float32 or tuple(t.shape) != (prob.heads, rows) or \
             not t.is_contiguous():
@@ -164,6 +173,32 @@ def packed_attn_fwd(prob, q, k, v, cu_q, cu_k, out, lse=None, dev_status=None, s
           *_rows(prob, v, tk, prob.kv_heads, dev, "v"), _ints(cu_q, n_seqs + 1, dev, "cu_q"),
           _ints(cu_k, n_seqs + 1, dev, "cu_k"), *_rows(prob, out, tq, prob.heads, dev, "out"),
           None if lse is None else _lse_ptr(prob, lse, tq, dev), _status_ptr(dev_status, dev))
+
+
+def packed_bwd_workspace_bytes(prob, total_q, n_seqs):
+    n = ctypes.c_size_t(0)
+    _check(_fn("bsa_query_packed_bwd_workspace")(ctypes.byref(prob), n_seqs, total_q,
+                                                 ctypes.byref(n)))
+    return int(n.value)
+
+
+def packed_attn_bwd(prob, q, k, v, out, dout, lse, cu_q, cu_k, dq, dk, dv, workspace,
+                    dev_status=None, stream=None):
+    """Gradients dq, dk, dv of packed_attn_fwd from its out and lse and the
+    gradient dout of out (bsa_packed_attn_bwd).  workspace: at least
+    packed_bwd_workspace_bytes(prob, total_q, n_seqs), one per call that may
+    overlap."""
+    dev = _device(q, "q")
+    tq, tk, n_seqs = q.shape[0], k.shape[0], cu_q.shape[0] - 1
+    H, K = prob.heads, prob.kv_heads
+    _call("bsa_packed_attn_bwd", dev, stream, ctypes.byref(prob), n_seqs, tq, tk,
+          *_rows(prob, q, tq, H, dev, "q"), *_rows(prob, k, tk, K, dev, "k"),
+          *_rows(prob, v, tk, K, dev, "v"), *_rows(prob, out, tq, H, dev, "out"),
+          *_rows(prob, dout, tq, H, dev, "dout"), _lse_ptr(prob, lse, tq, dev),
+          _ints(cu_q, n_seqs + 1, dev, "cu_q"), _ints(cu_k, n_seqs + 1, dev, "cu_k"),
+          *_rows(prob, dq, tq, H, dev, "dq"), *_rows(prob, dk, tk, K, dev, "dk"),
+          *_rows(prob, dv, tk, K, dev, "dv"), *_workspace(workspace, dev),
+          _status_ptr(dev_status, dev))
 
 
 def kv_append(prob, k, v, k_cache, v_cache, block_table, cu_new, seq_lens, rope=None,
@@ -205,12 +240,6 @@ def decode_workspace_bytes(prob):
     return int(n.value)
 
 
-def _workspace(t, dev):
-    if t.device != dev or not t.is_contiguous():
-        raise ValueError("workspace must be contiguous on %s" % dev)
-    return t.data_ptr(), t.numel() * t.element_size()
-
-
 def paged_attn_decode(prob, q, k_cache, v_cache, block_table, seq_lens, out, workspace,
                       dev_status=None, stream=None):
     """Attention of one new token per sequence, q [n_seqs, heads, head_dim],
@@ -225,4 +254,5 @@ def paged_attn_decode(prob, q, k_cache, v_cache, block_table, seq_lens, out, wor
           *_workspace(workspace, dev), _status_ptr(dev_status, dev))
 
 
-__all__ = ["SeqProblem", "packed_attn_fwd", "kv_append", "decode_workspace_bytes", "paged_attn_decode"]
+__all__ = ["SeqProblem", "packed_attn_fwd", "packed_bwd_workspace_bytes",
+           "packed_attn_bwd", "kv_append", "decode_workspace_bytes", "paged_attn_decode"]

@@ -82,6 +82,40 @@ bsa_status bsa_packed_attn_fwd(const bsa_seq_problem* prob, int32_t n_seqs, int6
                                void* o, int64_t o_stride_n, int64_t o_stride_h, float* lse,
                                int32_t* dev_status, void* stream);
 
+/* Bytes of bsa_packed_attn_bwd's workspace (row statistics).  Host only. */
+bsa_status bsa_query_packed_bwd_workspace(const bsa_seq_problem* prob, int32_t n_seqs,
+                                          int64_t total_q, size_t* bytes);
+
+/* Gradients of bsa_packed_attn_fwd:
+ *   dV = P^T dO,  dP = dO V^T,  D = rowsum(dO * O),  dS = P * (dP - D),
+ *   dQ = softmax_scale dS K,  dK = softmax_scale dS^T Q,
+ * dK and dV summed over the query heads of their kv head; P is recomputed
+ * from lse.  Every row of a sequence is written (0 where nothing was seen),
+ * rows no sequence owns are left as they were.  Sums are fp32, in a fixed
+ * order without atomics, so gradients do not vary from run to run; P and dS
+ * are rounded to the element type for their products (in fp16 with scales
+ * that keep them in its range).
+ *   q, k, v, cu_q, cu_k   the forward's
+ *   o, lse                its results;  dout the gradient of o, [total_q,
+ *                         heads, head_dim], strides not 0
+ *   dq, dk, dv            shaped as q, k, v; must not overlap any input
+ *   workspace             caller-owned, 16-byte aligned, ws_bytes at least
+ *                         bsa_query_packed_bwd_workspace; holds nothing
+ *                         between calls.  Calls that overlap on the GPU need
+ *                         one each. */
+bsa_status bsa_packed_attn_bwd(const bsa_seq_problem* prob, int32_t n_seqs, int64_t total_q,
+                               int64_t total_k, const void* q, int64_t q_stride_n,
+                               int64_t q_stride_h, const void* k, int64_t k_stride_n,
+                               int64_t k_stride_h, const void* v, int64_t v_stride_n,
+                               int64_t v_stride_h, const void* o, int64_t o_stride_n,
+                               int64_t o_stride_h, const void* dout, int64_t do_stride_n,
+                               int64_t do_stride_h, const float* lse, const int32_t* cu_q,
+                               const int32_t* cu_k, void* dq, int64_t dq_stride_n,
+                               int64_t dq_stride_h, void* dk, int64_t dk_stride_n,
+                               int64_t dk_stride_h, void* dv, int64_t dv_stride_n,
+                               int64_t dv_stride_h, void* workspace, size_t ws_bytes,
+                               int32_t* dev_status, void* stream);
+
 /* Append new keys and values to a paged cache, rotating keys (and queries)
  * on the way.  Token t of the packed [n_tokens, ...] inputs belongs to the
  * sequence b with cu_new[b] <= t < cu_new[b+1]; its position is

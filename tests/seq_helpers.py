@@ -84,3 +84,46 @@ def rope_table(rows, rot, device="cuda"):
     inv = 10000.0 ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
     ang = torch.arange(rows, dtype=torch.float64)[:, None] * inv[None]
     return torch.cat([ang.cos(), ang.sin()], dim=1).float().to(device)
+
+
+def grads64(q, k, v, dout, lim, scale, dtype, factor_bound=None):
+    """One head in float64: (dq, dk, dv) and their error bounds.
+
+    The kernels recompute p from the rounded row statistics, round p and dS
+    to the element type (half a step u), and form D = rowsum(dO * O) from the
+    forward's rounded output:
+        e_p  <= p gp,  gp = 2 g + 6e-6 + 2^-22 (1 + |lse2|)
+        e_dS <= |dS| (u + gp) + p (e_dP + e_D),
+        e_dP <= d 2^-24 |dO| |V|,  e_D <= |dO| (bound of O) + d 2^-24 |dO| |O|
+    and the products add n fp32 roundings and the final half step.  In fp16
+    p and dS are scaled to 2^13 and at most 2^15, so that a value below fp16's
+    normal range adds at most 2^-25 of that scale."""
+    u, n = HALF[dtype], max(q.shape[0], k.shape[0])
+    o, lse2, p, g = attention64(q, k, v, lim, scale)
+    q, k, v, do = q.double(), k.double(), v.double(), dout.double()
+    d = q.shape[1]
+    dp = do @ v.t()
+    row = (do * o).sum(dim=1, keepdim=True)
+    ds = p * (dp - row)
+    dq, dk, dv = scale * ds @ k, scale * ds.t() @ q, p.t() @ do
+    finite = torch.where(torch.isinf(lse2), torch.zeros_like(lse2), lse2)
+    gp = 2 * g + 6e-6 + 2.0 ** -22 * (1 + finite.abs())[:, None]
+    e_o = output_bound(o, p, v, g, dtype)
+    e_d = (do.abs() * e_o).sum(dim=1, keepdim=True) + d * 2.0 ** -24 * (do * o).abs().sum(dim=1, keepdim=True)
+    e_dp = d * 2.0 ** -24 * (do.abs() @ v.abs().t())
+    e_ds = ds.abs() * (u + gp) + p * (e_dp + e_d)
+    e_p = p * (u + gp)
+    if dtype == torch.float16:
+        e_p = e_p + 2.0 ** -25 * 2.0 ** -13
+        if factor_bound:  # 2 max|dO| max|V| sits between 2^14 and 2^15
+            e_ds = e_ds + 2.0 ** -25 * factor_bound * 2.0 ** -14
+    acc = 1.01 + n * 2.0 ** -23
+    e_q = scale * (e_ds @ k.abs()) * acc + n * 2.0 ** -23 * scale * (ds.abs() @ k.abs())
+    e_k = scale * (e_ds.t() @ q.abs()) * acc + n * 2.0 ** -23 * scale * (ds.abs().t() @ q.abs())
+    e_v = (e_p.t() @ do.abs()) * acc + n * 2.0 ** -23 * (p.t() @ do.abs())
+    return (dq, dk, dv), (e_q, e_k, e_v)
+
+
+def rounded_bound(x, e, dtype):
+    """The bound of a stored gradient: its sums' error and the last rounding."""
+    return e + HALF[dtype] * (x.abs() + e) + TINY[dtype]

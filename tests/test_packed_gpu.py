@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import block_sparse_attention_47_b200 as bsa
-from seq_helpers import assert_within, attention64, cu_of, limits, output_bound
+from seq_helpers import (assert_within, attention64, cu_of, grads64, limits, output_bound,
+                         rounded_bound)
 
 pytestmark = pytest.mark.gpu
 BF, FP = torch.bfloat16, torch.float16
@@ -202,3 +203,155 @@ def test_fwd_binding_refuses(cuda_ok):
     with pytest.raises(bsa.BSAError, match="broadcast"):
         bsa.packed_attn_fwd(*a)
     bsa.packed_attn_fwd(*ok)
+
+
+# ---- backward --------------------------------------------------------------------------
+def check_bwd(q, k, v, dout, lq, lk, causal, dq, dk, dv, scale):
+    H, K, dt = q.shape[1], k.shape[1], q.dtype
+    G = H // K
+    q0 = k0 = 0
+    do_n, v_n = dout[:sum(lq)].double(), v[:sum(lk)].double()
+    for a, b in zip(lq, lk):
+        lim = limits(a, b, causal)
+        for kv in range(K):
+            want_k = want_v = e_k = e_v = 0
+            for h in range(kv * G, (kv + 1) * G):
+                top = 2 * float(do_n[:, kv * G:(kv + 1) * G].norm(dim=-1).max() * v_n[:, kv].norm(dim=-1).max()) if sum(lk) and sum(lq) else None
+                (x, y, z), (e, f, g) = grads64(q[q0:q0 + a, h], k[k0:k0 + b, kv], v[k0:k0 + b, kv],
+                                               dout[q0:q0 + a, h], lim, scale, dt, top)
+                assert_within(dq[q0:q0 + a, h], x, rounded_bound(x, e, dt), "dq %d x %d head %d" % (a, b, h))
+                want_k, want_v, e_k, e_v = want_k + y, want_v + z, e_k + f, e_v + g
+            what = "%d x %d kv head %d" % (a, b, kv)
+            assert_within(dk[k0:k0 + b, kv], want_k, rounded_bound(want_k, e_k, dt), "dk " + what)
+            assert_within(dv[k0:k0 + b, kv], want_v, rounded_bound(want_v, e_v, dt), "dv " + what)
+        q0, k0 = q0 + a, k0 + b
+
+
+def backward(prob, q, k, v, dout, cq, ck, wide=8):
+    """Forward and backward into gradients that are slices of wider buffers,
+    with a workspace of NaN."""
+    out, lse = torch.zeros_like(q), torch.zeros(q.shape[1], q.shape[0], device="cuda")
+    st = status_word()
+    bsa.packed_attn_fwd(prob, q, k, v, cq, ck, out, lse, dev_status=st)
+    bufs = [torch.full((t.shape[0], t.shape[1] + 1, t.shape[2] + wide), 5.0, dtype=t.dtype, device="cuda")
+            for t in (q, k, v)]
+    dq, dk, dv = (x[:, :-1, :q.shape[2]] for x in bufs)
+    ws = torch.full((bsa.packed_bwd_workspace_bytes(prob, q.shape[0], cq.shape[0] - 1),), 255,
+                    dtype=torch.uint8, device="cuda")
+    bsa.packed_attn_bwd(prob, q, k, v, out, dout, lse, cq, ck, dq, dk, dv, ws, dev_status=st)
+    assert int(st) == 0
+    return dq, dk, dv, bufs
+
+
+BWD = [
+    # lens_q, lens_k, heads, kv, d, dtype, causal, scale of dout
+    ([1], [1], 1, 1, 64, BF, True, 1.0),
+    ([64, 100, 3], [64, 100, 3], 8, 2, 64, FP, True, 1.0),
+    ([127, 128, 129], [127, 128, 129], 4, 2, 128, BF, True, 1.0),
+    ([0, 300, 0, 5, 0], [0, 300, 7, 5, 0], 6, 2, 128, FP, True, 1e-4),
+    ([64, 511, 3], [640, 700, 130], 4, 1, 64, BF, True, 1.0),
+    ([300, 129, 40], [100, 1, 0], 4, 4, 128, BF, True, 1.0),
+    ([300, 40, 9], [77, 0, 513], 3, 3, 128, FP, False, 500.0),
+    ([700], [700], 3, 1, 128, BF, True, 1.0),
+    ([500, 257], [500, 257], 2, 2, 64, BF, False, 1.0),
+    ([5] * 40 + [200], [5] * 40 + [200], 2, 1, 64, FP, True, 1.0),
+]
+
+
+@pytest.mark.parametrize("case", BWD, ids=[str(i) for i in range(len(BWD))])
+def test_bwd(cuda_ok, case):
+    lq, lk, H, K, d, dt, causal, gain = case
+    q, k, v = inputs(lq, lk, H, K, d, dt)
+    gen = torch.Generator().manual_seed(12)
+    dout = (torch.randn(q.shape[0], H + 2, d, generator=gen) * gain).to(dt)
+    dout[sum(lq):] = math.nan
+    dout = dout.cuda()[:, 1:H + 1]
+    prob = bsa.SeqProblem.make(H, K, d, dt, causal=causal)
+    cq, ck = cu_of(lq), cu_of(lk)
+    dq, dk, dv, bufs = backward(prob, q, k, v, dout, cq, ck)
+    check_bwd(q, k, v, dout, lq, lk, causal, dq, dk, dv, 1 / math.sqrt(d))
+    for x, n in zip(bufs, (sum(lq), sum(lk), sum(lk))):
+        assert bool((x[n:] == 5.0).all()) and bool((x[:, -1] == 5.0).all()) and bool((x[:, :, d:] == 5.0).all())
+    again = backward(prob, q, k, v, dout, cq, ck, wide=0)
+    for x, y, n in zip((dq, dk, dv), again, (sum(lq), sum(lk), sum(lk))):
+        assert torch.equal(x[:n], y[:n])
+
+
+def test_bwd_one_dead_value_stays_where_it_is(cuda_ok):
+    lens = [200, 130, 64]
+    q, k, v = inputs(lens, lens, 2, 1, 64, BF, tail=0)
+    dout = torch.randn(q.shape, device="cuda").bfloat16()
+    prob, cu = bsa.SeqProblem.make(2, 1, 64), cu_of(lens)
+    a = backward(prob, q, k, v, dout, cu, cu)
+    for t in (q, k, v, dout):
+        t[200:330] = math.nan
+    b = backward(prob, q, k, v, dout, cu, cu)
+    for x, y in zip(a[:3], b[:3]):
+        for s in (slice(0, 200), slice(330, 394)):
+            assert torch.equal(x[s], y[s])
+        assert bool(y[200:330].isnan().all())
+
+
+def test_bwd_captured_and_replayed(cuda_ok):
+    lens = [130, 257]
+    q, k, v = inputs(lens, lens, 4, 2, 64, FP, tail=0)
+    dout = torch.randn(q.shape, device="cuda").half()
+    prob, cu = bsa.SeqProblem.make(4, 2, 64, FP), cu_of(lens)
+    want = backward(prob, q, k, v, dout, cu, cu)
+    out, lse = torch.empty_like(q), torch.empty(4, q.shape[0], device="cuda")
+    grads = [torch.zeros_like(t) for t in (q, k, v)]
+    ws = torch.empty(bsa.packed_bwd_workspace_bytes(prob, q.shape[0], 2), dtype=torch.uint8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        bsa.packed_attn_fwd(prob, q, k, v, cu, cu, out, lse)
+        bsa.packed_attn_bwd(prob, q, k, v, out, dout, lse, cu, cu, *grads, ws)
+    for _ in range(2):
+        g.replay()
+        for x, y in zip(grads, want):
+            assert torch.equal(x, y)
+            x.zero_()
+
+
+def test_bwd_timeout_path(cuda_ok):
+    lens = [300]
+    q, k, v = inputs(lens, lens, 2, 1, 64, BF, tail=0)
+    dout = torch.randn(q.shape, device="cuda").bfloat16()
+    prob, cu, st = bsa.SeqProblem.make(2, 1, 64), cu_of(lens), status_word()
+    want = backward(prob, q, k, v, dout, cu, cu)
+    out, lse = torch.empty_like(q), torch.empty(2, 300, device="cuda")
+    bsa.packed_attn_fwd(prob, q, k, v, cu, cu, out, lse)
+    grads = [torch.empty_like(t) for t in (q, k, v)]
+    ws = torch.empty(bsa.packed_bwd_workspace_bytes(prob, 300, 1), dtype=torch.uint8, device="cuda")
+    bsa.debug_stall_pv(True)
+    try:
+        bsa.packed_attn_bwd(prob, q, k, v, out, dout, lse, cu, cu, *grads, ws, dev_status=st)
+        torch.cuda.synchronize()
+    finally:
+        bsa.debug_stall_pv(False)
+    assert int(st) == 6
+    bsa.packed_attn_bwd(prob, q, k, v, out, dout, lse, cu, cu, *grads, ws)
+    for x, y in zip(grads, want):
+        assert torch.equal(x, y)
+
+
+def test_bwd_binding_refuses(cuda_ok):
+    lens = [40]
+    q, k, v = inputs(lens, lens, 4, 2, 64, BF, tail=0)
+    prob, cu = bsa.SeqProblem.make(4, 2, 64), cu_of(lens)
+    out, lse = torch.empty_like(q), torch.empty(4, 40, device="cuda")
+    bsa.packed_attn_fwd(prob, q, k, v, cu, cu, out, lse)
+    ws = torch.empty(bsa.packed_bwd_workspace_bytes(prob, 40, 1), dtype=torch.uint8, device="cuda")
+    ok = [prob, q, k, v, out, q.clone(), lse, cu, cu, torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), ws]
+    for i, bad in [(1, q.cpu()), (2, k.half()), (3, v[:, :1]), (4, out[:3]), (5, q.float()), (6, lse[:, :3]),
+                   (7, cu.long()), (8, cu[:1]), (9, k), (10, q), (11, v.cpu()), (12, ws.cpu())]:
+        a = list(ok)
+        a[i] = bad
+        with pytest.raises(ValueError):
+            bsa.packed_attn_bwd(*a)
+    with pytest.raises(bsa.BSAError):
+        bsa.packed_attn_bwd(*ok[:-1], ws[:64])
+    a = list(ok)
+    a[5] = q[:1].expand_as(q)  # the gradient of a sum: a broadcast view
+    with pytest.raises(bsa.BSAError, match="broadcast"):
+        bsa.packed_attn_bwd(*a)
+    bsa.packed_attn_bwd(*ok)

@@ -181,3 +181,60 @@ def test_binding_refuses_host_tensors():
         bsa.paged_attn_decode(prob(), t, None, None, None, i, t, None)
     with pytest.raises(ValueError, match="CUDA"):
         bsa.kv_append(prob(), t, t, None, None, None, i, i)
+
+
+# ---- the gradient oracle ------------------------------------------------------------
+@pytest.mark.parametrize("lq,lk,causal", [(7, 7, True), (5, 9, True), (9, 5, True), (6, 4, False)])
+def test_gradient_oracle_agrees_with_differences(lq, lk, causal):
+    from seq_helpers import attention64, grads64, limits
+    g = torch.Generator().manual_seed(3)
+    q, k, v, do = (torch.randn(n, 16, generator=g, dtype=torch.float64) for n in (lq, lk, lk, lq))
+    lim, scale, h = limits(lq, lk, causal), 0.3, 1e-5
+    (dq, dk, dv), _ = grads64(q, k, v, do, lim, scale, torch.bfloat16)
+
+    def loss(a, b, c):
+        return float((attention64(a, b, c, lim, scale)[0] * do).sum())
+
+    for i, (x, dx) in enumerate(((q, dq), (k, dk), (v, dv))):
+        for _ in range(4):
+            way = torch.randn(x.shape, generator=g, dtype=torch.float64)
+            up, down = [q, k, v], [q, k, v]
+            up[i], down[i] = x + h * way, x - h * way
+            num = (loss(*up) - loss(*down)) / (2 * h)
+            assert abs(num - float((dx * way).sum())) <= 1e-7 * (1 + abs(num))
+
+
+def bwd_args(**kw):
+    a = dict(prob=ctypes.byref(prob()), n_seqs=2, tq=100, tk=100, q=16, q_sn=512, q_sh=64, k=16,
+             k_sn=128, k_sh=64, v=16, v_sn=128, v_sh=64, o=16, o_sn=512, o_sh=64, do=16, do_sn=512,
+             do_sh=64, lse=16, cu_q=16, cu_k=16, dq=16, dq_sn=512, dq_sh=64, dk=16, dk_sn=128,
+             dk_sh=64, dv=16, dv_sn=128, dv_sh=64, ws=16, ws_bytes=1 << 30, status=None, stream=None)
+    a.update(kw)
+    return list(a.values())
+
+
+BWD_BAD = [
+    (dict(n_seqs=-1), SHAPE, b"n_seqs"), (dict(tq=1 << 31), SHAPE, b"total_q"),
+    (dict(tk=-1), SHAPE, b"total_k"), (dict(q=None), INVALID, b"q is NULL"),
+    (dict(k_sn=0), INVALID, b"broadcast"), (dict(v=17), INVALID, b"v is not"),
+    (dict(o=None), INVALID, b"o is NULL"), (dict(do_sh=0), INVALID, b"dout"),
+    (dict(do=4), INVALID, b"dout"), (dict(lse=None), INVALID, b"lse"), (dict(cu_q=1), INVALID, b"cu_q"),
+    (dict(cu_k=None), INVALID, b"cu_k"), (dict(dq=None), INVALID, b"dq"), (dict(dk_sh=8), INVALID, b"dk"),
+    (dict(dv_sn=0), INVALID, b"dv"), (dict(ws=None), INVALID, b"workspace"),
+    (dict(ws=8), INVALID, b"workspace"), (dict(ws_bytes=100), WORKSPACE, b"workspace"),
+    (dict(status=3), INVALID, b"dev_status"),
+]
+
+
+@pytest.mark.parametrize("kw,status,word", BWD_BAD, ids=[str(k) for k, _, _ in BWD_BAD])
+def test_packed_bwd_refuses(kw, status, word):
+    rc = seq._fn("bsa_packed_attn_bwd")(*bwd_args(**kw))
+    assert rc == status, (rc, bsa.lib().bsa_last_error())
+    assert word in bsa.lib().bsa_last_error()
+
+
+def test_bwd_workspace():
+    """Two floats per head and row of every 128-row tile there can be."""
+    for tq, n in ((0, 0), (1, 1), (1000, 3), (127, 127)):
+        assert bsa.packed_bwd_workspace_bytes(prob(), tq, n) == 4 * (2 * 8 * 128 * (tq // 128 + n + 1) + 2 * 2)
+    assert seq._fn("bsa_packed_attn_bwd")(*bwd_args(tq=0, tk=0)) == 0
