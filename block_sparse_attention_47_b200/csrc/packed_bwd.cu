@@ -40,16 +40,6 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPShift = 13.f;
 
-#define BSA_TMEM_ST16(taddr, r)                                                               \
-  asm volatile(                                                                               \
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "                                        \
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n\t"                         \
-      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),                                          \
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), \
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),       \
-      "r"(r[15])                                                                              \
-      : "memory")
-
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
                                           uint32_t bar) {
   asm volatile(
@@ -103,18 +93,19 @@ __device__ __forceinline__ void store_chunk(T* dst, const uint32_t (&a)[32], flo
 template <typename T, int D>
 __global__ void __launch_bounds__(256) bwd_prepare_kernel(SeqGeo g, const PackedBwdIO io) {
   constexpr int TPR = D / 8;  // threads per row, 16 bytes each
-  __shared__ int where[3];    // any, sequence, tile
+  __shared__ int where[5];    // any, sequence, tile, first row, length
   __shared__ float top[8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (warp == 0) {
-    int b = 0, t = 0;
-    const bool any = find_tile(io.cu_q, io.n_seqs, io.total_q, 128, blockIdx.x, lane, io.status, b, t);
-    if (lane == 0) where[0] = any, where[1] = b, where[2] = t;
+    const Tile f = find_tile(io.cu_q, io.total_q, io.cu_k, io.total_k, io.n_seqs, 128, blockIdx.x,
+                             lane, io.status);
+    if (lane == 0)
+      where[0] = f.any, where[1] = f.seq, where[2] = f.tile, where[3] = f.a.start, where[4] = f.a.len;
   }
   __syncthreads();
   if (!where[0]) return;
   const int b = where[1], t = where[2], head = blockIdx.y;
-  const Span q = span_of(io.cu_q, b, io.total_q, io.status);
+  const Span q{where[3], where[4]};
   const int64_t stats = stat_rows(io.total_q, io.n_seqs);
   const int64_t out0 = int64_t(head) * stats + stat_start(q.start, b) + int64_t(t) * 128;
   float most = 0.f;
@@ -284,17 +275,11 @@ __global__ void __launch_bounds__(352, 1)
     tmem_relinquish();
   }
   if (warp == 9) {
-    int b = 0, t = 0;
-    const bool any = find_tile(io.cu_q, io.n_seqs, io.total_q, 128, blockIdx.x / uint32_t(g.heads),
-                               lane, io.status, b, t);
+    const Tile t = find_tile(io.cu_q, io.total_q, io.cu_k, io.total_k, io.n_seqs, 128,
+                             blockIdx.x / uint32_t(g.heads), lane, io.status);
     if (lane == 0) {
-      found[0] = any;
-      if (any) {
-        const Span q = span_of(io.cu_q, b, io.total_q, io.status);
-        const Span k = span_of(io.cu_k, b, io.total_k, io.status);
-        found[1] = q.start, found[2] = q.len, found[3] = k.start, found[4] = k.len;
-        found[5] = t, found[6] = b;
-      }
+      found[0] = t.any, found[1] = t.a.start, found[2] = t.a.len;
+      found[3] = t.b.start, found[4] = t.b.len, found[5] = t.tile, found[6] = t.seq;
     }
   }
   tc_fence_before();
@@ -629,20 +614,14 @@ __global__ void __launch_bounds__(352, 1)
     tmem_relinquish();
   }
   if (warp == 9) {
-    int b = 0, t = 0;
-    const bool any = find_tile(io.cu_k, io.n_seqs, io.total_k, 128,
-                               blockIdx.x / uint32_t(g.kv_heads), lane, io.status, b, t);
+    const Tile t = find_tile(io.cu_k, io.total_k, io.cu_q, io.total_q, io.n_seqs, 128,
+                             blockIdx.x / uint32_t(g.kv_heads), lane, io.status);
     if (lane == 0) {
-      found[0] = any;
-      if (any) {
-        const Span q = span_of(io.cu_q, b, io.total_q, io.status);
-        const Span k = span_of(io.cu_k, b, io.total_k, io.status);
-        found[1] = q.start, found[2] = q.len, found[3] = k.start, found[4] = k.len;
-        // in causal order a sequence's first keys are seen by the most
-        // queries: the longest walks first
-        found[5] = g.causal ? (k.len + 127) / 128 - 1 - t : t;
-        found[6] = b;
-      }
+      found[0] = t.any, found[1] = t.b.start, found[2] = t.b.len;
+      found[3] = t.a.start, found[4] = t.a.len, found[6] = t.seq;
+      // in causal order a sequence's first keys are seen by the most
+      // queries: the longest walks first
+      found[5] = g.causal ? (t.a.len + 127) / 128 - 1 - t.tile : t.tile;
     }
   }
   tc_fence_before();

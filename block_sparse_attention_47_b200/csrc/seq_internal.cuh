@@ -138,6 +138,16 @@ __host__ __device__ constexpr uint32_t idesc_f32(int M, int N, bool b_mn_major) 
          (std::is_same<T, __half>::value ? ~((1u << 7) | (1u << 10)) : ~0u);
 }
 
+#define BSA_TMEM_ST16(taddr, r)                                                               \
+  asm volatile(                                                                               \
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "                                        \
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n\t"                         \
+      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),                                          \
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), \
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),       \
+      "r"(r[15])                                                                              \
+      : "memory")
+
 // 128 columns of this thread's tensor-memory lane
 #define BSA_TMEM_LD128(taddr, r)  \
   asm volatile(  \
@@ -163,63 +173,79 @@ __device__ __forceinline__ Span span_of(const int32_t* __restrict__ cu, int b, i
   return {a, z - a};
 }
 
-// The tile `target` of the list of all sequences' tiles of `rows` rows, last
-// sequence and last tile first (in causal order the longest walks come
-// first), by a whole warp.  False when the list is shorter.
-__device__ __forceinline__ bool find_tile(const int32_t* __restrict__ cu, int n_seqs, int64_t total,
-                                          int rows, int64_t target, int lane, int32_t* status,
-                                          int& seq, int& tile) {
+// A tile of a packed call: the rows of sequence `seq` in the tiled tensor (a)
+// and in the other one (b).
+struct Tile {
+  bool any;
+  int seq, tile;
+  Span a, b;
+};
+
+// The tile `target` of the list of all sequences' tiles of `rows` rows of a,
+// last sequence and last tile first (in causal order the longest walks come
+// first), by a whole warp.  any = false when the list is shorter.
+__device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ cu_a, int64_t total_a,
+                                          const int32_t* __restrict__ cu_b, int64_t total_b,
+                                          int n_seqs, int rows, int64_t target, int lane,
+                                          int32_t* status) {
+  Tile t{};
   int64_t before = 0;
   for (int base = 0; base < n_seqs; base += 32) {
-    const int b = n_seqs - 1 - base - lane;
-    const int n = b >= 0 ? (span_of(cu, b, total, status).len + rows - 1) / rows : 0;
+    const int s = n_seqs - 1 - base - lane;
+    Span a{0, 0}, b{0, 0};
+    if (s >= 0) {  // four independent loads: one latency
+      a = span_of(cu_a, s, total_a, status);
+      b = span_of(cu_b, s, total_b, status);
+    }
+    const int n = (a.len + rows - 1) / rows;
     int incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
     }
-    const bool here = before + incl > target;
-    const uint32_t m = __ballot_sync(0xffffffffu, here);
+    const uint32_t m = __ballot_sync(0xffffffffu, before + incl > target);
     if (m) {
       const int l = __ffs(m) - 1;
       const int n_l = __shfl_sync(0xffffffffu, n, l), incl_l = __shfl_sync(0xffffffffu, incl, l);
-      seq = n_seqs - 1 - base - l;
-      tile = n_l - 1 - int(target - (before + incl_l - n_l));
-      return true;
+      t.any = true;
+      t.seq = n_seqs - 1 - base - l;
+      t.tile = n_l - 1 - int(target - (before + incl_l - n_l));
+      t.a = {__shfl_sync(0xffffffffu, a.start, l), __shfl_sync(0xffffffffu, a.len, l)};
+      t.b = {__shfl_sync(0xffffffffu, b.start, l), __shfl_sync(0xffffffffu, b.len, l)};
+      return t;
     }
     before += __shfl_sync(0xffffffffu, incl, 31);
   }
-  return false;
+  return t;
+}
+
+// Rows of a 16-bit tile through shared memory, so that a warp writes whole
+// rows: a thread stages its own row (16-byte chunks swizzled by the row), and
+// the warp then writes 16 bytes a lane, 512 consecutive ones at d = 128.
+// `stage`: this warp's 32 rows of D * 2 bytes.
+template <int D>
+__device__ __forceinline__ void stage_chunk(uint32_t stage, int row, int chunk, uint4 v) {
+  st_shared_v4(stage + row * (2 * D) + ((chunk ^ (row & 7)) << 4), v);
+}
+template <typename T, int D>
+__device__ __forceinline__ void write_rows(uint32_t stage, T* dst, int64_t stride, int n_rows,
+                                           int lane) {
+  constexpr int CH = D / 8;  // 16-byte chunks of a row
+  __syncwarp();
+#pragma unroll
+  for (int it = 0; it < CH; ++it) {
+    const int row = it * (32 / CH) + lane / CH, ch = lane % CH;
+    const float4 v = ld_shared_f4(stage + row * (2 * D) + ((ch ^ (row & 7)) << 4));
+    if (row < n_rows)
+      *reinterpret_cast<float4*>(dst + int64_t(row) * stride + ch * 8) = v;
+  }
+  __syncwarp();
 }
 
 __device__ __forceinline__ void report_timeout(volatile int* abort_flag, int32_t* status) {
   *abort_flag = 1;
   atomicCAS(status, 0, int32_t(BSA_ERR_TIMEOUT));
-}
-
-// 2^x for two lanes on the FMA pipe: 2^n * 2^f, n the nearest integer (from
-// adding 1.5 * 2^23), 2^f on [-0.5, 0.5] by a degree-4 polynomial fitted for
-// the least largest relative error (2.7e-6).  x is clamped at -125 so that
-// the result stays a normal number.
-__device__ __forceinline__ void exp2_fma_x2(float& y0, float& y1, float x0, float x1) {
-  constexpr float kRound = 12582912.f;  // 1.5 * 2^23
-  constexpr float c0 = 0.99999928f, c1 = 0.69312179f, c2 = 0.24024744f, c3 = 0.05591786f,
-                  c4 = 0.00957010f;
-  x0 = fmaxf(x0, -125.f);
-  x1 = fmaxf(x1, -125.f);
-  float t0, t1, n0, n1, f0, f1, p0, p1;
-  add_f32x2(t0, t1, x0, x1, kRound, kRound);
-  add_f32x2(n0, n1, t0, t1, -kRound, -kRound);
-  add_f32x2(f0, f1, x0, x1, -n0, -n1);
-  fma_f32x2(p0, p1, f0, f1, c4, c4, c3, c3);
-  fma_f32x2(p0, p1, p0, p1, f0, f1, c2, c2);
-  fma_f32x2(p0, p1, p0, p1, f0, f1, c1, c1);
-  fma_f32x2(p0, p1, p0, p1, f0, f1, c0, c0);
-  // the low bits of t hold n (two's complement); shifted into the exponent
-  // field, the constant's own bits fall off the top
-  y0 = __int_as_float(__float_as_int(p0) + int(uint32_t(__float_as_int(t0)) << 23));
-  y1 = __int_as_float(__float_as_int(p1) + int(uint32_t(__float_as_int(t1)) << 23));
 }
 #endif
 

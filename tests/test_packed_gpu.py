@@ -67,6 +67,17 @@ FWD = [
 ]
 
 
+# few query tiles and many keys: the key axis is shared by a cluster
+FWD += [
+    ([1], [5000], 8, 1, 128, BF, True),
+    ([64, 1, 200], [4096, 3000, 129], 4, 2, 64, FP, True),
+    ([256, 130], [2600, 700], 3, 1, 128, BF, True),
+    ([130], [6001], 6, 2, 128, FP, False),
+    ([5, 0, 300], [1030, 0, 40], 2, 1, 64, BF, True),   # a text with no key for its first rows
+    ([700], [2000], 1, 1, 64, BF, True),
+]
+
+
 @pytest.mark.parametrize("case", FWD, ids=[str(i) for i in range(len(FWD))])
 def test_fwd(cuda_ok, case):
     lq, lk, H, K, d, dt, causal = case
