@@ -285,8 +285,54 @@ bsa_status check_raster_kv(const Geo& g, int64_t sh, const char* name) {
 namespace bsa {
 void clear_error() { g_last_error[0] = 0; }
 bsa_status cuda_error(cudaError_t e, const char* what) { return cuda_fail(e, what); }
-bsa_status require_device() { return check_device(); }
-bsa_status resolve_status(int32_t** status) { return status_word(status); }
+
+// What a device is does not change: looked up once per device, since these
+// calls are as short as the queries (about 1 us) are.
+namespace {
+struct DeviceFacts {
+  int sms = 0;
+  int32_t* word = nullptr;
+};
+std::mutex g_facts_mutex;
+DeviceFacts g_facts[64];
+
+bsa_status device_facts(DeviceFacts* out) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (dev < 0 || dev >= 64) return fail(BSA_ERR_UNSUPPORTED, "device %d", dev);
+  std::lock_guard<std::mutex> lock(g_facts_mutex);
+  DeviceFacts& f = g_facts[dev];
+  if (!f.sms) {
+    BSA_TRY(check_device());
+    int32_t* word = nullptr;
+    BSA_TRY(status_word(&word));
+    int sms = 0;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
+    f.word = word;
+    f.sms = sms;
+  }
+  *out = f;
+  return BSA_OK;
+}
+}  // namespace
+
+bsa_status require_device() {
+  DeviceFacts f;
+  return device_facts(&f);
+}
+bsa_status resolve_status(int32_t** status) {
+  if (*status) return BSA_OK;
+  DeviceFacts f;
+  BSA_TRY(device_facts(&f));
+  *status = f.word;
+  return BSA_OK;
+}
+int device_sms() {
+  DeviceFacts f;
+  return device_facts(&f) == BSA_OK ? f.sms : 0;
+}
 bool stall_enabled() { return g_stall_pv != 0; }
 void range_push(const char* name) { nvtxRangePushA(name); }
 void range_pop() { nvtxRangePop(); }

@@ -516,7 +516,8 @@ cudaError_t launch_t(const SeqGeo& g, const CUtensorMap* maps, const PackedIO& i
     return cudaFuncGetAttributes(&a, kern) == cudaSuccess ? a.numRegs : 0;
   }();
   if (regs != 168) return cudaErrorInvalidConfiguration;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static std::atomic<uint64_t> seen{0};
+  cudaError_t e = allow_smem(kern, C::SMEM, seen);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(unsigned(units * ranks));

@@ -934,14 +934,16 @@ cudaError_t launch_t(const SeqGeo& g, const CUtensorMap* maps, const PackedBwdIO
     }
     bwd_prepare_kernel<T, D><<<dim3(unsigned(tiles(io.total_q)), g.heads), 256, 0, st>>>(g, io);
     auto dq = packed_dq_kernel<T, D>;
-    e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, DqCfg<D>::SMEM);
+    static std::atomic<uint64_t> seen{0};
+    e = allow_smem(dq, DqCfg<D>::SMEM, seen);
     if (e != cudaSuccess) return e;
     dq<<<unsigned(tiles(io.total_q) * g.heads), DqCfg<D>::kThreads, DqCfg<D>::SMEM, st>>>(
         maps[0], maps[1], maps[2], g, io);
   }
   if (io.total_k > 0) {
     auto dkdv = packed_dkdv_kernel<T, D>;
-    e = cudaFuncSetAttribute(dkdv, cudaFuncAttributeMaxDynamicSharedMemorySize, DkdvCfg<D>::SMEM);
+    static std::atomic<uint64_t> seen{0};
+    e = allow_smem(dkdv, DkdvCfg<D>::SMEM, seen);
     if (e != cudaSuccess) return e;
     dkdv<<<unsigned(tiles(io.total_k) * g.kv_heads), DkdvCfg<D>::kThreads, DkdvCfg<D>::SMEM, st>>>(
         maps[0], maps[1], maps[2], maps[3], g, io);

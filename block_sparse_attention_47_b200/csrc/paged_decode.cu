@@ -511,10 +511,7 @@ __global__ void __launch_bounds__(128)
 template <typename T, int D>
 cudaError_t launch_t(const SeqGeo& g, const PagedCache& c, const DecodeIO& io, cudaStream_t st) {
   using C = DecCfg<D>;
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
+  const int sms = device_sms();
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   Shape sh;
   sh.n_seqs = io.n_seqs;
@@ -524,7 +521,8 @@ cudaError_t launch_t(const SeqGeo& g, const PagedCache& c, const DecodeIO& io, c
   sh.max_len = int(reach < (int64_t(1) << 31) - 64 ? reach : (int64_t(1) << 31) - 64);
   sh.lens = io.lens;
   auto kern = paged_decode_kernel<T, D>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static std::atomic<uint64_t> seen{0};
+  cudaError_t e = allow_smem(kern, C::SMEM, seen);
   if (e != cudaSuccess) return e;
   kern<<<ctas, 32 * kDecWarps, C::SMEM, st>>>(g, c, io, sh);
   e = cudaGetLastError();

@@ -65,8 +65,10 @@ bsa_status check_ptr(const void* p, const char* name, unsigned align = 16) {
 
 // A [rows, heads, d] tensor.  The stride of an axis of extent 1 is replaced
 // by the contiguous one; `own` (outputs): rows and heads must not overlap.
-bsa_status check_rows(bsa::Rows* r, const void* p, int64_t sn, int64_t sh, int64_t rows, int heads,
-                      int d, bool own, const char* name) {
+bsa_status check_rows(bsa::Rows* r, const bsa_rows& in, int64_t rows, int heads, int d, bool own,
+                      const char* name) {
+  void* p = in.data;
+  int64_t sn = in.stride_n, sh = in.stride_h;
   SEQ_TRY(check_ptr(p, name));
   if (heads == 1) sh = d;
   if (rows <= 1) sn = int64_t(heads) * d;
@@ -75,54 +77,55 @@ bsa_status check_rows(bsa::Rows* r, const void* p, int64_t sn, int64_t sh, int64
                 name);
   if (own && (sn < d || sh < d))
     return fail(BSA_ERR_INVALID_ARG, "%s is written: its strides must be at least head_dim", name);
-  r->p = const_cast<void*>(p);
+  r->p = p;
   r->sn = sn;
   r->sh = sh;
   return BSA_OK;
 }
 
-bsa_status check_cache(bsa::PagedCache* c, const SeqGeo& g, const void* k, const void* v,
-                       int32_t n_pages, int32_t page_size, int64_t sp, int64_t st, int64_t sh,
-                       const int32_t* table, int64_t table_stride, int32_t table_width,
-                       int32_t n_seqs) {
-  SEQ_TRY(check_ptr(k, "k_cache"));
-  SEQ_TRY(check_ptr(v, "v_cache"));
-  SEQ_TRY(check_ptr(table, "block_table", 4));
-  if (n_pages < 1 || page_size < 1)
-    return fail(BSA_ERR_SHAPE, "n_pages (%d) and page_size (%d) must be >= 1", n_pages, page_size);
-  if (table_width < 1 || (n_seqs > 1 && table_stride < table_width))
-    return fail(BSA_ERR_SHAPE, "block_table: width %d, row stride %lld", table_width,
-                (long long)table_stride);
-  if (n_pages == 1) sp = 0;
-  if (page_size == 1) st = 0;
-  if (g.kv_heads == 1) sh = 0;
+bsa_status check_cache(bsa::PagedCache* c, const SeqGeo& g, const bsa_paged_cache& in,
+                       int64_t n_seqs) {
+  SEQ_TRY(check_ptr(in.k, "k_cache"));
+  SEQ_TRY(check_ptr(in.v, "v_cache"));
+  SEQ_TRY(check_ptr(in.block_table, "block_table", 4));
+  if (in.n_pages < 1 || in.page_size < 1 || in.n_pages > INT32_MAX || in.page_size > INT32_MAX)
+    return fail(BSA_ERR_SHAPE, "n_pages (%lld) and page_size (%lld) must lie in 1..2^31-1",
+                (long long)in.n_pages, (long long)in.page_size);
+  if (in.table_width < 1 || in.table_width > INT32_MAX ||
+      (n_seqs > 1 && in.table_stride < in.table_width))
+    return fail(BSA_ERR_SHAPE, "block_table: width %lld, row stride %lld",
+                (long long)in.table_width, (long long)in.table_stride);
+  const int64_t sp = in.n_pages == 1 ? 0 : in.stride_page;
+  const int64_t st = in.page_size == 1 ? 0 : in.stride_token;
+  const int64_t sh = g.kv_heads == 1 ? 0 : in.stride_head;
   if (sp < 0 || st < 0 || sh < 0 || (sp % 8) || (st % 8) || (sh % 8) ||
-      (n_pages > 1 && sp < g.d) || (page_size > 1 && st < g.d) || (g.kv_heads > 1 && sh < g.d))
+      (in.n_pages > 1 && sp < g.d) || (in.page_size > 1 && st < g.d) ||
+      (g.kv_heads > 1 && sh < g.d))
     return fail(BSA_ERR_INVALID_ARG,
                 "cache strides must be multiples of 8 elements and at least head_dim");
-  c->k = const_cast<void*>(k);
-  c->v = const_cast<void*>(v);
+  c->k = in.k;
+  c->v = in.v;
   c->sp = sp;
   c->st = st;
   c->sh = sh;
-  c->n_pages = n_pages;
-  c->page_size = page_size;
-  c->table = table;
-  c->table_stride = table_stride;
-  c->table_width = table_width;
+  c->n_pages = int(in.n_pages);
+  c->page_size = int(in.page_size);
+  c->table = in.block_table;
+  c->table_stride = in.table_stride;
+  c->table_width = int(in.table_width);
   return BSA_OK;
 }
 
-bsa_status check_counts(int32_t n_seqs, int64_t rows, const char* what) {
+bsa_status check_counts(int64_t n_seqs, int64_t rows, const char* what) {
   if (n_seqs < 0 || n_seqs > (1 << 24))
-    return fail(BSA_ERR_SHAPE, "n_seqs %d outside 0..2^24", n_seqs);
+    return fail(BSA_ERR_SHAPE, "n_seqs %lld outside 0..2^24", (long long)n_seqs);
   if (rows < 0 || rows > INT32_MAX)
     return fail(BSA_ERR_SHAPE, "%s %lld outside 0..2^31-1", what, (long long)rows);
   return BSA_OK;
 }
 
 // one CTA per 128-row tile and head at most
-bsa_status check_grid(int64_t rows, int32_t n_seqs, int heads) {
+bsa_status check_grid(int64_t rows, int64_t n_seqs, int heads) {
   if ((rows / 128 + (n_seqs < rows ? n_seqs : rows)) * heads > INT32_MAX)
     return fail(BSA_ERR_SHAPE, "too many (tile, head) pairs for one call");
   return BSA_OK;
@@ -135,9 +138,9 @@ bsa_status check_status(const int32_t* p) {
 }
 
 // a tensor read by TMA boxes: broadcast views have no tensor map
-bsa_status check_tma_rows(bsa::Rows* r, const SeqGeo& g, const void* p, int64_t sn, int64_t sh,
-                          int64_t rows, int heads, const char* name) {
-  SEQ_TRY(check_rows(r, p, sn, sh, rows, heads, g.d, false, name));
+bsa_status check_tma_rows(bsa::Rows* r, const SeqGeo& g, const bsa_rows& in, int64_t rows,
+                          int heads, const char* name) {
+  SEQ_TRY(check_rows(r, in, rows, heads, g.d, false, name));
   if (r->sn == 0 || r->sh == 0)
     return fail(BSA_ERR_INVALID_ARG, "%s: strides of 0 (broadcast views) are not supported", name);
   return BSA_OK;
@@ -157,102 +160,41 @@ bsa_status done(cudaError_t e, const char* what) {
 
 extern "C" {
 
-bsa_status bsa_kv_append(const bsa_seq_problem* prob, int32_t n_seqs, int64_t n_tokens,
-                         const void* k, int64_t k_stride_n, int64_t k_stride_h, const void* v,
-                         int64_t v_stride_n, int64_t v_stride_h, void* k_cache, void* v_cache,
-                         int32_t n_pages, int32_t page_size, int64_t stride_page,
-                         int64_t stride_token, int64_t stride_head, const int32_t* block_table,
-                         int64_t table_stride, int32_t table_width, const int32_t* cu_new,
-                         const int32_t* seq_lens, const float* rope, int32_t rope_n,
-                         int32_t rot_dim, int32_t interleaved, const int32_t* rope_rows,
-                         const void* q, int64_t q_stride_n, int64_t q_stride_h, void* q_out,
-                         int64_t qo_stride_n, int64_t qo_stride_h, void* k_out,
-                         int64_t ko_stride_n, int64_t ko_stride_h, int32_t* dev_status,
-                         void* stream) {
-  SEQ_RANGE();
-  SeqGeo g;
-  SEQ_TRY(make_geo(prob, &g));
-  SEQ_TRY(check_counts(n_seqs, n_tokens, "n_tokens"));
-  if (n_tokens == 0 || n_seqs == 0) return BSA_OK;
-  bsa::AppendIO io{};
-  bsa::PagedCache c{};
-  SEQ_TRY(check_rows(&io.k, k, k_stride_n, k_stride_h, n_tokens, g.kv_heads, g.d, false, "k"));
-  SEQ_TRY(check_rows(&io.v, v, v_stride_n, v_stride_h, n_tokens, g.kv_heads, g.d, false, "v"));
-  SEQ_TRY(check_cache(&c, g, k_cache, v_cache, n_pages, page_size, stride_page, stride_token,
-                      stride_head, block_table, table_stride, table_width, n_seqs));
-  SEQ_TRY(check_ptr(cu_new, "cu_new", 4));
-  SEQ_TRY(check_ptr(seq_lens, "seq_lens", 4));
-  if (rope) {
-    SEQ_TRY(check_ptr(rope, "rope"));
-    if (rope_n < 1) return fail(BSA_ERR_SHAPE, "rope_n must be >= 1");
-    if (rot_dim < 16 || rot_dim > g.d || rot_dim % 16)
-      return fail(BSA_ERR_SHAPE, "rot_dim %d must be a multiple of 16 up to head_dim", rot_dim);
-    if (rope_rows) SEQ_TRY(check_ptr(rope_rows, "rope_rows", 4));
-  }
-  if (!q != !q_out) return fail(BSA_ERR_INVALID_ARG, "give q and q_out, or neither");
-  if (q) {
-    SEQ_TRY(check_rows(&io.q, q, q_stride_n, q_stride_h, n_tokens, g.heads, g.d, false, "q"));
-    SEQ_TRY(check_rows(&io.q_out, q_out, qo_stride_n, qo_stride_h, n_tokens, g.heads, g.d, true,
-                       "q_out"));
-  }
-  if (k_out)
-    SEQ_TRY(check_rows(&io.k_out, k_out, ko_stride_n, ko_stride_h, n_tokens, g.kv_heads, g.d, true,
-                       "k_out"));
-  SEQ_TRY(check_status(dev_status));
-  SEQ_TRY(bsa::require_device());
-  SEQ_TRY(bsa::resolve_status(&dev_status));
-  io.cu = cu_new;
-  io.lens = seq_lens;
-  io.rope = rope;
-  io.rope_rows = rope_rows;
-  io.rope_n = rope_n;
-  io.rot = rope ? rot_dim : 0;
-  io.interleaved = interleaved != 0;
-  io.n_seqs = n_seqs;
-  io.n_tokens = n_tokens;
-  io.status = dev_status;
-  return done(bsa::launch_kv_append(g, c, io, static_cast<cudaStream_t>(stream)),
-              "bsa_kv_append launch");
-}
-
-bsa_status bsa_packed_attn_fwd(const bsa_seq_problem* prob, int32_t n_seqs, int64_t total_q,
-                               int64_t total_k, const void* q, int64_t q_stride_n,
-                               int64_t q_stride_h, const void* k, int64_t k_stride_n,
-                               int64_t k_stride_h, const void* v, int64_t v_stride_n,
-                               int64_t v_stride_h, const int32_t* cu_q, const int32_t* cu_k,
-                               void* o, int64_t o_stride_n, int64_t o_stride_h, float* lse,
+bsa_status bsa_packed_attn_fwd(const bsa_seq_problem* prob, const bsa_packed_args* a,
                                int32_t* dev_status, void* stream) {
   SEQ_RANGE();
   SeqGeo g;
   SEQ_TRY(make_geo(prob, &g));
-  SEQ_TRY(check_counts(n_seqs, total_q, "total_q"));
-  SEQ_TRY(check_counts(n_seqs, total_k, "total_k"));
-  if (total_q == 0 || n_seqs == 0) return BSA_OK;
-  SEQ_TRY(check_grid(total_q, n_seqs, g.heads));
+  if (!a) return fail(BSA_ERR_INVALID_ARG, "args is NULL");
+  const int64_t tq = a->total_q, tk = a->total_k;
+  SEQ_TRY(check_counts(a->n_seqs, tq, "total_q"));
+  SEQ_TRY(check_counts(a->n_seqs, tk, "total_k"));
+  if (tq == 0 || a->n_seqs == 0) return BSA_OK;
+  SEQ_TRY(check_grid(tq, a->n_seqs, g.heads));
   bsa::PackedIO io{};
   bsa::Rows rq, rk{}, rv{};
-  SEQ_TRY(check_ptr(cu_q, "cu_q", 4));
-  SEQ_TRY(check_ptr(cu_k, "cu_k", 4));
-  SEQ_TRY(check_rows(&io.o, o, o_stride_n, o_stride_h, total_q, g.heads, g.d, true, "o"));
-  if (lse) SEQ_TRY(check_ptr(lse, "lse", 4));
+  SEQ_TRY(check_ptr(a->cu_q, "cu_q", 4));
+  SEQ_TRY(check_ptr(a->cu_k, "cu_k", 4));
+  SEQ_TRY(check_rows(&io.o, a->o, tq, g.heads, g.d, true, "o"));
+  if (a->lse) SEQ_TRY(check_ptr(a->lse, "lse", 4));
   SEQ_TRY(check_status(dev_status));
-  SEQ_TRY(check_tma_rows(&rq, g, q, q_stride_n, q_stride_h, total_q, g.heads, "q"));
-  if (total_k > 0) {  // else no row sees a key
-    SEQ_TRY(check_tma_rows(&rk, g, k, k_stride_n, k_stride_h, total_k, g.kv_heads, "k"));
-    SEQ_TRY(check_tma_rows(&rv, g, v, v_stride_n, v_stride_h, total_k, g.kv_heads, "v"));
+  SEQ_TRY(check_tma_rows(&rq, g, a->q, tq, g.heads, "q"));
+  if (tk > 0) {  // else no row sees a key
+    SEQ_TRY(check_tma_rows(&rk, g, a->k, tk, g.kv_heads, "k"));
+    SEQ_TRY(check_tma_rows(&rv, g, a->v, tk, g.kv_heads, "v"));
   }
   SEQ_TRY(bsa::require_device());
   CUtensorMap maps[3];
-  SEQ_TRY(rows_map(&maps[0], g, rq, total_q, g.heads));
-  SEQ_TRY(rows_map(&maps[1], g, rk, total_k, g.kv_heads));
-  SEQ_TRY(rows_map(&maps[2], g, rv, total_k, g.kv_heads));
+  SEQ_TRY(rows_map(&maps[0], g, rq, tq, g.heads));
+  SEQ_TRY(rows_map(&maps[1], g, rk, tk, g.kv_heads));
+  SEQ_TRY(rows_map(&maps[2], g, rv, tk, g.kv_heads));
   SEQ_TRY(bsa::resolve_status(&dev_status));
-  io.cu_q = cu_q;
-  io.cu_k = cu_k;
-  io.n_seqs = n_seqs;
-  io.total_q = total_q;
-  io.total_k = total_k;
-  io.lse = lse;
+  io.cu_q = a->cu_q;
+  io.cu_k = a->cu_k;
+  io.n_seqs = int(a->n_seqs);
+  io.total_q = tq;
+  io.total_k = tk;
+  io.lse = a->lse;
   io.status = dev_status;
   io.stall = bsa::stall_enabled();
   return done(bsa::launch_packed_fwd(g, maps, io, static_cast<cudaStream_t>(stream)),
@@ -270,66 +212,107 @@ bsa_status bsa_query_packed_bwd_workspace(const bsa_seq_problem* prob, int32_t n
   return BSA_OK;
 }
 
-bsa_status bsa_packed_attn_bwd(const bsa_seq_problem* prob, int32_t n_seqs, int64_t total_q,
-                               int64_t total_k, const void* q, int64_t q_stride_n,
-                               int64_t q_stride_h, const void* k, int64_t k_stride_n,
-                               int64_t k_stride_h, const void* v, int64_t v_stride_n,
-                               int64_t v_stride_h, const void* o, int64_t o_stride_n,
-                               int64_t o_stride_h, const void* dout, int64_t do_stride_n,
-                               int64_t do_stride_h, const float* lse, const int32_t* cu_q,
-                               const int32_t* cu_k, void* dq, int64_t dq_stride_n,
-                               int64_t dq_stride_h, void* dk, int64_t dk_stride_n,
-                               int64_t dk_stride_h, void* dv, int64_t dv_stride_n,
-                               int64_t dv_stride_h, void* workspace, size_t ws_bytes,
+bsa_status bsa_packed_attn_bwd(const bsa_seq_problem* prob, const bsa_packed_args* a,
                                int32_t* dev_status, void* stream) {
   SEQ_RANGE();
   SeqGeo g;
   SEQ_TRY(make_geo(prob, &g));
-  SEQ_TRY(check_counts(n_seqs, total_q, "total_q"));
-  SEQ_TRY(check_counts(n_seqs, total_k, "total_k"));
-  if (n_seqs == 0 || (total_q == 0 && total_k == 0)) return BSA_OK;
-  SEQ_TRY(check_grid(total_q, n_seqs, g.heads));
-  SEQ_TRY(check_grid(total_k, n_seqs, g.kv_heads));
+  if (!a) return fail(BSA_ERR_INVALID_ARG, "args is NULL");
+  const int64_t tq = a->total_q, tk = a->total_k;
+  SEQ_TRY(check_counts(a->n_seqs, tq, "total_q"));
+  SEQ_TRY(check_counts(a->n_seqs, tk, "total_k"));
+  if (a->n_seqs == 0 || (tq == 0 && tk == 0)) return BSA_OK;
+  SEQ_TRY(check_grid(tq, a->n_seqs, g.heads));
+  SEQ_TRY(check_grid(tk, a->n_seqs, g.kv_heads));
   bsa::PackedBwdIO io{};
   bsa::Rows rq{}, rk{};
-  SEQ_TRY(check_ptr(cu_q, "cu_q", 4));
-  SEQ_TRY(check_ptr(cu_k, "cu_k", 4));
-  if (total_q > 0) {
-    SEQ_TRY(check_tma_rows(&rq, g, q, q_stride_n, q_stride_h, total_q, g.heads, "q"));
-    SEQ_TRY(check_rows(&io.o, o, o_stride_n, o_stride_h, total_q, g.heads, g.d, false, "o"));
-    SEQ_TRY(check_tma_rows(&io.dout, g, dout, do_stride_n, do_stride_h, total_q, g.heads, "dout"));
-    SEQ_TRY(check_ptr(lse, "lse", 4));
-    SEQ_TRY(check_rows(&io.dq, dq, dq_stride_n, dq_stride_h, total_q, g.heads, g.d, true, "dq"));
+  SEQ_TRY(check_ptr(a->cu_q, "cu_q", 4));
+  SEQ_TRY(check_ptr(a->cu_k, "cu_k", 4));
+  if (tq > 0) {
+    SEQ_TRY(check_tma_rows(&rq, g, a->q, tq, g.heads, "q"));
+    SEQ_TRY(check_rows(&io.o, a->o, tq, g.heads, g.d, false, "o"));
+    SEQ_TRY(check_tma_rows(&io.dout, g, a->dout, tq, g.heads, "dout"));
+    SEQ_TRY(check_ptr(a->lse, "lse", 4));
+    SEQ_TRY(check_rows(&io.dq, a->dq, tq, g.heads, g.d, true, "dq"));
   }
-  if (total_k > 0) {
-    SEQ_TRY(check_tma_rows(&rk, g, k, k_stride_n, k_stride_h, total_k, g.kv_heads, "k"));
-    SEQ_TRY(check_tma_rows(&io.v, g, v, v_stride_n, v_stride_h, total_k, g.kv_heads, "v"));
-    SEQ_TRY(check_rows(&io.dk, dk, dk_stride_n, dk_stride_h, total_k, g.kv_heads, g.d, true, "dk"));
-    SEQ_TRY(check_rows(&io.dv, dv, dv_stride_n, dv_stride_h, total_k, g.kv_heads, g.d, true, "dv"));
+  if (tk > 0) {
+    SEQ_TRY(check_tma_rows(&rk, g, a->k, tk, g.kv_heads, "k"));
+    SEQ_TRY(check_tma_rows(&io.v, g, a->v, tk, g.kv_heads, "v"));
+    SEQ_TRY(check_rows(&io.dk, a->dk, tk, g.kv_heads, g.d, true, "dk"));
+    SEQ_TRY(check_rows(&io.dv, a->dv, tk, g.kv_heads, g.d, true, "dv"));
   }
-  SEQ_TRY(check_ptr(workspace, "workspace"));
-  if (ws_bytes < bsa::packed_bwd_workspace_bytes(g, total_q, n_seqs))
-    return fail(BSA_ERR_WORKSPACE, "workspace of %zu bytes; %zu are needed", ws_bytes,
-                bsa::packed_bwd_workspace_bytes(g, total_q, n_seqs));
+  SEQ_TRY(check_ptr(a->workspace, "workspace"));
+  if (a->ws_bytes < bsa::packed_bwd_workspace_bytes(g, tq, a->n_seqs))
+    return fail(BSA_ERR_WORKSPACE, "workspace of %zu bytes; %zu are needed", a->ws_bytes,
+                bsa::packed_bwd_workspace_bytes(g, tq, a->n_seqs));
   SEQ_TRY(check_status(dev_status));
   SEQ_TRY(bsa::require_device());
   CUtensorMap maps[4];
-  SEQ_TRY(rows_map(&maps[0], g, rq, total_q, g.heads));
-  SEQ_TRY(rows_map(&maps[1], g, rk, total_k, g.kv_heads));
-  SEQ_TRY(rows_map(&maps[2], g, io.v, total_k, g.kv_heads));
-  SEQ_TRY(rows_map(&maps[3], g, io.dout, total_q, g.heads));
+  SEQ_TRY(rows_map(&maps[0], g, rq, tq, g.heads));
+  SEQ_TRY(rows_map(&maps[1], g, rk, tk, g.kv_heads));
+  SEQ_TRY(rows_map(&maps[2], g, io.v, tk, g.kv_heads));
+  SEQ_TRY(rows_map(&maps[3], g, io.dout, tq, g.heads));
   SEQ_TRY(bsa::resolve_status(&dev_status));
-  io.cu_q = cu_q;
-  io.cu_k = cu_k;
-  io.n_seqs = n_seqs;
-  io.total_q = total_q;
-  io.total_k = total_k;
-  io.lse = lse;
+  io.cu_q = a->cu_q;
+  io.cu_k = a->cu_k;
+  io.n_seqs = int(a->n_seqs);
+  io.total_q = tq;
+  io.total_k = tk;
+  io.lse = a->lse;
   io.status = dev_status;
   io.stall = bsa::stall_enabled();
-  bsa::packed_bwd_workspace_split(g, &io, workspace);
+  bsa::packed_bwd_workspace_split(g, &io, a->workspace);
   return done(bsa::launch_packed_bwd(g, maps, io, static_cast<cudaStream_t>(stream)),
               "bsa_packed_attn_bwd launch");
+}
+
+bsa_status bsa_kv_append(const bsa_seq_problem* prob, const bsa_append_args* a,
+                         int32_t* dev_status, void* stream) {
+  SEQ_RANGE();
+  SeqGeo g;
+  SEQ_TRY(make_geo(prob, &g));
+  if (!a) return fail(BSA_ERR_INVALID_ARG, "args is NULL");
+  const int64_t n = a->n_tokens;
+  SEQ_TRY(check_counts(a->n_seqs, n, "n_tokens"));
+  if (n == 0 || a->n_seqs == 0) return BSA_OK;
+  bsa::AppendIO io{};
+  bsa::PagedCache c{};
+  SEQ_TRY(check_rows(&io.k, a->k, n, g.kv_heads, g.d, false, "k"));
+  SEQ_TRY(check_rows(&io.v, a->v, n, g.kv_heads, g.d, false, "v"));
+  SEQ_TRY(check_cache(&c, g, a->cache, a->n_seqs));
+  SEQ_TRY(check_ptr(a->cu_new, "cu_new", 4));
+  SEQ_TRY(check_ptr(a->seq_lens, "seq_lens", 4));
+  if (a->rope) {
+    SEQ_TRY(check_ptr(a->rope, "rope"));
+    if (a->rope_n < 1 || a->rope_n > INT32_MAX)
+      return fail(BSA_ERR_SHAPE, "rope_n must lie in 1..2^31-1");
+    if (a->rot_dim < 16 || a->rot_dim > g.d || a->rot_dim % 16)
+      return fail(BSA_ERR_SHAPE, "rot_dim %lld must be a multiple of 16 up to head_dim",
+                  (long long)a->rot_dim);
+    if (a->rope_rows) SEQ_TRY(check_ptr(a->rope_rows, "rope_rows", 4));
+  }
+  if (!a->q.data != !a->q_out.data)
+    return fail(BSA_ERR_INVALID_ARG, "give q and q_out, or neither");
+  if (a->q.data) {
+    SEQ_TRY(check_rows(&io.q, a->q, n, g.heads, g.d, false, "q"));
+    SEQ_TRY(check_rows(&io.q_out, a->q_out, n, g.heads, g.d, true, "q_out"));
+  }
+  if (a->k_out.data) SEQ_TRY(check_rows(&io.k_out, a->k_out, n, g.kv_heads, g.d, true, "k_out"));
+  SEQ_TRY(check_status(dev_status));
+  SEQ_TRY(bsa::require_device());
+  SEQ_TRY(bsa::resolve_status(&dev_status));
+  io.cu = a->cu_new;
+  io.lens = a->seq_lens;
+  io.rope = a->rope;
+  io.rope_rows = a->rope ? a->rope_rows : nullptr;
+  io.rope_n = int(a->rope_n);
+  io.rot = a->rope ? int(a->rot_dim) : 0;
+  io.interleaved = a->interleaved != 0;
+  io.n_seqs = int(a->n_seqs);
+  io.n_tokens = n;
+  io.status = dev_status;
+  return done(bsa::launch_kv_append(g, c, io, static_cast<cudaStream_t>(stream)),
+              "bsa_kv_append launch");
 }
 
 bsa_status bsa_query_decode_workspace(const bsa_seq_problem* prob, size_t* bytes) {
@@ -341,38 +324,33 @@ bsa_status bsa_query_decode_workspace(const bsa_seq_problem* prob, size_t* bytes
   return BSA_OK;
 }
 
-bsa_status bsa_paged_attn_decode(const bsa_seq_problem* prob, int32_t n_seqs, const void* q,
-                                 int64_t q_stride_n, int64_t q_stride_h, const void* k_cache,
-                                 const void* v_cache, int32_t n_pages, int32_t page_size,
-                                 int64_t stride_page, int64_t stride_token, int64_t stride_head,
-                                 const int32_t* block_table, int64_t table_stride,
-                                 int32_t table_width, const int32_t* seq_lens, void* o,
-                                 int64_t o_stride_n, int64_t o_stride_h, void* workspace,
-                                 size_t ws_bytes, int32_t* dev_status, void* stream) {
+bsa_status bsa_paged_attn_decode(const bsa_seq_problem* prob, const bsa_decode_args* a,
+                                 int32_t* dev_status, void* stream) {
   SEQ_RANGE();
   SeqGeo g;
   SEQ_TRY(make_geo(prob, &g));
-  SEQ_TRY(check_counts(n_seqs, n_seqs, "n_seqs"));
-  if (int64_t(n_seqs) * g.heads > INT32_MAX)
+  if (!a) return fail(BSA_ERR_INVALID_ARG, "args is NULL");
+  const int64_t n = a->n_seqs;
+  SEQ_TRY(check_counts(n, n, "n_seqs"));
+  if (n * g.heads > INT32_MAX)
     return fail(BSA_ERR_SHAPE, "n_seqs * heads must be <= 2^31-1");
-  if (n_seqs == 0) return BSA_OK;
+  if (n == 0) return BSA_OK;
   bsa::DecodeIO io{};
   bsa::PagedCache c{};
-  SEQ_TRY(check_rows(&io.q, q, q_stride_n, q_stride_h, n_seqs, g.heads, g.d, false, "q"));
-  SEQ_TRY(check_cache(&c, g, k_cache, v_cache, n_pages, page_size, stride_page, stride_token,
-                      stride_head, block_table, table_stride, table_width, n_seqs));
-  SEQ_TRY(check_ptr(seq_lens, "seq_lens", 4));
-  SEQ_TRY(check_rows(&io.o, o, o_stride_n, o_stride_h, n_seqs, g.heads, g.d, true, "o"));
-  SEQ_TRY(check_ptr(workspace, "workspace"));
-  if (ws_bytes < bsa::decode_workspace_bytes(g))
-    return fail(BSA_ERR_WORKSPACE, "workspace of %zu bytes; %zu are needed", ws_bytes,
+  SEQ_TRY(check_rows(&io.q, a->q, n, g.heads, g.d, false, "q"));
+  SEQ_TRY(check_cache(&c, g, a->cache, n));
+  SEQ_TRY(check_ptr(a->seq_lens, "seq_lens", 4));
+  SEQ_TRY(check_rows(&io.o, a->o, n, g.heads, g.d, true, "o"));
+  SEQ_TRY(check_ptr(a->workspace, "workspace"));
+  if (a->ws_bytes < bsa::decode_workspace_bytes(g))
+    return fail(BSA_ERR_WORKSPACE, "workspace of %zu bytes; %zu are needed", a->ws_bytes,
                 bsa::decode_workspace_bytes(g));
   SEQ_TRY(check_status(dev_status));
   SEQ_TRY(bsa::require_device());
   SEQ_TRY(bsa::resolve_status(&dev_status));
-  io.lens = seq_lens;
-  io.n_seqs = n_seqs;
-  io.workspace = workspace;
+  io.lens = a->seq_lens;
+  io.n_seqs = int(n);
+  io.workspace = a->workspace;
   io.status = dev_status;
   return done(bsa::launch_paged_decode(g, c, io, static_cast<cudaStream_t>(stream)),
               "bsa_paged_attn_decode launch");

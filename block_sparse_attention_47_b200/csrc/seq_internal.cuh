@@ -5,6 +5,7 @@
 
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "../../include/bsa_seq.h"
@@ -17,12 +18,26 @@ void clear_error();
 bsa_status cuda_error(cudaError_t e, const char* what);
 bsa_status require_device();                 // the current device is sm_100
 bsa_status resolve_status(int32_t** status);  // the caller's word or the library's
+int device_sms();                            // of the current device
 bool stall_enabled();                        // bsa_debug_stall_pv of this thread
 void range_push(const char* name);
 void range_pop();
 // a [rows, heads, d] 16-bit tensor as a 3-D map, box 64 columns x 1 head x box_rows
 bsa_status make_rows_map(CUtensorMap* m, const void* ptr, int64_t rows, int heads, int d,
                          int64_t stride_n, int64_t stride_h, int box_rows, bool fp16);
+
+// Opt a kernel in to its shared memory, once per device.
+template <typename K>
+inline cudaError_t allow_smem(K kern, int bytes, std::atomic<uint64_t>& seen) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (seen.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) seen.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 struct SeqGeo {
   int heads, kv_heads, group, d;

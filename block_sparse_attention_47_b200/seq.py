@@ -14,6 +14,7 @@ given, whatever device is current.
 """
 import ctypes
 import math
+import struct
 
 import torch
 
@@ -49,20 +50,20 @@ class SeqProblem(ctypes.Structure):
 
 _P, _I64, _I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
 _PROB = ctypes.POINTER(SeqProblem)
-_ROWS = [_P, _I64, _I64]
-_CACHE = [_P, _P, _I32, _I32, _I64, _I64, _I64, _P, _I64, _I32]
+# the argument structs travel as packed 8-byte fields: converting one pointer
+# costs a fraction of converting twenty to forty separate arguments
+_CALL = [_PROB, ctypes.c_char_p, _P, _P]
 _SIGS = {
-    "bsa_packed_attn_fwd": [_PROB, _I32, _I64, _I64, *_ROWS, *_ROWS, *_ROWS, _P, _P, *_ROWS, _P,
-                            _P, _P],
+    "bsa_packed_attn_fwd": _CALL,
     "bsa_query_packed_bwd_workspace": [_PROB, _I32, _I64, ctypes.POINTER(ctypes.c_size_t)],
-    "bsa_packed_attn_bwd": [_PROB, _I32, _I64, _I64, *_ROWS, *_ROWS, *_ROWS, *_ROWS, *_ROWS, _P,
-                            _P, _P, *_ROWS, *_ROWS, *_ROWS, _P, ctypes.c_size_t, _P, _P],
-    "bsa_kv_append": [_PROB, _I32, _I64, *_ROWS, *_ROWS, *_CACHE, _P, _P, _P, _I32, _I32, _I32, _P,
-                      *_ROWS, *_ROWS, *_ROWS, _P, _P],
+    "bsa_packed_attn_bwd": _CALL,
+    "bsa_kv_append": _CALL,
     "bsa_query_decode_workspace": [_PROB, ctypes.POINTER(ctypes.c_size_t)],
-    "bsa_paged_attn_decode": [_PROB, _I32, *_ROWS, *_CACHE, _P, *_ROWS, _P, ctypes.c_size_t, _P,
-                              _P],
+    "bsa_paged_attn_decode": _CALL,
 }
+_PACKED = struct.Struct("=32q")   # bsa_packed_args
+_APPEND = struct.Struct("=34q")   # bsa_append_args
+_DECODE = struct.Struct("=20q")   # bsa_decode_args
 _FNS = {}
 
 
@@ -76,16 +77,14 @@ def _fn(name):
 
 
 # ---- argument checks ----------------------------------------------------------
-_NO_ROWS = (None, 0, 0)
+_NO_ROWS = (0, 0, 0)
 
 
-def _rows(prob, t, rows, heads, dev, name):
+def _rows(t, shape, dtype, dev, name):
     """(pointer, row stride, head stride) of a [rows, heads, head_dim] tensor."""
-    if t.device != dev or t.dtype != prob.torch_dtype:
-        raise ValueError("%s must be %s on %s" % (name, prob.torch_dtype, dev))
-    if t.dim() != 3 or t.shape[0] != rows or t.shape[1] != heads or t.shape[2] != prob.head_dim:
-        raise ValueError("%s must be [%d, %d, %d], not %s" % (name, rows, heads, prob.head_dim,
-                                                              tuple(t.shape)))
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError("%s must be %s %s on cuda:%d, not %s %s on %s"
+                         % (name, dtype, list(shape), dev, t.dtype, list(t.shape), t.device))
     sn, sh, sd = t.stride()
     if sd != 1:
         raise ValueError("%s: head_dim must be contiguous" % name)
@@ -94,69 +93,88 @@ def _rows(prob, t, rows, heads, dev, name):
 
 def _ints(t, n, dev, name):
     """Pointer of a contiguous int32 vector of n entries."""
-    if t.device != dev or t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or \
+    if t.dtype is not torch.int32 or t.shape != (n,) or t.get_device() != dev or \
             not t.is_contiguous():
-        raise ValueError("%s must be a contiguous int32 vector of %d on %s" % (name, n, dev))
+        raise ValueError("%s must be a contiguous int32 vector of %d on cuda:%d" % (name, n, dev))
     return t.data_ptr()
 
 
-def _cache_args(prob, k_cache, v_cache, table, n_seqs, dev):
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or \
-            k_cache.stride() != v_cache.stride() or k_cache.shape[2] != prob.kv_heads or \
-            k_cache.shape[3] != prob.head_dim or k_cache.stride(3) != 1:
+def _cache(k_cache, v_cache, table, kv_heads, d, dtype, n_seqs, dev):
+    shape, strides = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.stride() != strides or \
+            shape[2] != kv_heads or shape[3] != d or strides[3] != 1:
         raise ValueError("k_cache and v_cache are [n_pages, page_size, kv_heads, head_dim] with "
                          "the same strides and head_dim contiguous")
-    if k_cache.device != dev or v_cache.device != dev or k_cache.dtype != prob.torch_dtype or \
-            v_cache.dtype != prob.torch_dtype:
-        raise ValueError("k_cache and v_cache must be %s on %s" % (prob.torch_dtype, dev))
-    if table.device != dev or table.dtype != torch.int32 or table.dim() != 2 or \
-            table.shape[0] != n_seqs or (table.shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError("block_table must be int32 [%d, width] on %s with contiguous rows"
+    if k_cache.dtype is not dtype or v_cache.dtype is not dtype or \
+            k_cache.get_device() != dev or v_cache.get_device() != dev:
+        raise ValueError("k_cache and v_cache must be %s on cuda:%d" % (dtype, dev))
+    wide = table.shape
+    if table.dtype is not torch.int32 or len(wide) != 2 or wide[0] != n_seqs or \
+            table.get_device() != dev or (wide[1] > 1 and table.stride(1) != 1):
+        raise ValueError("block_table must be int32 [%d, width] on cuda:%d with contiguous rows"
                          % (n_seqs, dev))
-    sp, st, sh, _ = k_cache.stride()
-    return (k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[0], k_cache.shape[1], sp, st, sh,
-            table.data_ptr(), table.stride(0), table.shape[1])
+    return (k_cache.data_ptr(), v_cache.data_ptr(), strides[0], strides[1], strides[2], shape[0],
+            shape[1], table.data_ptr(), table.stride(0), wide[1])
 
 
 def _device(t, name):
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    return t.device
+    return t.get_device()
+
+
+def _shape3(t, name):
+    if t.dim() != 3:
+        raise ValueError("%s must be [rows, heads, head_dim]" % name)
+    return t.shape[0]
+
+
+def _offsets(t, name):
+    if t.dim() != 1 or t.shape[0] < 1:
+        raise ValueError("%s holds n_seqs + 1 offsets" % name)
+    return t.shape[0] - 1
 
 
 def _status_ptr(t, dev):
     if t is None:
         return None
-    if t.device != dev or t.dtype != torch.int32 or t.numel() < 1:
-        raise ValueError("dev_status must be an int32 tensor on %s" % dev)
+    if t.get_device() != dev or t.dtype is not torch.int32 or t.numel() < 1:
+        raise ValueError("dev_status must be an int32 tensor on cuda:%d" % dev)
     return t.data_ptr()
-
-
-def _call(name, dev, stream, *args):
-    """The entry point on `dev` and `stream` (its current one by default)."""
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device != dev:
-        raise ValueError("stream belongs to %s, the tensors to %s" % (stream.device, dev))
-    f = _fn(name)
-    if torch.cuda.current_device() == dev.index:
-        _check(f(*args, stream.cuda_stream))
-    else:
-        with torch.cuda.device(dev):
-            _check(f(*args, stream.cuda_stream))
 
 
 def _workspace(t, dev):
-    if t.device != dev or not t.is_contiguous():
-        raise ValueError("workspace must be contiguous on %s" % dev)
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("workspace must be contiguous on cuda:%d" % dev)
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-def _lse_ptr(prob, t, rows, dev):
-    if t.device != dev or t.dtype != torch.float32 or tuple(t.shape) != (prob.heads, rows) or \
+def _lse_ptr(heads, t, rows, dev):
+    if t.dtype is not torch.float32 or t.shape != (heads, rows) or t.get_device() != dev or \
             not t.is_contiguous():
-        raise ValueError("lse must be a contiguous float32 [%d, %d] on %s" % (prob.heads, rows, dev))
+        raise ValueError("lse must be a contiguous float32 [%d, %d] on cuda:%d" % (heads, rows, dev))
     return t.data_ptr()
+
+
+def _call(name, dev, stream, prob, args, dev_status):
+    """The entry point on device `dev` and `stream` (its current one by default)."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device_index != dev:
+        raise ValueError("stream belongs to cuda:%d, the tensors to cuda:%d"
+                         % (stream.device_index, dev))
+    f, st = _fn(name), _status_ptr(dev_status, dev)
+    if torch.cuda.current_device() == dev:
+        _check(f(prob, args, st, stream.cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(f(prob, args, st, stream.cuda_stream))
+
+
+def _query(name, *args):
+    n = ctypes.c_size_t(0)
+    _check(_fn(name)(*args, ctypes.byref(n)))
+    return int(n.value)
 
 
 # ---- entry points ----------------------------------------------------------------
@@ -166,20 +184,20 @@ def packed_attn_fwd(prob, q, k, v, cu_q, cu_k, out, lse=None, dev_status=None, s
     and cu_k [n_seqs + 1] row offsets.  prob.causal aligns the last query
     with the last key.  lse, float32 [heads, total_q], receives the rows'
     log-sum-exp (exp2 domain) for packed_attn_bwd."""
-    dev = _device(q, "q")
-    tq, tk, n_seqs = q.shape[0], k.shape[0], cu_q.shape[0] - 1
-    _call("bsa_packed_attn_fwd", dev, stream, ctypes.byref(prob), n_seqs, tq, tk,
-          *_rows(prob, q, tq, prob.heads, dev, "q"), *_rows(prob, k, tk, prob.kv_heads, dev, "k"),
-          *_rows(prob, v, tk, prob.kv_heads, dev, "v"), _ints(cu_q, n_seqs + 1, dev, "cu_q"),
-          _ints(cu_k, n_seqs + 1, dev, "cu_k"), *_rows(prob, out, tq, prob.heads, dev, "out"),
-          None if lse is None else _lse_ptr(prob, lse, tq, dev), _status_ptr(dev_status, dev))
+    dev, dt, H, d = _device(q, "q"), prob.torch_dtype, prob.heads, prob.head_dim
+    tq, tk, n = _shape3(q, "q"), _shape3(k, "k"), _offsets(cu_q, "cu_q")
+    qs, ks = (tq, H, d), (tk, prob.kv_heads, d)
+    args = _PACKED.pack(
+        n, tq, tk, *_rows(q, qs, dt, dev, "q"), *_rows(k, ks, dt, dev, "k"),
+        *_rows(v, ks, dt, dev, "v"), *_rows(out, qs, dt, dev, "out"),
+        _ints(cu_q, n + 1, dev, "cu_q"), _ints(cu_k, n + 1, dev, "cu_k"),
+        0 if lse is None else _lse_ptr(H, lse, tq, dev), *_NO_ROWS, *_NO_ROWS, *_NO_ROWS,
+        *_NO_ROWS, 0, 0)
+    _call("bsa_packed_attn_fwd", dev, stream, prob, args, dev_status)
 
 
 def packed_bwd_workspace_bytes(prob, total_q, n_seqs):
-    n = ctypes.c_size_t(0)
-    _check(_fn("bsa_query_packed_bwd_workspace")(ctypes.byref(prob), n_seqs, total_q,
-                                                 ctypes.byref(n)))
-    return int(n.value)
+    return _query("bsa_query_packed_bwd_workspace", prob, n_seqs, total_q)
 
 
 def packed_attn_bwd(prob, q, k, v, out, dout, lse, cu_q, cu_k, dq, dk, dv, workspace,
@@ -188,17 +206,17 @@ def packed_attn_bwd(prob, q, k, v, out, dout, lse, cu_q, cu_k, dq, dk, dv, works
     gradient dout of out (bsa_packed_attn_bwd).  workspace: at least
     packed_bwd_workspace_bytes(prob, total_q, n_seqs), one per call that may
     overlap."""
-    dev = _device(q, "q")
-    tq, tk, n_seqs = q.shape[0], k.shape[0], cu_q.shape[0] - 1
-    H, K = prob.heads, prob.kv_heads
-    _call("bsa_packed_attn_bwd", dev, stream, ctypes.byref(prob), n_seqs, tq, tk,
-          *_rows(prob, q, tq, H, dev, "q"), *_rows(prob, k, tk, K, dev, "k"),
-          *_rows(prob, v, tk, K, dev, "v"), *_rows(prob, out, tq, H, dev, "out"),
-          *_rows(prob, dout, tq, H, dev, "dout"), _lse_ptr(prob, lse, tq, dev),
-          _ints(cu_q, n_seqs + 1, dev, "cu_q"), _ints(cu_k, n_seqs + 1, dev, "cu_k"),
-          *_rows(prob, dq, tq, H, dev, "dq"), *_rows(prob, dk, tk, K, dev, "dk"),
-          *_rows(prob, dv, tk, K, dev, "dv"), *_workspace(workspace, dev),
-          _status_ptr(dev_status, dev))
+    dev, dt, H, d = _device(q, "q"), prob.torch_dtype, prob.heads, prob.head_dim
+    tq, tk, n = _shape3(q, "q"), _shape3(k, "k"), _offsets(cu_q, "cu_q")
+    qs, ks = (tq, H, d), (tk, prob.kv_heads, d)
+    args = _PACKED.pack(
+        n, tq, tk, *_rows(q, qs, dt, dev, "q"), *_rows(k, ks, dt, dev, "k"),
+        *_rows(v, ks, dt, dev, "v"), *_rows(out, qs, dt, dev, "out"),
+        _ints(cu_q, n + 1, dev, "cu_q"), _ints(cu_k, n + 1, dev, "cu_k"),
+        _lse_ptr(H, lse, tq, dev), *_rows(dout, qs, dt, dev, "dout"),
+        *_rows(dq, qs, dt, dev, "dq"), *_rows(dk, ks, dt, dev, "dk"),
+        *_rows(dv, ks, dt, dev, "dv"), *_workspace(workspace, dev))
+    _call("bsa_packed_attn_bwd", dev, stream, prob, args, dev_status)
 
 
 def kv_append(prob, k, v, k_cache, v_cache, block_table, cu_new, seq_lens, rope=None,
@@ -210,34 +228,32 @@ def kv_append(prob, k, v, k_cache, v_cache, block_table, cu_new, seq_lens, rope=
     sequences' lengths including them.  rope is a float32 [rows, rot_dim]
     table of cos | sin halves, read at the token's position or at
     rope_rows[token]."""
-    dev = _device(k, "k")
-    n, n_seqs = k.shape[0], seq_lens.shape[0]
-    rope_ptr, rope_n, rot, rr = None, 0, 0, None
+    dev, dt, K, d = _device(k, "k"), prob.torch_dtype, prob.kv_heads, prob.head_dim
+    n, n_seqs = _shape3(k, "k"), _offsets(cu_new, "cu_new")
+    rope_ptr, rope_n, rot, rr = 0, 0, 0, 0
     if rope is not None:
-        if rope.device != dev or rope.dtype != torch.float32 or rope.dim() != 2 or \
+        if rope.dtype is not torch.float32 or rope.dim() != 2 or rope.get_device() != dev or \
                 not rope.is_contiguous():
-            raise ValueError("rope must be a contiguous float32 [rows, rot_dim] on %s" % dev)
-        rope_ptr, rope_n, rot = rope.data_ptr(), rope.shape[0], rope.shape[1]
+            raise ValueError("rope must be a contiguous float32 [rows, rot_dim] on cuda:%d" % dev)
+        rope_ptr, (rope_n, rot) = rope.data_ptr(), rope.shape
         if rope_rows is not None:
             rr = _ints(rope_rows, n, dev, "rope_rows")
     if (q is None) != (q_out is None):
         raise ValueError("give q and q_out, or neither")
-    K = prob.kv_heads
-    _call("bsa_kv_append", dev, stream, ctypes.byref(prob), n_seqs, n,
-          *_rows(prob, k, n, K, dev, "k"), *_rows(prob, v, n, K, dev, "v"),
-          *_cache_args(prob, k_cache, v_cache, block_table, n_seqs, dev),
-          _ints(cu_new, n_seqs + 1, dev, "cu_new"), _ints(seq_lens, n_seqs, dev, "seq_lens"),
-          rope_ptr, rope_n, rot, 1 if interleaved else 0, rr,
-          *(_NO_ROWS if q is None else _rows(prob, q, n, prob.heads, dev, "q")),
-          *(_NO_ROWS if q is None else _rows(prob, q_out, n, prob.heads, dev, "q_out")),
-          *(_NO_ROWS if k_out is None else _rows(prob, k_out, n, K, dev, "k_out")),
-          _status_ptr(dev_status, dev))
+    ks, qs = (n, K, d), (n, prob.heads, d)
+    args = _APPEND.pack(
+        n_seqs, n, *_rows(k, ks, dt, dev, "k"), *_rows(v, ks, dt, dev, "v"),
+        *_cache(k_cache, v_cache, block_table, K, d, dt, n_seqs, dev),
+        _ints(cu_new, n_seqs + 1, dev, "cu_new"), _ints(seq_lens, n_seqs, dev, "seq_lens"),
+        rope_ptr, rope_n, rot, 1 if interleaved else 0, rr,
+        *(_NO_ROWS if q is None else _rows(q, qs, dt, dev, "q")),
+        *(_NO_ROWS if q is None else _rows(q_out, qs, dt, dev, "q_out")),
+        *(_NO_ROWS if k_out is None else _rows(k_out, ks, dt, dev, "k_out")))
+    _call("bsa_kv_append", dev, stream, prob, args, dev_status)
 
 
 def decode_workspace_bytes(prob):
-    n = ctypes.c_size_t(0)
-    _check(_fn("bsa_query_decode_workspace")(ctypes.byref(prob), ctypes.byref(n)))
-    return int(n.value)
+    return _query("bsa_query_decode_workspace", prob)
 
 
 def paged_attn_decode(prob, q, k_cache, v_cache, block_table, seq_lens, out, workspace,
@@ -245,14 +261,16 @@ def paged_attn_decode(prob, q, k_cache, v_cache, block_table, seq_lens, out, wor
     """Attention of one new token per sequence, q [n_seqs, heads, head_dim],
     over the paged cache (bsa_paged_attn_decode).  workspace: at least
     decode_workspace_bytes(prob), one per call that may overlap."""
-    dev = _device(q, "q")
-    n = q.shape[0]
-    _call("bsa_paged_attn_decode", dev, stream, ctypes.byref(prob), n,
-          *_rows(prob, q, n, prob.heads, dev, "q"),
-          *_cache_args(prob, k_cache, v_cache, block_table, n, dev),
-          _ints(seq_lens, n, dev, "seq_lens"), *_rows(prob, out, n, prob.heads, dev, "out"),
-          *_workspace(workspace, dev), _status_ptr(dev_status, dev))
+    dev, dt, d = _device(q, "q"), prob.torch_dtype, prob.head_dim
+    n = _shape3(q, "q")
+    qs = (n, prob.heads, d)
+    args = _DECODE.pack(
+        n, *_rows(q, qs, dt, dev, "q"),
+        *_cache(k_cache, v_cache, block_table, prob.kv_heads, d, dt, n, dev),
+        _ints(seq_lens, n, dev, "seq_lens"), *_rows(out, qs, dt, dev, "out"),
+        *_workspace(workspace, dev))
+    _call("bsa_paged_attn_decode", dev, stream, prob, args, dev_status)
 
 
-__all__ = ["SeqProblem", "packed_attn_fwd", "packed_bwd_workspace_bytes",
-           "packed_attn_bwd", "kv_append", "decode_workspace_bytes", "paged_attn_decode"]
+__all__ = ["SeqProblem", "packed_attn_fwd", "packed_bwd_workspace_bytes", "packed_attn_bwd",
+           "kv_append", "decode_workspace_bytes", "paged_attn_decode"]

@@ -59,6 +59,53 @@ typedef struct bsa_seq_problem {
   float softmax_scale;  /* finite and > 0 */
 } bsa_seq_problem;
 
+/* A [rows, heads, head_dim] tensor: its data and element strides. */
+typedef struct bsa_rows {
+  void* data;
+  int64_t stride_n, stride_h;
+} bsa_rows;
+
+/* A paged cache and the pages of each sequence. */
+typedef struct bsa_paged_cache {
+  void *k, *v;
+  int64_t stride_page, stride_token, stride_head;
+  int64_t n_pages, page_size;
+  const int32_t* block_table;
+  int64_t table_stride, table_width;
+} bsa_paged_cache;
+
+/* Arguments of the packed calls; the forward reads q .. lse. */
+typedef struct bsa_packed_args {
+  int64_t n_seqs, total_q, total_k;
+  bsa_rows q, k, v, o;
+  const int32_t *cu_q, *cu_k;
+  float* lse;
+  bsa_rows dout, dq, dk, dv;
+  void* workspace;
+  size_t ws_bytes;
+} bsa_packed_args;
+
+typedef struct bsa_append_args {
+  int64_t n_seqs, n_tokens;
+  bsa_rows k, v;
+  bsa_paged_cache cache;
+  const int32_t *cu_new, *seq_lens;
+  const float* rope;
+  int64_t rope_n, rot_dim, interleaved;
+  const int32_t* rope_rows;
+  bsa_rows q, q_out, k_out;
+} bsa_append_args;
+
+typedef struct bsa_decode_args {
+  int64_t n_seqs;
+  bsa_rows q;
+  bsa_paged_cache cache;
+  const int32_t* seq_lens;
+  bsa_rows o;
+  void* workspace;
+  size_t ws_bytes;
+} bsa_decode_args;
+
 /* Attention over packed sequences: row i of sequence b (Lq queries, Lk keys)
  * sees keys j < lim,
  *   causal      lim = min(Lk, max(0, i + 1 + Lk - Lq)): the last query sees
@@ -74,12 +121,7 @@ typedef struct bsa_seq_problem {
  *               (-inf for a row that sees nothing), for the backward
  * Scores, statistics and outputs accumulate in fp32; the probabilities are
  * rounded to the element type for their product with V. */
-bsa_status bsa_packed_attn_fwd(const bsa_seq_problem* prob, int32_t n_seqs, int64_t total_q,
-                               int64_t total_k, const void* q, int64_t q_stride_n,
-                               int64_t q_stride_h, const void* k, int64_t k_stride_n,
-                               int64_t k_stride_h, const void* v, int64_t v_stride_n,
-                               int64_t v_stride_h, const int32_t* cu_q, const int32_t* cu_k,
-                               void* o, int64_t o_stride_n, int64_t o_stride_h, float* lse,
+bsa_status bsa_packed_attn_fwd(const bsa_seq_problem* prob, const bsa_packed_args* args,
                                int32_t* dev_status, void* stream);
 
 /* Bytes of bsa_packed_attn_bwd's workspace (row statistics).  Host only. */
@@ -103,17 +145,7 @@ bsa_status bsa_query_packed_bwd_workspace(const bsa_seq_problem* prob, int32_t n
  *                         bsa_query_packed_bwd_workspace; holds nothing
  *                         between calls.  Calls that overlap on the GPU need
  *                         one each. */
-bsa_status bsa_packed_attn_bwd(const bsa_seq_problem* prob, int32_t n_seqs, int64_t total_q,
-                               int64_t total_k, const void* q, int64_t q_stride_n,
-                               int64_t q_stride_h, const void* k, int64_t k_stride_n,
-                               int64_t k_stride_h, const void* v, int64_t v_stride_n,
-                               int64_t v_stride_h, const void* o, int64_t o_stride_n,
-                               int64_t o_stride_h, const void* dout, int64_t do_stride_n,
-                               int64_t do_stride_h, const float* lse, const int32_t* cu_q,
-                               const int32_t* cu_k, void* dq, int64_t dq_stride_n,
-                               int64_t dq_stride_h, void* dk, int64_t dk_stride_n,
-                               int64_t dk_stride_h, void* dv, int64_t dv_stride_n,
-                               int64_t dv_stride_h, void* workspace, size_t ws_bytes,
+bsa_status bsa_packed_attn_bwd(const bsa_seq_problem* prob, const bsa_packed_args* args,
                                int32_t* dev_status, void* stream);
 
 /* Append new keys and values to a paged cache, rotating keys (and queries)
@@ -138,18 +170,8 @@ bsa_status bsa_packed_attn_bwd(const bsa_seq_problem* prob, int32_t n_seqs, int6
  * reported as BSA_ERR_INVALID_ARG through the status word and none of its
  * outputs are written.  Two tokens must not share a cache slot (sequences
  * may share pages they do not write). */
-bsa_status bsa_kv_append(const bsa_seq_problem* prob, int32_t n_seqs, int64_t n_tokens,
-                         const void* k, int64_t k_stride_n, int64_t k_stride_h, const void* v,
-                         int64_t v_stride_n, int64_t v_stride_h, void* k_cache, void* v_cache,
-                         int32_t n_pages, int32_t page_size, int64_t stride_page,
-                         int64_t stride_token, int64_t stride_head, const int32_t* block_table,
-                         int64_t table_stride, int32_t table_width, const int32_t* cu_new,
-                         const int32_t* seq_lens, const float* rope, int32_t rope_n,
-                         int32_t rot_dim, int32_t interleaved, const int32_t* rope_rows,
-                         const void* q, int64_t q_stride_n, int64_t q_stride_h, void* q_out,
-                         int64_t qo_stride_n, int64_t qo_stride_h, void* k_out,
-                         int64_t ko_stride_n, int64_t ko_stride_h, int32_t* dev_status,
-                         void* stream);
+bsa_status bsa_kv_append(const bsa_seq_problem* prob, const bsa_append_args* args,
+                         int32_t* dev_status, void* stream);
 
 /* Bytes of bsa_paged_attn_decode's workspace; the same for every batch.
  * Host only. */
@@ -169,14 +191,8 @@ bsa_status bsa_query_decode_workspace(const bsa_seq_problem* prob, size_t* bytes
  * cache are reported as BSA_ERR_INVALID_ARG through the status word; the
  * length is clamped, such a page's keys are read as zeros, and the
  * sequence's output is then meaningless. */
-bsa_status bsa_paged_attn_decode(const bsa_seq_problem* prob, int32_t n_seqs, const void* q,
-                                 int64_t q_stride_n, int64_t q_stride_h, const void* k_cache,
-                                 const void* v_cache, int32_t n_pages, int32_t page_size,
-                                 int64_t stride_page, int64_t stride_token, int64_t stride_head,
-                                 const int32_t* block_table, int64_t table_stride,
-                                 int32_t table_width, const int32_t* seq_lens, void* o,
-                                 int64_t o_stride_n, int64_t o_stride_h, void* workspace,
-                                 size_t ws_bytes, int32_t* dev_status, void* stream);
+bsa_status bsa_paged_attn_decode(const bsa_seq_problem* prob, const bsa_decode_args* args,
+                                 int32_t* dev_status, void* stream);
 
 #ifdef __cplusplus
 }

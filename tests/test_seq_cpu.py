@@ -38,8 +38,10 @@ def test_header_is_strict_c99(tmp_path):
     src = tmp_path / "client.c"
     src.write_text('#include "bsa_seq.h"\n'
                    "int main(void) { bsa_seq_problem p = {8, 2, 96, BSA_DTYPE_FP16, 1, 0.1f};\n"
+                   "  if (sizeof(bsa_packed_args) != %d || sizeof(bsa_append_args) != %d ||\n"
+                   "      sizeof(bsa_decode_args) != %d) return 2;\n"
                    "  size_t n; return bsa_query_decode_workspace(&p, &n) == BSA_ERR_UNSUPPORTED "
-                   "? 0 : 1; }\n")
+                   "? 0 : 1; }\n" % (seq._PACKED.size, seq._APPEND.size, seq._DECODE.size))
     exe = tmp_path / "client"
     libdir = os.path.dirname(bsa.LIB_PATH)
     cc = subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-pedantic", "-Werror",
@@ -74,13 +76,20 @@ def test_dtype_of_the_problem():
     assert prob(dtype=torch.float16).torch_dtype == torch.float16
 
 
+def call(name, layout, a):
+    """The entry point with the dict's values as its argument struct."""
+    p, st, stream = a.pop("prob"), a.pop("status"), a.pop("stream")
+    return seq._fn(name)(p, layout.pack(*(0 if x is None else x for x in a.values())), st, stream)
+
+
 def decode_args(**kw):
     """Arguments of bsa_paged_attn_decode that pass every host check."""
-    a = dict(prob=ctypes.byref(prob()), n_seqs=2, q=16, q_sn=512, q_sh=64, k=16, v=16, n_pages=4,
-             page_size=16, sp=2048, st=128, sh=64, table=16, table_stride=4, table_width=4, lens=16,
+    a = dict(prob=ctypes.byref(prob()), n_seqs=2, q=16, q_sn=512, q_sh=64, k=16, v=16,
+             sp=2048, st=128, sh=64, n_pages=4, page_size=16, table=16, table_stride=4, table_width=4,
+             lens=16,
              o=16, o_sn=512, o_sh=64, ws=16, ws_bytes=1 << 30, status=None, stream=None)
     a.update(kw)
-    return list(a.values())
+    return a
 
 
 DECODE_BAD = [
@@ -101,25 +110,25 @@ DECODE_BAD = [
 
 @pytest.mark.parametrize("kw,status,word", DECODE_BAD, ids=[str(k) for k, _, _ in DECODE_BAD])
 def test_decode_refuses(kw, status, word):
-    rc = seq._fn("bsa_paged_attn_decode")(*decode_args(**kw))
+    rc = call("bsa_paged_attn_decode", seq._DECODE, decode_args(**kw))
     assert rc == status, (rc, bsa.lib().bsa_last_error())
     assert word in bsa.lib().bsa_last_error()
 
 
 def test_empty_batches_need_no_device():
-    assert seq._fn("bsa_packed_attn_fwd")(*fwd_args(tq=0)) == 0
-    assert seq._fn("bsa_paged_attn_decode")(*decode_args(n_seqs=0)) == 0
-    assert seq._fn("bsa_kv_append")(*append_args(n=0)) == 0
+    assert call("bsa_packed_attn_fwd", seq._PACKED, fwd_args(tq=0)) == 0
+    assert call("bsa_paged_attn_decode", seq._DECODE, decode_args(n_seqs=0)) == 0
+    assert call("bsa_kv_append", seq._APPEND, append_args(n=0)) == 0
 
 
 def append_args(**kw):
     a = dict(prob=ctypes.byref(prob()), n_seqs=2, n=5, k=16, k_sn=128, k_sh=64, v=16, v_sn=128,
-             v_sh=64, kc=16, vc=16, n_pages=4, page_size=16, sp=2048, st=128, sh=64, table=16,
+             v_sh=64, kc=16, vc=16, sp=2048, st=128, sh=64, n_pages=4, page_size=16, table=16,
              table_stride=4, table_width=4, cu=16, lens=16, rope=16, rope_n=100, rot=64,
              interleaved=0, rope_rows=None, q=16, q_sn=512, q_sh=64, qo=16, qo_sn=512, qo_sh=64,
              ko=16, ko_sn=128, ko_sh=64, status=None, stream=None)
     a.update(kw)
-    return list(a.values())
+    return a
 
 
 APPEND_BAD = [
@@ -139,17 +148,17 @@ APPEND_BAD = [
 
 @pytest.mark.parametrize("kw,status,word", APPEND_BAD, ids=[str(k) for k, _, _ in APPEND_BAD])
 def test_append_refuses(kw, status, word):
-    rc = seq._fn("bsa_kv_append")(*append_args(**kw))
+    rc = call("bsa_kv_append", seq._APPEND, append_args(**kw))
     assert rc == status, (rc, bsa.lib().bsa_last_error())
     assert word in bsa.lib().bsa_last_error()
 
 
 def fwd_args(**kw):
     a = dict(prob=ctypes.byref(prob()), n_seqs=2, tq=100, tk=100, q=16, q_sn=512, q_sh=64, k=16,
-             k_sn=128, k_sh=64, v=16, v_sn=128, v_sh=64, cu_q=16, cu_k=16, o=16, o_sn=512, o_sh=64,
-             lse=None, status=None, stream=None)
+             k_sn=128, k_sh=64, v=16, v_sn=128, v_sh=64, o=16, o_sn=512, o_sh=64, cu_q=16, cu_k=16,
+             lse=None, **{"rest%d" % i: 0 for i in range(14)}, status=None, stream=None)
     a.update(kw)
-    return list(a.values())
+    return a
 
 
 FWD_BAD = [
@@ -169,7 +178,7 @@ def test_packed_fwd_refuses(kw, status, word):
     kw = dict(kw)
     if kw.get("prob") == "wide":
         kw["prob"] = ctypes.byref(prob(heads=4096, kv_heads=2))
-    rc = seq._fn("bsa_packed_attn_fwd")(*fwd_args(**kw))
+    rc = call("bsa_packed_attn_fwd", seq._PACKED, fwd_args(**kw))
     assert rc == status, (rc, bsa.lib().bsa_last_error())
     assert word in bsa.lib().bsa_last_error()
 
@@ -206,11 +215,11 @@ def test_gradient_oracle_agrees_with_differences(lq, lk, causal):
 
 def bwd_args(**kw):
     a = dict(prob=ctypes.byref(prob()), n_seqs=2, tq=100, tk=100, q=16, q_sn=512, q_sh=64, k=16,
-             k_sn=128, k_sh=64, v=16, v_sn=128, v_sh=64, o=16, o_sn=512, o_sh=64, do=16, do_sn=512,
-             do_sh=64, lse=16, cu_q=16, cu_k=16, dq=16, dq_sn=512, dq_sh=64, dk=16, dk_sn=128,
+             k_sn=128, k_sh=64, v=16, v_sn=128, v_sh=64, o=16, o_sn=512, o_sh=64, cu_q=16,
+             cu_k=16, lse=16, do=16, do_sn=512, do_sh=64, dq=16, dq_sn=512, dq_sh=64, dk=16, dk_sn=128,
              dk_sh=64, dv=16, dv_sn=128, dv_sh=64, ws=16, ws_bytes=1 << 30, status=None, stream=None)
     a.update(kw)
-    return list(a.values())
+    return a
 
 
 BWD_BAD = [
@@ -228,13 +237,19 @@ BWD_BAD = [
 
 @pytest.mark.parametrize("kw,status,word", BWD_BAD, ids=[str(k) for k, _, _ in BWD_BAD])
 def test_packed_bwd_refuses(kw, status, word):
-    rc = seq._fn("bsa_packed_attn_bwd")(*bwd_args(**kw))
+    rc = call("bsa_packed_attn_bwd", seq._PACKED, bwd_args(**kw))
     assert rc == status, (rc, bsa.lib().bsa_last_error())
     assert word in bsa.lib().bsa_last_error()
+
+
+def test_args_are_required():
+    for n in ("bsa_packed_attn_fwd", "bsa_packed_attn_bwd", "bsa_kv_append", "bsa_paged_attn_decode"):
+        assert seq._fn(n)(ctypes.byref(prob()), None, None, None) == INVALID
+        assert b"args" in bsa.lib().bsa_last_error()
 
 
 def test_bwd_workspace():
     """Two floats per head and row of every 128-row tile there can be."""
     for tq, n in ((0, 0), (1, 1), (1000, 3), (127, 127)):
         assert bsa.packed_bwd_workspace_bytes(prob(), tq, n) == 4 * (2 * 8 * 128 * (tq // 128 + n + 1) + 2 * 2)
-    assert seq._fn("bsa_packed_attn_bwd")(*bwd_args(tq=0, tk=0)) == 0
+    assert call("bsa_packed_attn_bwd", seq._PACKED, bwd_args(tq=0, tk=0)) == 0
