@@ -341,11 +341,12 @@ bsa_status make_rows_map(CUtensorMap* m, const void* ptr, int64_t rows, int head
                          int64_t stride_n, int64_t stride_h, int box_rows, bool fp16) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return fail(BSA_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-  cuuint64_t dims[3] = {cuuint64_t(d), cuuint64_t(heads), cuuint64_t(rows)};
-  cuuint64_t strides[2] = {cuuint64_t(stride_h) * 2, cuuint64_t(stride_n) * 2};
-  cuuint32_t box[3] = {64, 1, cuuint32_t(box_rows)};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = fn(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+  // 64 columns, rows, column box, head: a box lands as [column box][row][64]
+  cuuint64_t dims[4] = {64, cuuint64_t(rows), cuuint64_t(d / 64), cuuint64_t(heads)};
+  cuuint64_t strides[3] = {cuuint64_t(stride_n) * 2, 128, cuuint64_t(stride_h) * 2};
+  cuuint32_t box[4] = {64, cuuint32_t(box_rows), cuuint32_t(d / 64), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
                   const_cast<void*>(ptr), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);

@@ -38,7 +38,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMinShare = 4;  // key steps a CTA of a cluster takes at least
 #ifndef KSPLIT
-#define KSPLIT 640
+#define KSPLIT 300
 #endif
 constexpr int kSplitCtas = KSPLIT;
 
@@ -156,13 +156,34 @@ __global__ void __launch_bounds__(384, 1)
   auto load_tile = [&](int i) {  // K (even) and V (odd) tiles in walk order
     const uint32_t bar = full + 8 * (i % RING);
     mbar_arrive_expect_tx(bar, C::TILE);
-    for (int bx = 0; bx < C::KB; ++bx)
-      tma_load_3d(slot(i) + bx * C::BOX, (i & 1) ? &mv : &mk, bar, 64 * bx, kvh,
-                  w.k0 + (w.kb + (i >> 1)) * 128);
+    tma_load_rows(slot(i), (i & 1) ? &mv : &mk, bar, w.k0 + (w.kb + (i >> 1)) * 128, kvh);
   };
 
   int loaded = 0;
   if (warp == 8) {
+    const Tile t =
+        find_tile<kWalkQ>(io.cu_q, io.total_q, io.cu_k, io.total_k, io.n_seqs, g.causal,
+                          HEADS ? 128 : 256, unit / uint32_t(n_hp), lane, io.status);
+    w.any = t.any;
+    w.q0 = t.a.start, w.Lq = t.a.len, w.k0 = t.b.start, w.Lk = t.b.len, w.first = t.tile;
+    if (lane == 0) {
+      found[0] = t.any, found[1] = w.q0, found[2] = w.Lq, found[3] = w.k0, found[4] = w.Lk;
+      found[5] = t.tile;
+    }
+    plan();
+    named_bar_sync(1, 64);  // the barriers are set up
+    // the copies that the first scores need start before the rest of the set-up
+    if (lane == 0 && w.n > 0) {
+      load_tile(0);
+      loaded = 1;
+      mbar_arrive_expect_tx(bar_q, ((w.n0 > 0) + (w.n1 > 0)) * C::TILE);
+      for (int u = 0; u < 2; ++u)
+        if ((u ? w.n1 : w.n0) > 0)
+          tma_load_rows(base + C::OFF_Q + u * C::TILE, &mq, bar_q,
+                        w.q0 + w.first + (HEADS ? 0 : 128 * u), head0 + (HEADS ? u : 0));
+    }
+    __syncwarp();
+  } else if (warp == 10) {
     if (lane == 0) {
       for (int s = 0; s < RING; ++s) {
         mbar_init(full + 8 * s, 1);
@@ -181,26 +202,12 @@ __global__ void __launch_bounds__(384, 1)
       fence_mbar_init();
       fence_proxy_async_smem();
     }
-    const Tile t = find_tile(io.cu_q, io.total_q, io.cu_k, io.total_k, io.n_seqs,
-                             HEADS ? 128 : 256, unit / uint32_t(n_hp), lane, io.status);
-    w.any = t.any;
-    w.q0 = t.a.start, w.Lq = t.a.len, w.k0 = t.b.start, w.Lk = t.b.len, w.first = t.tile;
-    if (lane == 0) {
-      found[0] = t.any, found[1] = w.q0, found[2] = w.Lq, found[3] = w.k0, found[4] = w.Lk;
-      found[5] = t.tile;
-    }
-    plan();
-    // the first copies start before the rest of the set-up
-    if (lane == 0 && w.n > 0) {
-      mbar_arrive_expect_tx(bar_q, ((w.n0 > 0) + (w.n1 > 0)) * C::TILE);
-      for (int u = 0; u < 2; ++u)
-        if ((u ? w.n1 : w.n0) > 0)
-          for (int bx = 0; bx < C::KB; ++bx)
-            tma_load_3d(base + C::OFF_Q + u * C::TILE + bx * C::BOX, &mq, bar_q, 64 * bx,
-                        head0 + (HEADS ? u : 0), w.q0 + w.first + (HEADS ? 0 : 128 * u));
-      for (; loaded < 2 * w.n && loaded < RING; ++loaded) load_tile(loaded);
-    }
     __syncwarp();
+    named_bar_sync(1, 64);
+  } else if (warp == 11 && lane == 0) {
+    tma_prefetch_desc(&mq);
+    tma_prefetch_desc(&mk);
+    tma_prefetch_desc(&mv);
   } else if (warp == 9) {
     tmem_alloc(smem_u32(tmem_holder), C::TMEM_COLS);
     tmem_relinquish();
@@ -235,7 +242,7 @@ __global__ void __launch_bounds__(384, 1)
     if (lane == 0 && n > 0) {
       int i = loaded;
       for (; i < 2 * n; ++i) {
-        if (!mbar_wait(empty + 8 * (i % RING), ((i / RING) - 1) & 1, abort_flag)) {
+        if (i >= RING && !mbar_wait(empty + 8 * (i % RING), ((i / RING) - 1) & 1, abort_flag)) {
           ok = false;
           break;
         }

@@ -97,8 +97,8 @@ __global__ void __launch_bounds__(256) bwd_prepare_kernel(SeqGeo g, const Packed
   __shared__ float top[8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (warp == 0) {
-    const Tile f = find_tile(io.cu_q, io.total_q, io.cu_k, io.total_k, io.n_seqs, 128, blockIdx.x,
-                             lane, io.status);
+    const Tile f = find_tile<kWalkQ>(io.cu_q, io.total_q, io.cu_k, io.total_k, io.n_seqs, g.causal,
+                                     128, blockIdx.x, lane, io.status);
     if (lane == 0)
       where[0] = f.any, where[1] = f.seq, where[2] = f.tile, where[3] = f.a.start, where[4] = f.a.len;
   }
@@ -275,8 +275,8 @@ __global__ void __launch_bounds__(352, 1)
     tmem_relinquish();
   }
   if (warp == 9) {
-    const Tile t = find_tile(io.cu_q, io.total_q, io.cu_k, io.total_k, io.n_seqs, 128,
-                             blockIdx.x / uint32_t(g.heads), lane, io.status);
+    const Tile t = find_tile<kWalkQ>(io.cu_q, io.total_q, io.cu_k, io.total_k, io.n_seqs, g.causal,
+                                     128, blockIdx.x / uint32_t(g.heads), lane, io.status);
     if (lane == 0) {
       found[0] = t.any, found[1] = t.a.start, found[2] = t.a.len;
       found[3] = t.b.start, found[4] = t.b.len, found[5] = t.tile, found[6] = t.seq;
@@ -302,8 +302,7 @@ __global__ void __launch_bounds__(352, 1)
       tma_prefetch_desc(&mk);
       tma_prefetch_desc(&mv);
       mbar_arrive_expect_tx(bar_q, C::TILE);
-      for (int bx = 0; bx < C::KB; ++bx)
-        tma_load_3d(sQ + bx * C::BOX, &mq, bar_q, 64 * bx, head, q0 + first);
+      tma_load_rows(sQ, &mq, bar_q, q0 + first, head);
       bool ok = true;
       int kl = 0, vl = 0;  // tiles whose K / V copies have been issued
       for (int p = 0; p < np; ++p) {
@@ -312,18 +311,14 @@ __global__ void __launch_bounds__(352, 1)
           break;
         }
         mbar_arrive_expect_tx(kfull + 8 * (p % NK), C::TILE);
-        for (int bx = 0; bx < C::KB; ++bx)
-          tma_load_3d(kslot(p) + bx * C::BOX, &mk, kfull + 8 * (p % NK), 64 * bx, kvh,
-                      k0 + p * 128);
+        tma_load_rows(kslot(p), &mk, kfull + 8 * (p % NK), k0 + p * 128, kvh);
         kl = p + 1;
         if (p >= NV && !mbar_wait(vempty + 8 * (p % NV), ((p - NV) / NV) & 1, abort_flag)) {
           ok = false;
           break;
         }
         mbar_arrive_expect_tx(vfull + 8 * (p % NV), C::TILE);
-        for (int bx = 0; bx < C::KB; ++bx)
-          tma_load_3d(vslot(p) + bx * C::BOX, &mv, vfull + 8 * (p % NV), 64 * bx, kvh,
-                      k0 + p * 128);
+        tma_load_rows(vslot(p), &mv, vfull + 8 * (p % NV), k0 + p * 128, kvh);
         vl = p + 1;
       }
       if (!ok) report_timeout(abort_flag, io.status);
@@ -614,14 +609,11 @@ __global__ void __launch_bounds__(352, 1)
     tmem_relinquish();
   }
   if (warp == 9) {
-    const Tile t = find_tile(io.cu_k, io.total_k, io.cu_q, io.total_q, io.n_seqs, 128,
-                             blockIdx.x / uint32_t(g.kv_heads), lane, io.status);
+    const Tile t = find_tile<kWalkK>(io.cu_k, io.total_k, io.cu_q, io.total_q, io.n_seqs, g.causal,
+                                     128, blockIdx.x / uint32_t(g.kv_heads), lane, io.status);
     if (lane == 0) {
       found[0] = t.any, found[1] = t.b.start, found[2] = t.b.len;
-      found[3] = t.a.start, found[4] = t.a.len, found[6] = t.seq;
-      // in causal order a sequence's first keys are seen by the most
-      // queries: the longest walks first
-      found[5] = g.causal ? (t.a.len + 127) / 128 - 1 - t.tile : t.tile;
+      found[3] = t.a.start, found[4] = t.a.len, found[5] = t.tile, found[6] = t.seq;
     }
   }
   tc_fence_before();
@@ -664,20 +656,16 @@ __global__ void __launch_bounds__(352, 1)
       tma_prefetch_desc(&mq);
       tma_prefetch_desc(&mdo);
       mbar_arrive_expect_tx(own, 2 * C::TILE);
-      for (int bx = 0; bx < C::KB; ++bx) {
-        tma_load_3d(sK + bx * C::BOX, &mk, own, 64 * bx, kvh, k0 + first);
-        tma_load_3d(sV + bx * C::BOX, &mv, own, 64 * bx, kvh, k0 + first);
-      }
+      tma_load_rows(sK, &mk, own, k0 + first, kvh);
+      tma_load_rows(sV, &mv, own, k0 + first, kvh);
       const int64_t stats = stat_rows(io.total_q, io.n_seqs), at0 = stat_start(q0, seq);
       // Q and dO tiles of step p with their rows' lse2 and D
       int lh = kvh * g.group, lt = qt0;  // head and query tile of the next load
       auto load = [&](int p) {
         const uint32_t bar = full + 8 * (p % NR);
         mbar_arrive_expect_tx(bar, 2 * C::TILE + 1024);
-        for (int bx = 0; bx < C::KB; ++bx) {
-          tma_load_3d(qslot(p) + bx * C::BOX, &mq, bar, 64 * bx, lh, q0 + lt * 128);
-          tma_load_3d(doslot(p) + bx * C::BOX, &mdo, bar, 64 * bx, lh, q0 + lt * 128);
-        }
+        tma_load_rows(qslot(p), &mq, bar, q0 + lt * 128, lh);
+        tma_load_rows(doslot(p), &mdo, bar, q0 + lt * 128, lh);
         const int64_t at = lh * stats + at0 + lt * 128;
         bulk_load(vecslot(p), io.stat_lse + at, 512, bar);
         bulk_load(vecslot(p) + 512, io.stat_delta + at, 512, bar);

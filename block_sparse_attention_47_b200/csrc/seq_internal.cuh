@@ -22,7 +22,8 @@ int device_sms();                            // of the current device
 bool stall_enabled();                        // bsa_debug_stall_pv of this thread
 void range_push(const char* name);
 void range_pop();
-// a [rows, heads, d] 16-bit tensor as a 3-D map, box 64 columns x 1 head x box_rows
+// a [rows, heads, d] 16-bit tensor as a 4-D map whose box is box_rows rows of
+// one head, 64 columns after the other ([column box][row][64] in shared memory)
 bsa_status make_rows_map(CUtensorMap* m, const void* ptr, int64_t rows, int heads, int d,
                          int64_t stride_n, int64_t stride_h, int box_rows, bool fp16);
 
@@ -172,6 +173,16 @@ __host__ __device__ constexpr uint32_t idesc_f32(int M, int N, bool b_mn_major) 
       : "r"(taddr)  \
       : "memory")
 
+// one box of such a map: `row` and the next rows of `head`
+__device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                              int row, int head) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(row), "r"(0), "r"(head)
+      : "memory");
+}
+
 // ---- packed sequences ------------------------------------------------------------
 // One sequence of a packed call; offsets that descend or leave the tensor are
 // reported and read as an empty sequence.
@@ -196,41 +207,85 @@ struct Tile {
   Span a, b;
 };
 
+// How long the walks of a sequence's tiles are.  kWalkQ: tiles of `rows`
+// queries (a) over 128-key steps of b, the last tile's the longest; kWalkK:
+// tiles of 128 keys (a) over the 128-query steps of b that see them, the
+// first tile's the longest.
+enum { kWalkQ, kWalkK };
+
+// tiles whose walk is longer than thr steps (they are the longest-walk end)
+template <int WALK>
+__device__ __forceinline__ int tiles_beyond(const Span& a, const Span& b, bool causal, int rows,
+                                            int thr) {
+  const int n = (a.len + rows - 1) / rows;
+  if (thr < 0) return n;
+  if (WALK == kWalkQ) {
+    if (b.len <= 128 * thr) return 0;
+    if (!causal) return n;
+    const int need = 128 * thr - (b.len - a.len);  // rows up to here see no more than thr steps
+    return n - (need < 0 ? 0 : need / rows);
+  }
+  const int left = (b.len + 127) / 128 - thr;
+  if (left <= 0) return 0;
+  if (!causal) return n;
+  const int reach = 128 * left - (b.len - a.len);
+  return reach <= 0 ? 0 : min(n, (reach + 127) / 128);
+}
+
 // The tile `target` of the list of all sequences' tiles of `rows` rows of a,
-// last sequence and last tile first (in causal order the longest walks come
-// first), by a whole warp.  any = false when the list is shorter.
+// by a whole warp; any = false when the list is shorter.  Long walks come
+// first, so that the grid does not end on them: up to 32 sequences in four
+// classes (walks beyond 1/2, 1/4 and 1/8 of the longest, the others), more
+// sequences only each by itself.
+template <int WALK>
 __device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ cu_a, int64_t total_a,
                                           const int32_t* __restrict__ cu_b, int64_t total_b,
-                                          int n_seqs, int rows, int64_t target, int lane,
-                                          int32_t* status) {
+                                          int n_seqs, bool causal, int rows, int64_t target,
+                                          int lane, int32_t* status) {
   Tile t{};
   int64_t before = 0;
   for (int base = 0; base < n_seqs; base += 32) {
-    const int s = n_seqs - 1 - base - lane;
+    const int s = base + lane;
     Span a{0, 0}, b{0, 0};
-    if (s >= 0) {  // four independent loads: one latency
+    if (s < n_seqs) {  // four independent loads: one latency
       a = span_of(cu_a, s, total_a, status);
       b = span_of(cu_b, s, total_b, status);
     }
-    const int n = (a.len + rows - 1) / rows;
-    int incl = n;
+    const int n_all = (a.len + rows - 1) / rows;
+    int longest = a.len > 0 ? (b.len + 127) / 128 : 0;
+    int classes = 1;
+    if (n_seqs > 1 && n_seqs <= 32) {
+      longest = __reduce_max_sync(0xffffffffu, longest);
+      classes = 4;
+    }
+    int done = 0;  // this sequence's tiles in the classes so far
+    for (int c = 0; c < classes; ++c) {
+      const int upto = c + 1 == classes
+                           ? n_all
+                           : tiles_beyond<WALK>(a, b, causal, rows, longest >> (c + 1));
+      const int n = upto - done;
+      int incl = n;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const uint32_t m = __ballot_sync(0xffffffffu, before + incl > target);
+      if (m) {
+        const int l = __ffs(m) - 1;
+        // its place among the sequence's tiles, longest walk first
+        const int p = __shfl_sync(0xffffffffu, done + int(target - (before + incl - n)), l);
+        const int n_l = __shfl_sync(0xffffffffu, n_all, l);
+        t.any = true;
+        t.seq = base + l;
+        t.tile = WALK == kWalkQ ? n_l - 1 - p : p;
+        t.a = {__shfl_sync(0xffffffffu, a.start, l), __shfl_sync(0xffffffffu, a.len, l)};
+        t.b = {__shfl_sync(0xffffffffu, b.start, l), __shfl_sync(0xffffffffu, b.len, l)};
+        return t;
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+      done = upto;
     }
-    const uint32_t m = __ballot_sync(0xffffffffu, before + incl > target);
-    if (m) {
-      const int l = __ffs(m) - 1;
-      const int n_l = __shfl_sync(0xffffffffu, n, l), incl_l = __shfl_sync(0xffffffffu, incl, l);
-      t.any = true;
-      t.seq = n_seqs - 1 - base - l;
-      t.tile = n_l - 1 - int(target - (before + incl_l - n_l));
-      t.a = {__shfl_sync(0xffffffffu, a.start, l), __shfl_sync(0xffffffffu, a.len, l)};
-      t.b = {__shfl_sync(0xffffffffu, b.start, l), __shfl_sync(0xffffffffu, b.len, l)};
-      return t;
-    }
-    before += __shfl_sync(0xffffffffu, incl, 31);
   }
   return t;
 }
