@@ -17,11 +17,21 @@
 // columns, and once S_(i+1) is signalled PV_i has finished and O may be
 // rescaled.  O is rescaled only when the maximum has grown by more than 2^8.
 //
-// K and V come through one ring of 128-row TMA boxes of the packed tensors.
+// K and V come as 128-row TMA boxes of the packed tensors, in a ring of
+// stages of two tiles: V_i beside K_(i+1), which the same turn of the products
+// takes, so a turn waits for and releases one stage (each such step costs the
+// issuing thread some 150 cycles, during which the pipe runs dry).
 // The box of a sequence's last tile runs into its neighbour's rows (or into
 // whatever lies behind the last sequence): such K columns are masked by a
 // select, and those V rows are zeroed in shared memory before the product,
 // since 0 times a NaN would reach the output.
+//
+// The grid is one CTA per SM; a CTA takes every G-th tile of the list, longest
+// walks first and back and forth, so that shares come out alike.  The copy
+// warp finds the next tile and loads its first operands while the last steps
+// of the current one run, and a warpgroup writes its rows while the pipe is
+// on the other tile's or the next one's products: at 4 steps a tile (cross
+// attention to a short text) the set-up was 60 % of the time.
 //
 // Few tiles and many keys (the next part of a long text): a cluster of CTAs
 // shares a tile's key steps; each leaves its maxima, sums and unnormalised O
@@ -37,32 +47,43 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMinShare = 4;  // key steps a CTA of a cluster takes at least
-#ifndef KSPLIT
-#define KSPLIT 300
-#endif
-constexpr int kSplitCtas = KSPLIT;
+// CTAs that clusters may ask for: at 72 tiles of 512 keys to 5,000 (8 heads
+// pairs) two, four and eight CTAs a tile took 44.9, 40.8 and 72 us, one 76 us;
+// few clusters of eight find room at a time
+constexpr int kSplitCtas = 300;
 
 template <int D>
 struct FwdCfg {
-  // warps 0-3 / 4-7: softmax of tile 0 / 1; 8: finds the tile, copies;
-  // 9: products; 10: the V tail
+  // warps 0-3 / 4-7: softmax of tile 0 / 1; 8: finds the tiles, copies;
+  // 9: products; 10: the V tails
   static constexpr int kThreads = 384;
   static constexpr int KB = D / 64;               // 64-column boxes
   static constexpr int BOX = 128 * 128;           // one box of 128 rows
   static constexpr int TILE = KB * BOX;           // 128 rows
-  static constexpr int RING = D == 128 ? 5 : 8;   // K and V tiles
+  static constexpr int RING = D == 128 ? 2 : 4;   // stages: V_(j-1), then K_j
+  static constexpr int STAGE = 32 * 128;          // a warp's 32 rows of 64 output channels
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_KV = 2 * TILE;
-  static constexpr int OFF_BAR = OFF_KV + RING * TILE;
-  // full[RING] empty[RING] q s[2] p[2] o[2] fix_go fixed drain
-  static constexpr int N_BARS = 2 * RING + 10;
-  static constexpr int OFF_MISC = OFF_BAR + 8 * N_BARS;
-  static constexpr int SMEM = OFF_MISC + 64 + 1024;
+  static constexpr int OFF_STAGE = OFF_KV + RING * 2 * TILE;
+  static constexpr int OFF_BAR = OFF_STAGE + 8 * STAGE;
+  // full[RING] empty[RING] q q_free info[2] info_free[2] s[2] p[2] o[2] fix_go
+  // fixed drain
+  static constexpr int N_BARS = 2 * RING + 15;
+  static constexpr int OFF_MISC = OFF_BAR + 8 * N_BARS;  // tmem, abort, then info[2][8]
+  static constexpr int SMEM = OFF_MISC + 16 + 64 + 1024;
   static constexpr uint32_t TMEM_COLS = 512, COL_O = 256;
   // a cluster's join: fp32 O [256][D], then (max, sum) [256]; over Q and the ring
   static constexpr int OFF_ML = 256 * D * 4;
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
   static_assert(OFF_ML + 256 * 8 <= OFF_BAR, "the join lies below the barriers");
+};
+
+// One entry of the tile list for this CTA: the sequence's rows and keys, the
+// first row of tile 0, this CTA's key steps.
+struct Plan {
+  bool any;
+  int q0, Lq, k0, Lk, first, hp;
+  int kb, n0, n1, n;  // first key tile, steps of the two tiles, their maximum
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -104,7 +125,8 @@ __device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
 template <typename T, int D, bool HEADS, bool SPLIT>
 __global__ void __launch_bounds__(384, 1)
     packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                      const __grid_constant__ CUtensorMap mv, SeqGeo g, const PackedIO io) {
+                      const __grid_constant__ CUtensorMap mv, SeqGeo g, const PackedIO io,
+                      int n_units) {
   using C = FwdCfg<D>;
   constexpr int RING = C::RING;
   constexpr float kShift = std::is_same<T, __half>::value ? 6.f : 0.f;
@@ -113,29 +135,24 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t base = (raw + 1023u) & ~1023u;
   unsigned char* sm = smem_raw + (base - raw);
   const uint32_t full = base + C::OFF_BAR, empty = full + 8 * RING, bar_q = empty + 8 * RING;
-  const uint32_t bar_s = bar_q + 8, bar_p = bar_s + 16, bar_o = bar_p + 16;
+  const uint32_t q_free = bar_q + 8, bar_info = q_free + 8, info_free = bar_info + 16;
+  const uint32_t bar_s = info_free + 16, bar_p = bar_s + 16, bar_o = bar_p + 16;
   const uint32_t fix_go = bar_o + 16, fixed = fix_go + 8, drain = fixed + 8;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 4);
-  int* found = reinterpret_cast<int*>(sm + C::OFF_MISC + 8);  // any, q start, Lq, k start, Lk, tile
-  auto slot = [&](int i) { return base + C::OFF_KV + uint32_t(i % RING) * C::TILE; };
+  volatile int* info = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 16);  // [2][8]
+  auto slot = [&](int j) { return base + C::OFF_KV + uint32_t(j % RING) * (2 * C::TILE); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_hp = HEADS ? g.heads >> 1 : g.heads;
   const int rank = SPLIT ? int(cluster_rank()) : 0, ranks = SPLIT ? int(cluster_size()) : 1;
-  const uint32_t unit = SPLIT ? blockIdx.x / uint32_t(ranks) : blockIdx.x;
-  const int hp = int(unit % uint32_t(n_hp));
-  const int head0 = HEADS ? 2 * hp : hp, kvh = head0 / g.group;
+  const int cta = int(blockIdx.x) / ranks, ctas = int(gridDim.x) / ranks;
+  // this CTA's it-th entry of the list, back and forth over the CTAs
+  auto unit_of = [&](int it) { return it * ctas + ((it & 1) ? ctas - 1 - cta : cta); };
 
-  // the walk of a tile: rows, and key steps of this CTA
-  struct {
-    bool any;
-    int q0, Lq, k0, Lk, first;
-    int kb, n0, n1, n;  // first key tile, steps of the two tiles, their maximum
-  } w;
-  auto plan = [&] {
-    w.first *= HEADS ? 128 : 256;  // first row of tile 0
-    auto steps = [&](int r) {      // key tiles that a tile's last row sees
-      if (!w.any || r >= w.Lq) return 0;
+  // (by value throughout: nothing of a role may live in local memory)
+  auto plan = [&](Plan w) {
+    auto steps = [&](int r) {  // key tiles that a tile's last row sees
+      if (r >= w.Lq) return 0;
       const int last = min(r + 128, w.Lq) - 1;
       const int lim = g.causal ? min(w.Lk, max(0, last + 1 + w.Lk - w.Lq)) : w.Lk;
       return (lim + 127) >> 7;
@@ -152,45 +169,40 @@ __global__ void __launch_bounds__(384, 1)
       w.n1 = max(0, min(w.n1, end) - w.kb);
       w.n = max(w.n0, w.n1);
     }
+    return w;
   };
-  auto load_tile = [&](int i) {  // K (even) and V (odd) tiles in walk order
-    const uint32_t bar = full + 8 * (i % RING);
-    mbar_arrive_expect_tx(bar, C::TILE);
-    tma_load_rows(slot(i), (i & 1) ? &mv : &mk, bar, w.k0 + (w.kb + (i >> 1)) * 128, kvh);
+  // The entry `it` as published by the copy warp; false at the list's end or
+  // on an abort.  All lanes of the calling warp, or one thread alone (mask).
+  // A wait may last as long as another tile's walk.
+  constexpr uint64_t kLong = 20000000000ull;
+  auto take = [&](int it, bool whole_warp) {
+    const uint32_t b = uint32_t(it & 1);
+    Plan w{};
+    bool got = mbar_wait(bar_info + 8 * b, (it >> 1) & 1, abort_flag, kLong);
+    if (whole_warp) got = __all_sync(0xffffffffu, got);
+    if (!got) {  // some role has given up, or does now
+      report_timeout(abort_flag, io.status);
+      return w;
+    }
+    const volatile int* e = info + 8 * b;
+    w.any = e[0] != 0;
+    w.q0 = e[1], w.Lq = e[2], w.k0 = e[3], w.Lk = e[4], w.first = e[5], w.hp = e[6];
+    if (whole_warp) __syncwarp();
+    if (!whole_warp || lane == 0) mbar_arrive(info_free + 8 * b);
+    return w.any ? plan(w) : w;
   };
 
-  int loaded = 0;
-  if (warp == 8) {
-    const Tile t =
-        find_tile<kWalkQ>(io.cu_q, io.total_q, io.cu_k, io.total_k, io.n_seqs, g.causal,
-                          HEADS ? 128 : 256, unit / uint32_t(n_hp), lane, io.status);
-    w.any = t.any;
-    w.q0 = t.a.start, w.Lq = t.a.len, w.k0 = t.b.start, w.Lk = t.b.len, w.first = t.tile;
-    if (lane == 0) {
-      found[0] = t.any, found[1] = w.q0, found[2] = w.Lq, found[3] = w.k0, found[4] = w.Lk;
-      found[5] = t.tile;
-    }
-    plan();
-    named_bar_sync(1, 64);  // the barriers are set up
-    // the copies that the first scores need start before the rest of the set-up
-    if (lane == 0 && w.n > 0) {
-      load_tile(0);
-      loaded = 1;
-      mbar_arrive_expect_tx(bar_q, ((w.n0 > 0) + (w.n1 > 0)) * C::TILE);
-      for (int u = 0; u < 2; ++u)
-        if ((u ? w.n1 : w.n0) > 0)
-          tma_load_rows(base + C::OFF_Q + u * C::TILE, &mq, bar_q,
-                        w.q0 + w.first + (HEADS ? 0 : 128 * u), head0 + (HEADS ? u : 0));
-    }
-    __syncwarp();
-  } else if (warp == 10) {
+  if (warp == 10) {
     if (lane == 0) {
       for (int s = 0; s < RING; ++s) {
         mbar_init(full + 8 * s, 1);
         mbar_init(empty + 8 * s, 1);
       }
       mbar_init(bar_q, 1);
+      mbar_init(q_free, 1);
       for (int u = 0; u < 2; ++u) {
+        mbar_init(bar_info + 8 * u, 1);
+        mbar_init(info_free + 8 * u, 10);  // products, tails, 8 softmax warps
         mbar_init(bar_s + 8 * u, 1);
         mbar_init(bar_p + 8 * u, 4);
         mbar_init(bar_o + 8 * u, 1);
@@ -203,71 +215,119 @@ __global__ void __launch_bounds__(384, 1)
       fence_proxy_async_smem();
     }
     __syncwarp();
-    named_bar_sync(1, 64);
-  } else if (warp == 11 && lane == 0) {
-    tma_prefetch_desc(&mq);
-    tma_prefetch_desc(&mk);
-    tma_prefetch_desc(&mv);
   } else if (warp == 9) {
     tmem_alloc(smem_u32(tmem_holder), C::TMEM_COLS);
     tmem_relinquish();
+  } else if (warp == 8 && lane == 0) {
+    tma_prefetch_desc(&mq);
+    tma_prefetch_desc(&mk);
+    tma_prefetch_desc(&mv);
   }
+  // the first entry is found during the set-up
+  Tile next{};
+  auto find = [&](int it) {
+    const int unit = unit_of(it);
+    Tile t{};
+    if (unit < n_units)
+      t = find_tile<kWalkQ>(io.cu_q, io.total_q, io.cu_k, io.total_k, io.n_seqs, g.causal,
+                            HEADS ? 128 : 256, unit / n_hp, lane, io.status);
+    return t;
+  };
+  if (warp == 8) next = find(0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  if (warp != 8) {
-    w.any = found[0] != 0;
-    w.q0 = found[1], w.Lq = found[2], w.k0 = found[3], w.Lk = found[4], w.first = found[5];
-    plan();
-  }
-  const int n0 = w.n0, n1 = w.n1, n = w.n, kb = w.kb, Lk = w.Lk, Lq = w.Lq;
-  const bool has_tail = n > 0 && (kb + n) * 128 > Lk;  // the walk ends in a partial key tile
+  bool ok = true;
 
-  // what a softmax thread ends with: its row and the row's statistics
+  // a softmax thread's row of the entry, and the row's statistics
   const int u = (warp >> 2) & 1, quad = warp & 3;
-  const int r = w.first + (HEADS ? 0 : 128 * u) + quad * 32 + lane;  // row within the sequence
-  const bool exists = warp < 8 && w.any && r < Lq;
-  const int nu = u ? n1 : n0;
   const uint32_t lane_base = uint32_t(quad * 32) << 16;
   const uint32_t tO = tmem + C::COL_O + 128u * u + lane_base;
+  int nu = 0;
   float m = -INFINITY, l = 0.f;
-  bool ok = true;
 
   // The softmax threads hold a row of 128 scores and take the other warps'
   // registers: 256 * 216 + 128 * 72 = 384 * 168, those of the launch.
   if (warp == 8) {
     // ------------------------------------------------------------ copies
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (lane == 0 && n > 0) {
-      int i = loaded;
-      for (; i < 2 * n; ++i) {
-        if (i >= RING && !mbar_wait(empty + 8 * (i % RING), ((i / RING) - 1) & 1, abort_flag)) {
-          ok = false;
-          break;
-        }
-        load_tile(i);
+    int c = 0, nq = 0;  // stages so far, entries with a walk so far
+    for (int it = 0; !SPLIT || it < 1; ++it) {
+      if (it > 0) next = find(it);
+      if (it >= 2) {
+        ok = __all_sync(0xffffffffu, mbar_wait(info_free + 8 * (it & 1), ((it >> 1) - 1) & 1,
+                                               abort_flag, kLong));
+        if (!ok) break;
       }
+      const Plan w = plan({next.any, next.a.start, next.a.len, next.b.start, next.b.len,
+                           next.tile * (HEADS ? 128 : 256), unit_of(it) % n_hp, 0, 0, 0, 0});
+      if (lane == 0) {
+        volatile int* e = info + 8 * (it & 1);
+        e[0] = w.any, e[1] = w.q0, e[2] = w.Lq, e[3] = w.k0, e[4] = w.Lk, e[5] = w.first, e[6] = w.hp;
+        mbar_arrive(bar_info + 8 * (it & 1));
+      }
+      __syncwarp();
+      if (!w.any) break;
+      if (w.n == 0) continue;
+      if (lane == 0) {
+        const int head0 = HEADS ? 2 * w.hp : w.hp, kvh = head0 / g.group;
+        auto load_stage = [&](int j) {  // V_(j-1) (none for j = 0) and K_j (none for j = n)
+          const int x = c + j;
+          if (x >= RING && !mbar_wait(empty + 8 * (x % RING), ((x / RING) - 1) & 1, abort_flag))
+            return false;
+          const uint32_t bar = full + 8 * (x % RING);
+          const int row = w.k0 + (w.kb + j) * 128;
+          mbar_arrive_expect_tx(bar, ((j > 0) + (j < w.n)) * C::TILE);
+          if (j > 0) tma_load_rows(slot(x), &mv, bar, row - 128, kvh);
+          if (j < w.n) tma_load_rows(slot(x) + C::TILE, &mk, bar, row, kvh);
+          return true;
+        };
+        ok = load_stage(0);
+        // Q once the previous entry's last scores have read theirs
+        if (ok && nq > 0) ok = mbar_wait(q_free, (nq - 1) & 1, abort_flag, kLong);
+        if (ok) {
+          mbar_arrive_expect_tx(bar_q, ((w.n0 > 0) + (w.n1 > 0)) * C::TILE);
+          for (int t = 0; t < 2; ++t)
+            if ((t ? w.n1 : w.n0) > 0)
+              tma_load_rows(base + C::OFF_Q + t * C::TILE, &mq, bar_q,
+                            w.q0 + w.first + (HEADS ? 0 : 128 * t), head0 + (HEADS ? t : 0));
+          ++nq;
+        }
+        for (int j = 1; ok && j <= w.n; ++j) ok = load_stage(j);
+      }
+      c += w.n + 1;
+      ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
+      if (!ok) break;
+    }
+    if (lane == 0) {
       if (!ok) report_timeout(abort_flag, io.status);
-      // on an abort the newest copy into each slot (and Q) may still be landing
+      // on an abort copies may still be landing: the newest into Q and each
+      // slot; a phase that never began ends the wait at its limit
       if (!ok || *abort_flag) {
-        mbar_wait(bar_q, 0, nullptr, 200000000ull);
-        for (int j = i > RING ? i - RING : 0; j < i; ++j)
-          mbar_wait(full + 8 * (j % RING), (j / RING) & 1, nullptr, 200000000ull);
+        if (nq > 0) mbar_wait(bar_q, (nq - 1) & 1, nullptr, 200000000ull);
+        for (int s = 0; s < RING; ++s) {
+          const int uses = c > s ? (c - s + RING - 1) / RING : 0;
+          for (int x = uses > 1 ? uses - 2 : 0; x < uses; ++x)
+            mbar_wait(full + 8 * s, x & 1, nullptr, 100000000ull);
+        }
       }
     }
     __syncwarp();
   } else if (warp == 9) {
     // ---------------------------------------------------------- products
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (lane == 0 && n > 0) {
+    if (lane == 0) {
       constexpr uint32_t id_s = idesc_f32<T>(128, 128, false);
       constexpr uint32_t id_o = idesc_f32<T>(128, D, true);
+      int c = 0, nq = 0, tails = 0;
+      int done0 = 0, done1 = 0;  // steps of each tile so far
       auto wait_full = [&](int i) {
-        return mbar_wait(full + 8 * (i % RING), (i / RING) & 1, abort_flag);
+        const int x = c + i;
+        return mbar_wait(full + 8 * (x % RING), (x / RING) & 1, abort_flag);
       };
       auto scores = [&](int t, int i) {  // S_t = Q_t K_i^T
-        const uint32_t sq = base + C::OFF_Q + t * C::TILE, sk = slot(2 * i);
+        const uint32_t sq = base + C::OFF_Q + t * C::TILE, sk = slot(c + i) + C::TILE;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (kk / 4) * C::BOX + (kk % 4) * 32;
@@ -276,40 +336,56 @@ __global__ void __launch_bounds__(384, 1)
         }
         tc_commit(bar_s + 8 * t);
       };
-      ok = mbar_wait(bar_q, 0, abort_flag) && wait_full(0);
-      if (ok) {
+      for (int it = 0; !SPLIT || it < 1; ++it) {
+        const Plan w = take(it, false);
+        if (!w.any) break;
+        const int n = w.n, n0 = w.n0, n1 = w.n1;
+        if (n == 0) continue;
+        const bool has_tail = (w.kb + n) * 128 > w.Lk;  // the walk ends in a partial key tile
+        ok = wait_full(0) && mbar_wait(bar_q, nq & 1, abort_flag);
+        ++nq;
+        if (!ok) break;
         tc_fence_after();
+#pragma unroll
         for (int t = 0; t < 2; ++t)
           if ((t ? n1 : n0) > 0) scores(t, 0);
-        tc_commit(empty);
-      }
-      // test hook: with `stall` set no PV is issued and the softmax's wait runs out
-      for (int i = 0; ok && i < n && !io.stall; ++i) {
-        const int vi = 2 * i + 1, ki = 2 * i + 2;
-        ok = wait_full(vi) && (i + 1 >= n || wait_full(ki));
-        if (ok && has_tail && i == n - 1) {
-          mbar_arrive(fix_go);  // the tail rows of V are zeroed by warp 10
-          ok = mbar_wait(fixed, 0, abort_flag);
-        }
-        for (int t = 0; ok && t < 2; ++t) {
-          const int nt = t ? n1 : n0;
-          if (i >= nt) continue;
-          ok = mbar_wait(bar_p + 8 * t, i & 1, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t sv = slot(vi);
+        tc_commit(empty + 8 * (c % RING));
+        if (n == 1) tc_commit(q_free);
+        // test hook: with `stall` set no PV is issued and the softmax's wait runs out
+        if (io.stall) break;
+        for (int i = 0; i < n; ++i) {
+          ok = wait_full(i + 1);
+          if (ok && has_tail && i == n - 1) {
+            mbar_arrive(fix_go);  // the tail rows of V are zeroed by warp 10
+            ok = mbar_wait(fixed, tails & 1, abort_flag);
+            ++tails;
+          }
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            tc_mma_ts(tmem + C::COL_O + 128u * t, tmem + 128u * t + 8u * kk,
-                      sdesc_sw128(sv + kk * 2048, C::BOX, 1024), id_o, (i > 0 || kk > 0) ? 1u : 0u);
-          if (i + 1 < nt)
-            scores(t, i + 1);
-          else
-            tc_commit(bar_o + 8 * t);
+          for (int t = 0; t < 2; ++t) {
+            const int nt = t ? n1 : n0;
+            if (!ok || i >= nt) continue;
+            ok = mbar_wait(bar_p + 8 * t, ((t ? done1 : done0) + i) & 1, abort_flag);
+            if (!ok) continue;
+            tc_fence_after();
+            const uint32_t sv = slot(c + i + 1);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              tc_mma_ts(tmem + C::COL_O + 128u * t, tmem + 128u * t + 8u * kk,
+                        sdesc_sw128(sv + kk * 2048, C::BOX, 1024), id_o,
+                        (i > 0 || kk > 0) ? 1u : 0u);
+            if (i + 1 < nt)
+              scores(t, i + 1);
+            else
+              tc_commit(bar_o + 8 * t);
+          }
+          if (!ok) break;
+          tc_commit(empty + 8 * ((c + i + 1) % RING));
+          if (i + 2 == n) tc_commit(q_free);
         }
         if (!ok) break;
-        tc_commit(empty + 8 * (vi % RING));
-        if (i + 1 < n) tc_commit(empty + 8 * (ki % RING));
+        done0 += n0;
+        done1 += n1;
+        c += n + 1;
       }
       if (!ok) report_timeout(abort_flag, io.status);
       // every MMA this thread issued has completed once the drain barrier flips
@@ -318,127 +394,149 @@ __global__ void __launch_bounds__(384, 1)
     }
     __syncwarp();
   } else if (warp == 10) {
-    // ------------------------------------------------------------ V tail
+    // ----------------------------------------------------------- V tails
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (has_tail) {
-      // asked for at the walk's end: the limit grows with its length
-      if (__all_sync(0xffffffffu, mbar_wait(fix_go, 0, abort_flag,
-                                            2000000000ull + uint64_t(n) * 10000ull))) {
-        const uint32_t sv = slot(2 * n - 1);
-        for (int bx = 0; bx < C::KB; ++bx)
-          for (int o = (Lk & 127) * 128 + lane * 16; o < C::BOX; o += 512)
-            st_shared_v4(sv + bx * C::BOX + o, make_uint4(0u, 0u, 0u, 0u));
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(fixed);
-      } else if (lane == 0) {
-        report_timeout(abort_flag, io.status);
-      }
+    int c = 0, tails = 0;
+    for (int it = 0; !SPLIT || it < 1; ++it) {
+      const Plan w = take(it, true);
+      if (!w.any) break;
+      c += w.n > 0 ? w.n + 1 : 0;
+      if (w.n == 0 || (w.kb + w.n) * 128 <= w.Lk) continue;
+      ok = __all_sync(0xffffffffu, mbar_wait(fix_go, tails & 1, abort_flag, kLong));
+      if (!ok) break;
+      ++tails;
+      const uint32_t sv = slot(c - 1);
+      for (int bx = 0; bx < C::KB; ++bx)
+        for (int o = (w.Lk & 127) * 128 + lane * 16; o < C::BOX; o += 512)
+          st_shared_v4(sv + bx * C::BOX + o, make_uint4(0u, 0u, 0u, 0u));
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(fixed);
     }
+    if (!ok && lane == 0) report_timeout(abort_flag, io.status);
   } else if (warp == 11) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   } else {
     // ----------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    const int lim = !exists ? 0 : (g.causal ? min(Lk, max(0, r + 1 + Lk - Lq)) : Lk);
     const uint32_t tS = tmem + 128u * u + lane_base;
     const float sl2 = g.scale * kLog2e;
-    for (int i = 0; i < nu; ++i) {
-      ok = __all_sync(0xffffffffu, mbar_wait(bar_s + 8 * u, i & 1, abort_flag));
+    int done = 0, tiles = 0;  // steps and tiles with a walk so far
+    for (int it = 0; !SPLIT || it < 1; ++it) {
+      const Plan w = take(it, true);
+      if (!w.any) break;
+      nu = u ? w.n1 : w.n0;
+      const int r = w.first + (HEADS ? 0 : 128 * u) + quad * 32 + lane;  // row within the sequence
+      const bool exists = r < w.Lq;
+      const int lim = !exists ? 0 : (g.causal ? min(w.Lk, max(0, r + 1 + w.Lk - w.Lq)) : w.Lk);
+      m = -INFINITY;
+      l = 0.f;
+      for (int i = 0; i < nu; ++i) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_s + 8 * u, (done + i) & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[128];
+        BSA_TMEM_LD128(tS, s);
+        const int seen = lim - 128 * (w.kb + i);
+        if (!__all_sync(0xffffffffu, !exists || seen >= 128)) {
+#pragma unroll
+          for (int x = 0; x < 128; ++x)
+            if (x >= seen) s[x] = 0xFF800000u;  // -inf
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int x = 0; x < 128; x += 2)
+          mx[(x >> 1) & 3] =
+              max3f(mx[(x >> 1) & 3], __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
+        const float mxs = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+        float factor = 1.f;
+        bool rescale = false;
+        if (mxs > m + 8.f) {
+          if (m != -INFINITY) {
+            factor = ex2_approx(m - mxs);
+            rescale = true;
+          }
+          m = mxs;
+        }
+        // the previous PV finished before this step's S did
+        if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll 1
+          for (int ch = 0; ch < D / 32; ++ch) {
+            uint32_t o[32];
+            BSA_TMEM_LD32(tO + 32u * ch, o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * factor);
+            BSA_TMEM_ST32(tO + 32u * ch, o);
+          }
+        }
+        // P <= 2^8; fp16 shifts it up by 2^6 so that fewer small ones vanish.
+        // One warp per scheduler takes 21.6 cycles a column pair here against
+        // 16 of the exponential unit alone; moving a share of the exponentials
+        // to the FMA pipe, or P to the products in parts, measured slower.
+        const float off = (m == -INFINITY ? 0.f : -m) + kShift;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < 128; x += 2) {
+          float x0, x1;
+          fma_f32x2(x0, x1, __uint_as_float(s[x]), __uint_as_float(s[x + 1]), sl2, sl2, off, off);
+          const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+          const int a = (x >> 1) & 1;
+          add_f32x2(sum[2 * a], sum[2 * a + 1], sum[2 * a], sum[2 * a + 1], p0, p1);
+          s[x >> 1] = pack2<T>(p0, p1);
+        }
+        BSA_TMEM_ST64(tS, s);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_p + 8 * u);
+        l = l * factor + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+      }
+      done += nu;
+      if (ok && nu > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_o + 8 * u, tiles & 1, abort_flag));
+        ++tiles;
+      }
       if (!ok) break;
       tc_fence_after();
-      uint32_t s[128];
-      BSA_TMEM_LD128(tS, s);
-      const int seen = lim - 128 * (kb + i);
-      if (!__all_sync(0xffffffffu, !exists || seen >= 128)) {
-#pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c >= seen) s[c] = 0xFF800000u;  // -inf
-      }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int c = 0; c < 128; c += 2)
-        mx[(c >> 1) & 3] = max3f(mx[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-      const float mxs = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-      float factor = 1.f;
-      bool rescale = false;
-      if (mxs > m + 8.f) {
-        if (m != -INFINITY) {
-          factor = ex2_approx(m - mxs);
-          rescale = true;
-        }
-        m = mxs;
-      }
-      // the previous PV finished before this step's S did
-      if (__any_sync(0xffffffffu, rescale)) {
+      if constexpr (!SPLIT) {
+        // ------------------------------------------------------ epilogue
+        const int head = HEADS ? 2 * w.hp + u : w.hp;
+        // a NaN sum stays one; a row that saw nothing gives 0
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        if (exists && io.lse)
+          io.lse[int64_t(head) * io.total_q + w.q0 + r] =
+              l == 0.f ? -INFINITY : m - kShift + log2f(l);
+        const uint32_t stage = base + C::OFF_STAGE + warp * C::STAGE;
+        const int row0 = r - lane;  // the warp's first row
+        T* dst = static_cast<T*>(io.o.p) + int64_t(w.q0 + row0) * io.o.sn + int64_t(head) * io.o.sh;
 #pragma unroll 1
-        for (int ch = 0; ch < D / 32; ++ch) {
-          uint32_t o[32];
-          BSA_TMEM_LD32(tO + 32u * ch, o);
+        for (int half = 0; half < D / 64; ++half) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * factor);
-          BSA_TMEM_ST32(tO + 32u * ch, o);
+          for (int ch = 0; ch < 2; ++ch) {
+            uint32_t o[32];
+            if (nu > 0) {  // else no product was issued
+              BSA_TMEM_LD32(tO + 64u * half + 32u * ch, o);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = 0u;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t v[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                v[x] = pack2<T>(__uint_as_float(o[8 * j + 2 * x]) * inv,
+                                __uint_as_float(o[8 * j + 2 * x + 1]) * inv);
+              stage_chunk<64>(stage, lane, 4 * ch + j, make_uint4(v[0], v[1], v[2], v[3]));
+            }
+          }
+          write_rows<T, 64>(stage, dst + 64 * half, io.o.sn, min(32, w.Lq - row0), lane);
         }
+        // O has been read: the next entry's first PV may overwrite it once
+        // this warp has handed in its P
+        tc_fence_before();
       }
-      // P <= 2^8; fp16 shifts it up by 2^6 so that fewer small ones vanish.
-      // One warp per scheduler takes 21.6 cycles a column pair here against
-      // 16 of the exponential unit alone; moving a share of the exponentials
-      // to the FMA pipe, or P to the products in parts, measured slower.
-      const float off = (m == -INFINITY ? 0.f : -m) + kShift;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < 128; c += 2) {
-        float x0, x1;
-        fma_f32x2(x0, x1, __uint_as_float(s[c]), __uint_as_float(s[c + 1]), sl2, sl2, off, off);
-        const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-        const int a = (c >> 1) & 1;
-        add_f32x2(sum[2 * a], sum[2 * a + 1], sum[2 * a], sum[2 * a + 1], p0, p1);
-        s[c >> 1] = pack2<T>(p0, p1);
-      }
-      BSA_TMEM_ST64(tS, s);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_p + 8 * u);
-      l = l * factor + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
     }
-    if (ok && nu > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar_o + 8 * u, 0, abort_flag));
-    if (!ok) {
-      if (lane == 0) report_timeout(abort_flag, io.status);
-    } else if (!SPLIT) {
-      // -------------------------------------------------------- epilogue
-      tc_fence_after();
-      const int head = head0 + (HEADS ? u : 0);
-      // a NaN sum stays one; a row that saw nothing gives 0
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      if (exists && io.lse)
-        io.lse[int64_t(head) * io.total_q + w.q0 + r] = l == 0.f ? -INFINITY : m - kShift + log2f(l);
-      // over the tile's own Q, which its products have read
-      const uint32_t stage = base + C::OFF_Q + u * C::TILE + quad * 32 * (2 * D);
-#pragma unroll 1
-      for (int ch = 0; ch < D / 32; ++ch) {
-        uint32_t o[32];
-        if (nu > 0) {  // else no product was issued
-          BSA_TMEM_LD32(tO + 32u * ch, o);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = 0u;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t v[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            v[x] = pack2<T>(__uint_as_float(o[8 * j + 2 * x]) * inv,
-                            __uint_as_float(o[8 * j + 2 * x + 1]) * inv);
-          stage_chunk<D>(stage, lane, 4 * ch + j, make_uint4(v[0], v[1], v[2], v[3]));
-        }
-      }
-      const int row0 = r - lane;  // the warp's first row
-      if (w.any)
-        write_rows<T, D>(stage, static_cast<T*>(io.o.p) + int64_t(w.q0 + row0) * io.o.sn +
-                                    int64_t(head) * io.o.sh,
-                         io.o.sn, min(32, Lq - row0), lane);
-    }
+    if (!ok && lane == 0) report_timeout(abort_flag, io.status);
   }
 
   tc_fence_before();
@@ -469,11 +567,13 @@ __global__ void __launch_bounds__(384, 1)
     }
     cluster_sync();
     // rank c writes rows c, c + ranks, ..: 16-byte output chunks, D / 8 a row
-    if (w.any && !*abort_flag) {
+    const bool live = info[0] != 0 && !*abort_flag;
+    const int q0 = info[1], Lq = info[2], first = info[5], hp = info[6];
+    if (live) {
       constexpr int CH = D / 8;
       for (int i = threadIdx.x; i < (256 / ranks) * CH; i += C::kThreads) {
         const int row = (i / CH) * ranks + rank, ch = i % CH;
-        const int t = row >> 7, rr = w.first + (HEADS ? 0 : 128 * t) + (row & 127);
+        const int t = row >> 7, rr = first + (HEADS ? 0 : 128 * t) + (row & 127);
         if (rr >= Lq) continue;
         float mm = -INFINITY, ll = 0.f;
         for (int c = 0; c < ranks; ++c)
@@ -496,13 +596,13 @@ __global__ void __launch_bounds__(384, 1)
           }
         }
         const float inv = ll == 0.f ? 0.f : 1.f / ll;
-        const int head = head0 + (HEADS ? t : 0);
+        const int head = HEADS ? 2 * hp + t : hp;
         if (io.lse && ch == 0)
-          io.lse[int64_t(head) * io.total_q + w.q0 + rr] =
+          io.lse[int64_t(head) * io.total_q + q0 + rr] =
               ll == 0.f ? -INFINITY : mm - kShift + log2f(ll);
         uint4 v = make_uint4(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv),
                              pack2<T>(o[4] * inv, o[5] * inv), pack2<T>(o[6] * inv, o[7] * inv));
-        *reinterpret_cast<uint4*>(static_cast<T*>(io.o.p) + int64_t(w.q0 + rr) * io.o.sn +
+        *reinterpret_cast<uint4*>(static_cast<T*>(io.o.p) + int64_t(q0 + rr) * io.o.sn +
                                   int64_t(head) * io.o.sh + ch * 8) = v;
       }
     }
@@ -513,7 +613,7 @@ __global__ void __launch_bounds__(384, 1)
 }
 
 template <typename T, int D, bool HEADS, bool SPLIT>
-cudaError_t launch_t(const SeqGeo& g, const CUtensorMap* maps, const PackedIO& io, int64_t units,
+cudaError_t launch_t(const SeqGeo& g, const CUtensorMap* maps, const PackedIO& io, int units,
                      int ranks, cudaStream_t st) {
   using C = FwdCfg<D>;
   auto kern = packed_fwd_kernel<T, D, HEADS, SPLIT>;
@@ -527,7 +627,8 @@ cudaError_t launch_t(const SeqGeo& g, const CUtensorMap* maps, const PackedIO& i
   cudaError_t e = allow_smem(kern, C::SMEM, seen);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(units * ranks));
+  const int sms = device_sms();
+  cfg.gridDim = dim3(unsigned(SPLIT ? units * ranks : (units < sms ? units : sms)));
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
@@ -537,7 +638,7 @@ cudaError_t launch_t(const SeqGeo& g, const CUtensorMap* maps, const PackedIO& i
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = SPLIT ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], g, io);
+  return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], g, io, units);
 }
 
 template <typename T, int D>
@@ -547,7 +648,7 @@ cudaError_t launch_d(const SeqGeo& g, const CUtensorMap* maps, const PackedIO& i
   // no more tiles than this whatever the lengths; the ones too many return
   const int64_t rows = heads ? 128 : 256;
   const int64_t tiles = io.total_q / rows + (io.n_seqs < io.total_q ? io.n_seqs : io.total_q);
-  const int64_t units = tiles * (heads ? g.heads / 2 : g.heads);
+  const int units = int(tiles * (heads ? g.heads / 2 : g.heads));
   // a tile per CTA fills less than half of the 148 SMs and some sequence may
   // have keys enough for two shares: split the keys
   int ranks = 1;
