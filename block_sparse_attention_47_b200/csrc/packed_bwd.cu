@@ -12,10 +12,14 @@
 //   dK/dV  CTA = 128 keys of a kv head, walking the query tiles that see them
 //          of every head of the group, so shared heads are summed in the
 //          accumulators.
-// Both follow the block-sparse backward's scheme: per step the two score-like
-// products are one N=128 burst each, two row groups of 128 threads take 64
-// of the 128 columns each, and the results return to tensor memory as A
-// operands of the accumulations, which run while the next step is loaded.
+// Per step the two score-like products are one N=128 burst each, two row
+// groups of 128 threads take 64 of the 128 columns each, and the results
+// return to tensor memory as A operands of the accumulations.  In dK/dV two
+// 128-column regions change roles from step to step: S^T in one, dP^T in the
+// other; P^T and dS^T go over S^T, so the next S^T can follow into dP^T's
+// region as soon as the groups have read it, under their remaining work (with
+// P^T over S^T and dS^T over dP^T a step took 3,450 cycles, now about 2,300
+// of which the products fill 2,048).
 //
 // Preparation: lse2 and D are written per 128-row tile of a sequence (rows
 // behind its end get lse2 = +inf, D = 0, so that P = 0 there), sequence b at
@@ -71,20 +75,28 @@ __device__ __forceinline__ void zero_rows(uint32_t tile, int boxes, int r0, int 
       st_shared_v4(tile + bx * 128 * 128 + o, make_uint4(0u, 0u, 0u, 0u));
 }
 
-// one 32-column chunk of an accumulator row, scaled, to 64 bytes of a gradient row
+// 64 columns of an accumulator, scaled, to 64 channels of a warp's 32 rows;
+// `stage`: 4 KB of the warp's own.  live = false writes zeros.
 template <typename T>
-__device__ __forceinline__ void store_chunk(T* dst, const uint32_t (&a)[32], float f, bool live) {
-  uint4* d4 = reinterpret_cast<uint4*>(dst);
+__device__ __forceinline__ void write_channels(uint32_t stage, uint32_t tcol, T* dst,
+                                               int64_t stride, int n_rows, float f, bool live,
+                                               int lane) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t w[4];
+  for (int ch = 0; ch < 2; ++ch) {
+    uint32_t a[32];
+    BSA_TMEM_LD32(tcol + 32u * ch, a);
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
-      w[x] = live ? pack2<T>(__uint_as_float(a[8 * i + 2 * x]) * f,
-                             __uint_as_float(a[8 * i + 2 * x + 1]) * f)
-                  : 0u;
-    d4[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        w[x] = live ? pack2<T>(__uint_as_float(a[8 * i + 2 * x]) * f,
+                               __uint_as_float(a[8 * i + 2 * x + 1]) * f)
+                    : 0u;
+      stage_chunk<64>(stage, lane, 4 * ch + i, make_uint4(w[0], w[1], w[2], w[3]));
+    }
   }
+  write_rows<T, 64>(stage, dst, stride, n_rows, lane);
 }
 
 // ============================================================================
@@ -199,8 +211,8 @@ __global__ void __launch_bounds__(256) bwd_vnorm_kernel(SeqGeo g, const PackedBw
 template <int D>
 struct DqCfg {
   // warps 0-3 / 4-7: row groups 0 / 1 (64 key columns of a step each);
-  // 8: S/dP issuer; 9: finds the tile, copies, the K tail; 10: accumulations
-  static constexpr int kThreads = 352;
+  // 8: S/dP issuer; 9: finds the tile, copies; 10: accumulations; 11: the K tail
+  static constexpr int kThreads = 384;
   static constexpr int KB = D / 64;
   static constexpr int NK = 3, NV = 2;       // K / V ring slots
   static constexpr int BOX = 128 * 128;
@@ -210,8 +222,8 @@ struct DqCfg {
   static constexpr int OFF_V = OFF_K + NK * TILE;
   static constexpr int OFF_BAR = OFF_V + NV * TILE;
   // kfull[NK] kempty[NK] vfull[NV] vempty[NV] sd_ready read x_ready[2]
-  // x_free own q fix_go fixed done drain[2]
-  static constexpr int N_BARS = 2 * NK + 2 * NV + 12;
+  // x_free own q do fix_go fixed done drain[2]
+  static constexpr int N_BARS = 2 * NK + 2 * NV + 13;
   static constexpr int OFF_MISC = OFF_BAR + 8 * N_BARS;
   static constexpr int SMEM = OFF_MISC + 64 + 1024;
   static constexpr uint32_t TMEM_COLS = 512;
@@ -222,9 +234,10 @@ struct DqCfg {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(352, 1)
+__global__ void __launch_bounds__(384, 1)
     packed_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                     const __grid_constant__ CUtensorMap mv, SeqGeo g, const PackedBwdIO io) {
+                     const __grid_constant__ CUtensorMap mv,
+                     const __grid_constant__ CUtensorMap mdo, SeqGeo g, const PackedBwdIO io) {
   using C = DqCfg<D>;
   constexpr bool kHalf = std::is_same<T, __half>::value;
   constexpr int NK = C::NK, NV = C::NV;
@@ -237,7 +250,8 @@ __global__ void __launch_bounds__(352, 1)
   const uint32_t vfull = kempty + 8 * NK, vempty = vfull + 8 * NV;
   const uint32_t sd_ready = vempty + 8 * NV, read = sd_ready + 8, x_ready = read + 8;
   const uint32_t x_free = x_ready + 16, own = x_free + 8, bar_q = own + 8;
-  const uint32_t fix_go = bar_q + 8, fixed = fix_go + 8, done = fixed + 8, drain = done + 8;
+  const uint32_t bar_do = bar_q + 8, fix_go = bar_do + 8, fixed = fix_go + 8, done = fixed + 8;
+  const uint32_t drain = done + 8;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 4);
   int* found = reinterpret_cast<int*>(sm + C::OFF_MISC + 8);
@@ -246,67 +260,90 @@ __global__ void __launch_bounds__(352, 1)
   auto kslot = [&](int p) { return base + C::OFF_K + (p % NK) * C::TILE; };
   auto vslot = [&](int p) { return base + C::OFF_V + (p % NV) * C::TILE; };
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < NK; ++s) {
-      mbar_init(kfull + 8 * s, 1);
-      mbar_init(kempty + 8 * s, 1);
+  int q0 = 0, Lq = 0, k0 = 0, Lk = 0, first = 0, seq = 0, np = 0;
+  bool any = false;
+  auto plan = [&] {  // np: key tiles that the tile's last row sees
+    const int last = min(first + 128, Lq) - 1;
+    np = any ? ((g.causal ? min(Lk, max(0, last + 1 + Lk - Lq)) : Lk) + 127) >> 7 : 0;
+  };
+  if (warp == 10) {
+    if (lane == 0) {
+      for (int s = 0; s < NK; ++s) {
+        mbar_init(kfull + 8 * s, 1);
+        mbar_init(kempty + 8 * s, 1);
+      }
+      for (int s = 0; s < NV; ++s) {
+        mbar_init(vfull + 8 * s, 1);
+        mbar_init(vempty + 8 * s, 1);
+      }
+      mbar_init(sd_ready, 1);
+      mbar_init(read, 8);
+      mbar_init(x_ready, 4);
+      mbar_init(x_ready + 8, 4);
+      mbar_init(x_free, 1);
+      mbar_init(own, 4);
+      mbar_init(bar_q, 1);
+      mbar_init(bar_do, 1);
+      mbar_init(fix_go, 1);
+      mbar_init(fixed, 1);
+      mbar_init(done, 2);
+      mbar_init(drain, 1);
+      mbar_init(drain + 8, 1);
+      *abort_flag = 0;
+      fence_mbar_init();
+      fence_proxy_async_smem();
     }
-    for (int s = 0; s < NV; ++s) {
-      mbar_init(vfull + 8 * s, 1);
-      mbar_init(vempty + 8 * s, 1);
-    }
-    mbar_init(sd_ready, 1);
-    mbar_init(read, 8);
-    mbar_init(x_ready, 4);
-    mbar_init(x_ready + 8, 4);
-    mbar_init(x_free, 1);
-    mbar_init(own, 4);
-    mbar_init(bar_q, 1);
-    mbar_init(fix_go, 1);
-    mbar_init(fixed, 1);
-    mbar_init(done, 2);
-    mbar_init(drain, 1);
-    mbar_init(drain + 8, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-  }
-  if (warp == 8) {
+    __syncwarp();
+    named_bar_sync(1, 64);
+  } else if (warp == 8) {
     tmem_alloc(smem_u32(tmem_holder), C::TMEM_COLS);
     tmem_relinquish();
-  }
-  if (warp == 9) {
+  } else if (warp == 11 && lane == 0) {
+    tma_prefetch_desc(&mq);
+    tma_prefetch_desc(&mk);
+    tma_prefetch_desc(&mv);
+    tma_prefetch_desc(&mdo);
+  } else if (warp == 9) {
     const Tile t = find_tile<kWalkQ>(io.cu_q, io.total_q, io.cu_k, io.total_k, io.n_seqs, g.causal,
                                      128, blockIdx.x / uint32_t(g.heads), lane, io.status);
+    any = t.any, q0 = t.a.start, Lq = t.a.len, k0 = t.b.start, Lk = t.b.len;
+    first = t.tile * 128, seq = t.seq;
     if (lane == 0) {
-      found[0] = t.any, found[1] = t.a.start, found[2] = t.a.len;
-      found[3] = t.b.start, found[4] = t.b.len, found[5] = t.tile, found[6] = t.seq;
+      found[0] = any, found[1] = q0, found[2] = Lq, found[3] = k0, found[4] = Lk;
+      found[5] = first, found[6] = seq;
     }
+    plan();
+    named_bar_sync(1, 64);  // the barriers are set up
+    // the first copies start before the rest of the set-up; dO passes through
+    // the third K slot on its way to tensor memory
+    if (lane == 0 && np > 0) {
+      mbar_arrive_expect_tx(bar_do, C::TILE);
+      tma_load_rows(kslot(2), &mdo, bar_do, q0 + first, head);
+      mbar_arrive_expect_tx(bar_q, C::TILE);
+      tma_load_rows(sQ, &mq, bar_q, q0 + first, head);
+    }
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const bool any = found[0] != 0;
-  const int q0 = found[1], Lq = found[2], k0 = found[3], Lk = found[4];
-  const int first = any ? found[5] * 128 : 0, seq = found[6];
-  int np = 0;  // key tiles that the tile's last row sees
-  if (any) {
-    const int last = min(first + 128, Lq) - 1;
-    np = ((g.causal ? min(Lk, max(0, last + 1 + Lk - Lq)) : Lk) + 127) >> 7;
+  if (warp != 9) {
+    any = found[0] != 0;
+    q0 = found[1], Lq = found[2], k0 = found[3], Lk = found[4], first = found[5], seq = found[6];
+    plan();
   }
   const bool has_tail = np > 0 && np * 128 > Lk;
 
   if (warp == 9) {
-    // ---- the copies: Q, then K and V tiles into their rings
+    // ---- the copies: K and V tiles into their rings
     if (lane == 0 && np > 0) {
-      tma_prefetch_desc(&mk);
-      tma_prefetch_desc(&mv);
-      mbar_arrive_expect_tx(bar_q, C::TILE);
-      tma_load_rows(sQ, &mq, bar_q, q0 + first, head);
       bool ok = true;
       int kl = 0, vl = 0;  // tiles whose K / V copies have been issued
       for (int p = 0; p < np; ++p) {
-        if (p >= NK && !mbar_wait(kempty + 8 * (p % NK), ((p - NK) / NK) & 1, abort_flag)) {
+        // (the third K slot is free once dO has been taken out of it)
+        if ((p >= NK && !mbar_wait(kempty + 8 * (p % NK), ((p - NK) / NK) & 1, abort_flag)) ||
+            (p == 2 && !mbar_wait(own, 0, abort_flag))) {
           ok = false;
           break;
         }
@@ -325,6 +362,7 @@ __global__ void __launch_bounds__(352, 1)
       if (!ok || *abort_flag) {
         // the newest copies may still be landing
         mbar_wait(bar_q, 0, nullptr, 200000000ull);
+        mbar_wait(bar_do, 0, nullptr, 200000000ull);
         for (int p = kl > NK ? kl - NK : 0; p < kl; ++p)
           mbar_wait(kfull + 8 * (p % NK), (p / NK) & 1, nullptr, 200000000ull);
         for (int p = vl > NV ? vl - NV : 0; p < vl; ++p)
@@ -332,9 +370,11 @@ __global__ void __launch_bounds__(352, 1)
       }
     }
     __syncwarp();
+  } else if (warp == 11) {
     // ---- the last tile's foreign K rows, once it has landed
     if (has_tail) {
-      if (__all_sync(0xffffffffu, mbar_wait(fix_go, 0, abort_flag))) {
+      if (__all_sync(0xffffffffu, mbar_wait(fix_go, 0, abort_flag,
+                                            2000000000ull + uint64_t(np) * 10000ull))) {
         zero_rows(kslot(np - 1), C::KB, Lk - (np - 1) * 128, lane);
         fence_proxy_async_smem();
         __syncwarp();
@@ -418,19 +458,20 @@ __global__ void __launch_bounds__(352, 1)
     const uint32_t lane_base = uint32_t(quad * 32) << 16;
     const bool exists = any && r < Lq;
     const int lim = !exists ? 0 : (g.causal ? min(Lk, max(0, r + 1 + Lk - Lq)) : Lk);
+    bool ok = true;
     if (grp == 1 && np > 0) {
-      // dO rows into tensor memory: the A operand of dP
-      const T* src = static_cast<const T*>(io.dout.p) + int64_t(q0 + r) * io.dout.sn +
-                     int64_t(head) * io.dout.sh;
+      // dO rows into tensor memory: the A operand of dP (rows behind the end
+      // are foreign and only reach rows that are not stored)
+      ok = __all_sync(0xffffffffu, mbar_wait(bar_do, 0, abort_flag));
       uint32_t rw[D / 2];
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
-        const uint4 u = exists ? __ldg(reinterpret_cast<const uint4*>(src) + i)
-                               : make_uint4(0u, 0u, 0u, 0u);
-        rw[4 * i] = u.x;
-        rw[4 * i + 1] = u.y;
-        rw[4 * i + 2] = u.z;
-        rw[4 * i + 3] = u.w;
+        const float4 x = ld_shared_f4(kslot(2) + (i >> 3) * C::BOX + row * 128 +
+                                      (((i & 7) ^ (row & 7)) << 4));
+        rw[4 * i] = __float_as_uint(x.x);
+        rw[4 * i + 1] = __float_as_uint(x.y);
+        rw[4 * i + 2] = __float_as_uint(x.z);
+        rw[4 * i + 3] = __float_as_uint(x.w);
       }
       if constexpr (D == 128) {
         BSA_TMEM_ST64(tmem + C::COL_DO + lane_base, rw);
@@ -439,7 +480,7 @@ __global__ void __launch_bounds__(352, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(own);
+      if (lane == 0 && ok) mbar_arrive(own);
     }
     float lse2 = INFINITY, dlt = 0.f, fac = 1.f;
     if (exists && np > 0) {
@@ -453,8 +494,7 @@ __global__ void __launch_bounds__(352, 1)
     const uint32_t tS = tmem + C::COL_S + 64u * grp + lane_base;
     const uint32_t tDP = tmem + C::COL_DP + 64u * grp + lane_base;
     const uint32_t tDS = tmem + C::COL_DS + 32u * grp + lane_base;
-    bool ok = true;
-    for (int p = 0; p < np; ++p) {
+    for (int p = 0; ok && p < np; ++p) {
       ok = __all_sync(0xffffffffu, mbar_wait(sd_ready, p & 1, abort_flag));
       if (!ok) break;
       tc_fence_after();
@@ -508,15 +548,14 @@ __global__ void __launch_bounds__(352, 1)
     if (!ok) {
       if (lane == 0) report_timeout(abort_flag, io.status);
     } else {
-      // group grp writes channels grp * D/2 ..; no step: the gradient is 0
+      // group grp writes channels 64 grp ..; no step: the gradient is 0
       tc_fence_after();
-      T* dst = static_cast<T*>(io.dq.p) + int64_t(q0 + r) * io.dq.sn + int64_t(head) * io.dq.sh;
-      const float f = g.scale / fac;
-#pragma unroll 1
-      for (int ch = grp * (D / 64); ch < (grp + 1) * (D / 64); ++ch) {
-        uint32_t a[32];
-        BSA_TMEM_LD32(tmem + C::COL_ACC + 32u * ch + lane_base, a);
-        if (exists) store_chunk<T>(dst + 32 * ch, a, f, np > 0);
+      if (any && 64 * grp < D) {
+        const int row0 = first + quad * 32;  // the warp's first row
+        write_channels<T>(sQ + warp * 4096, tmem + C::COL_ACC + 64u * grp + lane_base,
+                          static_cast<T*>(io.dq.p) + int64_t(q0 + row0) * io.dq.sn +
+                              int64_t(head) * io.dq.sh + 64 * grp,
+                          io.dq.sn, min(32, Lq - row0), g.scale / fac, np > 0, lane);
       }
     }
   }
@@ -534,9 +573,9 @@ __global__ void __launch_bounds__(352, 1)
 template <int D>
 struct DkdvCfg {
   // warps 0-3 / 4-7: row groups 0 / 1 (64 query columns of a step each);
-  // 8: S^T/dP^T issuer and copies; 9: finds the tile, the Q/dO tails; 10:
-  // accumulations
-  static constexpr int kThreads = 352;
+  // 8: S^T/dP^T issuer; 9: finds the tile, copies; 10: accumulations; 11: the
+  // Q/dO tails
+  static constexpr int kThreads = 384;
   static constexpr int KB = D / 64;
   static constexpr int NR = 2;                 // Q/dO ring slots
   static constexpr int BOX = 128 * 128;
@@ -545,20 +584,21 @@ struct DkdvCfg {
   static constexpr int OFF_STG = 2 * TILE;     // [slot][Q | dO]
   static constexpr int OFF_VEC = OFF_STG + NR * 2 * TILE;  // [slot][lse2 128 | D 128] fp32
   static constexpr int OFF_BAR = OFF_VEC + NR * 1024;
-  // full[NR] s_ready dp_ready st_issued p_ready[2] ds_ready[2] xv_free
-  // xk_free own fix_go fixed done drain[2]
+  // full[NR] s_ready dp_ready dp_read st_issued p_ready[2] ds_ready[2] x_free own
+  // fix_go fixed done drain[2]
   static constexpr int N_BARS = NR + 15;
   static constexpr int OFF_MISC = OFF_BAR + 8 * N_BARS;
   static constexpr int SMEM = OFF_MISC + 64 + 1024;
   static constexpr uint32_t TMEM_COLS = 512;
-  // S^T at 0 (group w's half at 64 w, P^T over it), dP^T at 128 (dS^T over
-  // it), dV at 256, dK at 256 + D
-  static constexpr uint32_t COL_ST = 0, COL_DPT = 128, COL_DV = 256, COL_DK = 256 + D;
+  // step p: S^T at 128 (p & 1) (group w's half at + 64 w; P^T over its first
+  // 32 columns, dS^T over its last), dP^T in the other region; dV at 256, dK
+  // at 256 + D
+  static constexpr uint32_t COL_DV = 256, COL_DK = 256 + D;
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(352, 1)
+__global__ void __launch_bounds__(384, 1)
     packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq,
                        const __grid_constant__ CUtensorMap mk,
                        const __grid_constant__ CUtensorMap mv,
@@ -572,8 +612,9 @@ __global__ void __launch_bounds__(352, 1)
   unsigned char* sm = smem_raw + (base - raw);
   const uint32_t sK = base + C::OFF_K, sV = base + C::OFF_V;
   const uint32_t full = base + C::OFF_BAR, s_ready = full + 8 * NR, dp_ready = s_ready + 8;
-  const uint32_t st_issued = dp_ready + 8, p_ready = st_issued + 8, ds_ready = p_ready + 16;
-  const uint32_t xv_free = ds_ready + 16, xk_free = xv_free + 8, own = xk_free + 8;
+  const uint32_t dp_read = dp_ready + 8, st_issued = dp_read + 8;
+  const uint32_t p_ready = st_issued + 8, ds_ready = p_ready + 16;
+  const uint32_t x_free = ds_ready + 16, own = x_free + 8;
   const uint32_t fix_go = own + 8, fixed = fix_go + 8, done = fixed + 8, drain = done + 8;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 4);
@@ -584,55 +625,117 @@ __global__ void __launch_bounds__(352, 1)
   auto doslot = [&](int p) { return qslot(p) + C::TILE; };
   auto vecslot = [&](int p) { return base + C::OFF_VEC + (p % NR) * 1024; };
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < NR; ++s) mbar_init(full + 8 * s, 1);
-    mbar_init(s_ready, 1);
-    mbar_init(dp_ready, 1);
-    mbar_init(st_issued, 1);
-    for (int w = 0; w < 2; ++w) {
-      mbar_init(p_ready + 8 * w, 4);
-      mbar_init(ds_ready + 8 * w, 4);
+  int q0 = 0, Lq = 0, k0 = 0, Lk = 0, first = 0, seq = 0;
+  // query tiles qt0 .. qt0+per-1 of each of the group's heads, head after head
+  int qt0 = 0, per = 0, np = 0;
+  bool any = false;
+  auto plan = [&] {
+    if (any && Lq > 0) {
+      if (g.causal) qt0 = max(0, first + Lq - Lk) >> 7;
+      per = ((Lq + 127) >> 7) - qt0;
+      np = per * g.group;
     }
-    mbar_init(xv_free, 1);
-    mbar_init(xk_free, 1);
-    mbar_init(own, 1);
-    mbar_init(fix_go, 1);
-    mbar_init(fixed, 1);
-    mbar_init(done, 2);
-    mbar_init(drain, 1);
-    mbar_init(drain + 8, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-  }
-  if (warp == 8) {
+  };
+  // Q and dO tiles of step p with their rows' lse2 and D
+  const int64_t stats = stat_rows(io.total_q, io.n_seqs);
+  int lh = kvh * g.group, lt = 0, loaded = 0;  // head, query tile and step of the next load
+  auto load = [&] {
+    const int p = loaded++;
+    const uint32_t bar = full + 8 * (p % NR);
+    mbar_arrive_expect_tx(bar, 2 * C::TILE + 1024);
+    tma_load_rows(qslot(p), &mq, bar, q0 + lt * 128, lh);
+    tma_load_rows(doslot(p), &mdo, bar, q0 + lt * 128, lh);
+    const int64_t at = lh * stats + stat_start(q0, seq) + lt * 128;
+    bulk_load(vecslot(p), io.stat_lse + at, 512, bar);
+    bulk_load(vecslot(p) + 512, io.stat_delta + at, 512, bar);
+    if (++lt == qt0 + per) {
+      lt = qt0;
+      ++lh;
+    }
+  };
+  if (warp == 10) {
+    if (lane == 0) {
+      for (int s = 0; s < NR; ++s) mbar_init(full + 8 * s, 1);
+      mbar_init(s_ready, 1);
+      mbar_init(dp_ready, 1);
+      mbar_init(dp_read, 8);
+      mbar_init(st_issued, 1);
+      for (int w = 0; w < 2; ++w) {
+        mbar_init(p_ready + 8 * w, 4);
+        mbar_init(ds_ready + 8 * w, 4);
+      }
+      mbar_init(x_free, 1);
+      mbar_init(own, 1);
+      mbar_init(fix_go, 1);
+      mbar_init(fixed, 1);
+      mbar_init(done, 2);
+      mbar_init(drain, 1);
+      mbar_init(drain + 8, 1);
+      *abort_flag = 0;
+      fence_mbar_init();
+      fence_proxy_async_smem();
+    }
+    __syncwarp();
+    named_bar_sync(1, 64);
+  } else if (warp == 8) {
     tmem_alloc(smem_u32(tmem_holder), C::TMEM_COLS);
     tmem_relinquish();
-  }
-  if (warp == 9) {
+  } else if (warp == 11 && lane == 0) {
+    tma_prefetch_desc(&mq);
+    tma_prefetch_desc(&mk);
+    tma_prefetch_desc(&mv);
+    tma_prefetch_desc(&mdo);
+  } else if (warp == 9) {
     const Tile t = find_tile<kWalkK>(io.cu_k, io.total_k, io.cu_q, io.total_q, io.n_seqs, g.causal,
                                      128, blockIdx.x / uint32_t(g.kv_heads), lane, io.status);
+    any = t.any, q0 = t.b.start, Lq = t.b.len, k0 = t.a.start, Lk = t.a.len;
+    first = t.tile * 128, seq = t.seq;
     if (lane == 0) {
-      found[0] = t.any, found[1] = t.b.start, found[2] = t.b.len;
-      found[3] = t.a.start, found[4] = t.a.len, found[5] = t.tile, found[6] = t.seq;
+      found[0] = any, found[1] = q0, found[2] = Lq, found[3] = k0, found[4] = Lk;
+      found[5] = first, found[6] = seq;
     }
+    plan();
+    lt = qt0;
+    named_bar_sync(1, 64);  // the barriers are set up
+    // the first copies start before the rest of the set-up
+    if (lane == 0 && np > 0) {
+      mbar_arrive_expect_tx(own, 2 * C::TILE);
+      tma_load_rows(sK, &mk, own, k0 + first, kvh);
+      tma_load_rows(sV, &mv, own, k0 + first, kvh);
+      load();
+    }
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const bool any = found[0] != 0;
-  const int q0 = found[1], Lq = found[2], k0 = found[3], Lk = found[4];
-  const int first = any ? found[5] * 128 : 0, seq = found[6];
-  // query tiles qt0 .. n_qt-1 of each of the group's heads, head after head
-  int qt0 = 0, per = 0;
-  if (any && Lq > 0) {
-    if (g.causal) qt0 = max(0, first + Lq - Lk) >> 7;
-    per = ((Lq + 127) >> 7) - qt0;
+  if (warp != 9) {
+    any = found[0] != 0;
+    q0 = found[1], Lq = found[2], k0 = found[3], Lk = found[4], first = found[5], seq = found[6];
+    plan();
   }
-  const int np = per * g.group;
   const bool has_tail = np > 0 && (Lq & 127) != 0;  // every per-th step's tile is partial
 
   if (warp == 9) {
+    // ---- the copies: step p into the slot of step p - 2 once its
+    // accumulations have finished
+    if (lane == 0 && np > 0) {
+      bool ok = true;
+      while (ok && loaded < np) {
+        if (loaded >= NR) ok = mbar_wait(x_free, (loaded - NR) & 1, abort_flag);
+        if (ok) load();
+      }
+      if (!ok) report_timeout(abort_flag, io.status);
+      if (!ok || *abort_flag) {
+        // the newest copies may still be landing
+        mbar_wait(own, 0, nullptr, 200000000ull);
+        for (int p = loaded > NR ? loaded - NR : 0; p < loaded; ++p)
+          mbar_wait(full + 8 * (p % NR), (p / NR) & 1, nullptr, 200000000ull);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 11) {
     // ---- the foreign rows of the heads' last Q and dO tiles
     if (has_tail) {
       for (int h = 0; h < g.group; ++h) {
@@ -650,135 +753,81 @@ __global__ void __launch_bounds__(352, 1)
       }
     }
   } else if (warp == 8) {
-    // ---- S^T and dP^T of each step, and the copies
+    // ---- S^T and dP^T of each step
     if (lane == 0 && np > 0) {
       constexpr uint32_t idesc_s = idesc_f32<T>(128, 128, false);
-      tma_prefetch_desc(&mq);
-      tma_prefetch_desc(&mdo);
-      mbar_arrive_expect_tx(own, 2 * C::TILE);
-      tma_load_rows(sK, &mk, own, k0 + first, kvh);
-      tma_load_rows(sV, &mv, own, k0 + first, kvh);
-      const int64_t stats = stat_rows(io.total_q, io.n_seqs), at0 = stat_start(q0, seq);
-      // Q and dO tiles of step p with their rows' lse2 and D
-      int lh = kvh * g.group, lt = qt0;  // head and query tile of the next load
-      auto load = [&](int p) {
-        const uint32_t bar = full + 8 * (p % NR);
-        mbar_arrive_expect_tx(bar, 2 * C::TILE + 1024);
-        tma_load_rows(qslot(p), &mq, bar, q0 + lt * 128, lh);
-        tma_load_rows(doslot(p), &mdo, bar, q0 + lt * 128, lh);
-        const int64_t at = lh * stats + at0 + lt * 128;
-        bulk_load(vecslot(p), io.stat_lse + at, 512, bar);
-        bulk_load(vecslot(p) + 512, io.stat_delta + at, 512, bar);
-        if (++lt == qt0 + per) {
-          lt = qt0;
-          ++lh;
-        }
-      };
-      int loaded = 0, in_head = 0, tails = 0;
-      for (; loaded < np && loaded < NR; ++loaded) load(loaded);
+      int in_head = 0, tails = 0;
       bool ok = mbar_wait(own, 0, abort_flag);
       for (int p = 0; ok && p < np; ++p) {
-        // S^T of step p once dV has read P^T of step p-1 from its columns
-        if (!mbar_wait(full + 8 * (p % NR), (p / NR) & 1, abort_flag)) {
-          ok = false;
-          break;
-        }
+        const uint32_t cS = 128u * (p & 1), cDP = 128u - cS;
+        ok = mbar_wait(full + 8 * (p % NR), (p / NR) & 1, abort_flag);
+        if (!ok) break;
         if (++in_head == per) {
           in_head = 0;
           if (has_tail) {
             mbar_arrive(fix_go);
-            if (!mbar_wait(fixed, tails & 1, abort_flag)) {
-              ok = false;
-              break;
-            }
+            ok = mbar_wait(fixed, tails & 1, abort_flag);
+            if (!ok) break;
             ++tails;
           }
         }
-        if (p > 0 && !mbar_wait(xv_free, (p - 1) & 1, abort_flag)) {
-          ok = false;
-          break;
-        }
+        // S^T once the groups have read dP^T of step p-1 from its region
+        if (p > 0) ok = mbar_wait(dp_read, (p - 1) & 1, abort_flag);
+        if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (kk / 4) * C::BOX + (kk % 4) * 32;
-          tc_mma_ss(tmem + C::COL_ST, sdesc_sw128(sK + off, 16, 1024),
+          tc_mma_ss(tmem + cS, sdesc_sw128(sK + off, 16, 1024),
                     sdesc_sw128(qslot(p) + off, 16, 1024), idesc_s, kk > 0);
         }
         tc_commit(s_ready);
         mbar_arrive(st_issued);
-        // dP^T once dK has read dS^T of step p-1; step p+1 goes into the slot
-        // of step p-1 as soon as both its accumulations have finished
-        if (p > 0 && !mbar_wait(xk_free, (p - 1) & 1, abort_flag)) {
-          ok = false;
-          break;
-        }
-        if (p >= 1 && p + 1 < np) {
-          load(p + 1);
-          loaded = p + 2;
-        }
+        // dP^T once the accumulations of step p-1 have read P^T and dS^T from its region
+        if (p > 0) ok = mbar_wait(x_free, (p - 1) & 1, abort_flag);
+        if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (kk / 4) * C::BOX + (kk % 4) * 32;
-          tc_mma_ss(tmem + C::COL_DPT, sdesc_sw128(sV + off, 16, 1024),
+          tc_mma_ss(tmem + cDP, sdesc_sw128(sV + off, 16, 1024),
                     sdesc_sw128(doslot(p) + off, 16, 1024), idesc_s, kk > 0);
         }
         tc_commit(dp_ready);
       }
-      if (!ok) {
-        report_timeout(abort_flag, io.status);
-        // the newest copies may still be landing
-        mbar_wait(own, 0, nullptr, 200000000ull);
-        for (int pp = loaded > NR ? loaded - NR : 0; pp < loaded; ++pp)
-          mbar_wait(full + 8 * (pp % NR), (pp / NR) & 1, nullptr, 200000000ull);
-      }
+      if (!ok) report_timeout(abort_flag, io.status);
       tc_commit(done);
       tc_commit(drain);
       mbar_wait(drain, 0, nullptr, 200000000ull);
     }
     __syncwarp();
   } else if (warp == 10) {
-    // ---- dV += P^T_w dO_w as each group's P^T is in, then (after the next
-    // step's S^T, so that the groups' next P^T is not held up) dK += dS^T_w
-    // Q_w; B read N-major
+    // ---- dV += P^T_w dO_w as each group's P^T is in, then dK += dS^T_w Q_w;
+    // B read N-major
     if (lane == 0 && np > 0) {
       constexpr uint32_t idesc_acc = idesc_f32<T>(128, D, true);
       bool ok = true;
       // test hook: with `stall` set no accumulation is issued (the timeout path)
       for (int p = 0; ok && p < np && !io.stall; ++p) {
-        for (int h = 0; h < 2; ++h) {
-          if (!mbar_wait(p_ready + 8 * h, p & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
+        const uint32_t cS = 128u * (p & 1);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {  // dV of the two groups, dK of the two
+          const int h = x & 1;
+          // dK is queued behind the next S^T, which the groups wait for first
+          if (x == 2 && p + 1 < np) ok = ok && mbar_wait(st_issued, (p + 1) & 1, abort_flag);
+          ok = ok && mbar_wait((x < 2 ? p_ready : ds_ready) + 8 * h, p & 1, abort_flag);
+          if (!ok) break;
           tc_fence_after();
+          const uint32_t rows = (x < 2 ? doslot(p) : qslot(p)) + h * 8192;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc_mma_ts(tmem + C::COL_DV, tmem + C::COL_ST + 64u * h + 8u * kk,
-                      sdesc_sw128(doslot(p) + h * 8192 + kk * 2048, C::BOX, 1024), idesc_acc,
+            tc_mma_ts(tmem + (x < 2 ? C::COL_DV : C::COL_DK),
+                      tmem + cS + 64u * h + (x < 2 ? 0u : 32u) + 8u * kk,
+                      sdesc_sw128(rows + kk * 2048, C::BOX, 1024), idesc_acc,
                       (p > 0 || h > 0 || kk > 0) ? 1u : 0u);
         }
         if (!ok) break;
-        tc_commit(xv_free);
-        if (p + 1 < np && !mbar_wait(st_issued, (p + 1) & 1, abort_flag)) {
-          ok = false;
-          break;
-        }
-        for (int h = 0; h < 2; ++h) {
-          if (!mbar_wait(ds_ready + 8 * h, p & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_ts(tmem + C::COL_DK, tmem + C::COL_DPT + 64u * h + 8u * kk,
-                      sdesc_sw128(qslot(p) + h * 8192 + kk * 2048, C::BOX, 1024), idesc_acc,
-                      (p > 0 || h > 0 || kk > 0) ? 1u : 0u);
-        }
-        if (!ok) break;
-        tc_commit(xk_free);
+        tc_commit(x_free);
       }
       if (!ok) report_timeout(abort_flag, io.status);
       tc_commit(done);
@@ -796,11 +845,11 @@ __global__ void __launch_bounds__(352, 1)
     const float fac = kHalf && np > 0 ? ds_factor(io.norms, kvh, g.kv_heads) : 1.f;
     const float fac_p = kHalf ? fac * exp2f(-kPShift) : 1.f;
     const float shift = kHalf ? kPShift : 0.f;
-    const uint32_t tS = tmem + C::COL_ST + 64u * grp + lane_base;
-    const uint32_t tDP = tmem + C::COL_DPT + 64u * grp + lane_base;
     bool ok = true;
     int qt = qt0;
     for (int p = 0; p < np; ++p) {
+      const uint32_t tS = tmem + 128u * (p & 1) + 64u * grp + lane_base;
+      const uint32_t tDP = tmem + 128u * ((p & 1) ^ 1) + 64u * grp + lane_base;
       ok = __all_sync(0xffffffffu, mbar_wait(s_ready, p & 1, abort_flag));
       if (!ok) break;
       tc_fence_after();
@@ -848,13 +897,19 @@ __global__ void __launch_bounds__(352, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(p_ready + 8 * grp);
-      // dS^T = P^T * (dP^T - D) over dP^T, 32 columns at a time
+      // dS^T = P^T * (dP^T - D) beside P^T, 32 columns at a time
       ok = __all_sync(0xffffffffu, mbar_wait(dp_ready, p & 1, abort_flag));
       if (!ok) break;
       tc_fence_after();
 #pragma unroll
       for (int h2 = 0; h2 < 2; ++h2) {
         BSA_TMEM_LD32(tDP + 32u * h2, (dp + 32 * h2));
+        if (h2 == 1) {
+          // dP^T read: the next S^T may go over it
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(dp_read);
+        }
         uint32_t pk[16];
 #pragma unroll
         for (int c4 = 8 * h2; c4 < 8 * h2 + 8; ++c4) {
@@ -872,7 +927,7 @@ __global__ void __launch_bounds__(352, 1)
             pk[(c - 32 * h2) / 2] = pack2<T>(d0, d1);
           }
         }
-        BSA_TMEM_ST16(tDP + 16u * h2, pk);
+        BSA_TMEM_ST16(tS + 32u + 16u * h2, pk);
       }
       tc_fence_before();
       __syncwarp();
@@ -885,13 +940,15 @@ __global__ void __launch_bounds__(352, 1)
       // group 0 writes dV, group 1 dK; keys no query saw have zero gradients
       tc_fence_after();
       const Rows& out = grp ? io.dk : io.dv;
-      T* dst = static_cast<T*>(out.p) + int64_t(k0 + kr) * out.sn + int64_t(kvh) * out.sh;
       const float f = grp ? g.scale / fac : (kHalf ? exp2f(-kPShift) : 1.f);
+      if (any) {
+        const int row0 = first + quad * 32;  // the warp's first row
+        T* dst = static_cast<T*>(out.p) + int64_t(k0 + row0) * out.sn + int64_t(kvh) * out.sh;
 #pragma unroll 1
-      for (int ch = 0; ch < D / 32; ++ch) {
-        uint32_t a[32];
-        BSA_TMEM_LD32(tmem + (grp ? C::COL_DK : C::COL_DV) + 32u * ch + lane_base, a);
-        if (exists) store_chunk<T>(dst + 32 * ch, a, f, np > 0);
+        for (int c = 0; c < D / 64; ++c)
+          write_channels<T>(sK + warp * 4096,
+                            tmem + (grp ? C::COL_DK : C::COL_DV) + 64u * c + lane_base,
+                            dst + 64 * c, out.sn, min(32, Lk - row0), f, np > 0, lane);
       }
     }
   }
@@ -926,7 +983,7 @@ cudaError_t launch_t(const SeqGeo& g, const CUtensorMap* maps, const PackedBwdIO
     e = allow_smem(dq, DqCfg<D>::SMEM, seen);
     if (e != cudaSuccess) return e;
     dq<<<unsigned(tiles(io.total_q) * g.heads), DqCfg<D>::kThreads, DqCfg<D>::SMEM, st>>>(
-        maps[0], maps[1], maps[2], g, io);
+        maps[0], maps[1], maps[2], maps[3], g, io);
   }
   if (io.total_k > 0) {
     auto dkdv = packed_dkdv_kernel<T, D>;
