@@ -102,8 +102,50 @@ __device__ __forceinline__ void write_channels(uint32_t stage, uint32_t tcol, T*
 // ============================================================================
 // D = rowsum(dO * O), the statistics' layout, and the norms for fp16
 // ============================================================================
+// largest squared norm of a V row per kv head (fp16): block `part` of `parts`
+template <int D>
+__device__ __forceinline__ void v_norms(const SeqGeo& g, const PackedBwdIO& io, int part, int parts,
+                                        int kvh) {
+  constexpr int TPR = D / 8;
+  const int lane = threadIdx.x & 31;
+  // rows that a sequence owns: from the first offset to the last
+  const int64_t lo = max(0, __ldg(io.cu_k)), hi = min(int64_t(__ldg(io.cu_k + io.n_seqs)), io.total_k);
+  float most = 0.f;
+  for (int64_t r0 = lo + int64_t(part) * (256 / TPR); r0 < hi; r0 += int64_t(parts) * (256 / TPR)) {
+    const int64_t r = r0 + threadIdx.x / TPR;
+    float sq = 0.f;
+    if (r < hi) {
+      const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const __half*>(io.v.p) + r * io.v.sn +
+                                                      int64_t(kvh) * io.v.sh + (threadIdx.x % TPR) * 8);
+      const uint32_t av[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 x = unpack2<__half>(av[i]);
+        sq = fmaf(x.x, x.x, sq);
+        sq = fmaf(x.y, x.y, sq);
+      }
+    }
+#pragma unroll
+    for (int o = TPR / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+    most = fmaxf(most, sq);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  if (lane == 0)
+    atomicMax(reinterpret_cast<int*>(io.norms) + g.kv_heads + kvh, __float_as_int(most));
+}
+
 template <typename T, int D>
-__global__ void __launch_bounds__(256) bwd_prepare_kernel(SeqGeo g, const PackedBwdIO io) {
+__global__ void __launch_bounds__(256) bwd_prepare_kernel(SeqGeo g, const PackedBwdIO io,
+                                                          int tiles) {
+  if constexpr (std::is_same<T, __half>::value) {
+    // the blocks behind the tiles' look at V
+    if (int(blockIdx.x) >= tiles) {
+      if (int(blockIdx.y) < g.kv_heads)
+        v_norms<D>(g, io, int(blockIdx.x) - tiles, int(gridDim.x) - tiles, blockIdx.y);
+      return;
+    }
+  }
   constexpr int TPR = D / 8;  // threads per row, 16 bytes each
   __shared__ int where[5];    // any, sequence, tile, first row, length
   __shared__ float top[8];
@@ -171,40 +213,6 @@ __global__ void __launch_bounds__(256) bwd_prepare_kernel(SeqGeo g, const Packed
   }
 }
 
-// largest squared norm of a V row per kv head (fp16)
-template <int D>
-__global__ void __launch_bounds__(256) bwd_vnorm_kernel(SeqGeo g, const PackedBwdIO io) {
-  constexpr int TPR = D / 8;
-  const int lane = threadIdx.x & 31, kvh = blockIdx.y;
-  // rows that a sequence owns, taking the offsets' ends (gaps do not occur)
-  const int64_t lo = max(0, __ldg(io.cu_k)), hi = min(int64_t(__ldg(io.cu_k + io.n_seqs)), io.total_k);
-  float most = 0.f;
-  const int64_t step = int64_t(gridDim.x) * (256 / TPR);
-  const int64_t first = lo + int64_t(blockIdx.x) * (256 / TPR);
-  for (int64_t r0 = first; r0 < hi; r0 += step) {
-    const int64_t r = r0 + threadIdx.x / TPR;
-    float sq = 0.f;
-    if (r < hi) {
-      const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const __half*>(io.v.p) + r * io.v.sn +
-                                                      int64_t(kvh) * io.v.sh + (threadIdx.x % TPR) * 8);
-      const uint32_t av[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 x = unpack2<__half>(av[i]);
-        sq = fmaf(x.x, x.x, sq);
-        sq = fmaf(x.y, x.y, sq);
-      }
-    }
-#pragma unroll
-    for (int o = TPR / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-    most = fmaxf(most, sq);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-  if (lane == 0)
-    atomicMax(reinterpret_cast<int*>(io.norms) + g.kv_heads + kvh, __float_as_int(most));
-}
-
 // ============================================================================
 // dQ: CTA = 128 query rows of a head
 // ============================================================================
@@ -257,6 +265,7 @@ __global__ void __launch_bounds__(384, 1)
   int* found = reinterpret_cast<int*>(sm + C::OFF_MISC + 8);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int head = int(blockIdx.x % uint32_t(g.heads)), kvh = head / g.group;
+  cudaTriggerProgrammaticLaunchCompletion();  // see the launch of dK/dV
   auto kslot = [&](int p) { return base + C::OFF_K + (p % NK) * C::TILE; };
   auto vslot = [&](int p) { return base + C::OFF_V + (p % NV) * C::TILE; };
 
@@ -958,6 +967,7 @@ __global__ void __launch_bounds__(384, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
+  cudaGridDependencySynchronize();  // dQ has finished, too
 }
 
 template <typename T, int D>
@@ -968,16 +978,16 @@ cudaError_t launch_t(const SeqGeo& g, const CUtensorMap* maps, const PackedBwdIO
   };
   cudaError_t e;
   if (io.total_q > 0) {
+    const int64_t n_tiles = tiles(io.total_q);
+    int64_t v_blocks = 0;
     if (std::is_same<T, __half>::value) {
       e = cudaMemsetAsync(io.norms, 0, 2 * sizeof(float) * g.kv_heads, st);
       if (e != cudaSuccess) return e;
-      if (io.total_k > 0) {
-        int64_t blocks = (io.total_k + 255) / 256;
-        blocks = blocks < 256 ? blocks : 256;
-        bwd_vnorm_kernel<D><<<dim3(unsigned(blocks), g.kv_heads), 256, 0, st>>>(g, io);
-      }
+      v_blocks = (io.total_k + 255) / 256;
+      v_blocks = v_blocks < 256 ? v_blocks : 256;
     }
-    bwd_prepare_kernel<T, D><<<dim3(unsigned(tiles(io.total_q)), g.heads), 256, 0, st>>>(g, io);
+    bwd_prepare_kernel<T, D>
+        <<<dim3(unsigned(n_tiles + v_blocks), g.heads), 256, 0, st>>>(g, io, int(n_tiles));
     auto dq = packed_dq_kernel<T, D>;
     static std::atomic<uint64_t> seen{0};
     e = allow_smem(dq, DqCfg<D>::SMEM, seen);
@@ -990,8 +1000,23 @@ cudaError_t launch_t(const SeqGeo& g, const CUtensorMap* maps, const PackedBwdIO
     static std::atomic<uint64_t> seen{0};
     e = allow_smem(dkdv, DkdvCfg<D>::SMEM, seen);
     if (e != cudaSuccess) return e;
-    dkdv<<<unsigned(tiles(io.total_k) * g.kv_heads), DkdvCfg<D>::kThreads, DkdvCfg<D>::SMEM, st>>>(
-        maps[0], maps[1], maps[2], maps[3], g, io);
+    // dK/dV needs the preparation's results, not dQ's: it may start when the
+    // last dQ tiles have started (which was after the preparation), on the SMs
+    // that dQ leaves idle, and ends after dQ
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(tiles(io.total_k) * g.kv_heads));
+    cfg.blockDim = dim3(DkdvCfg<D>::kThreads);
+    cfg.dynamicSmemBytes = DkdvCfg<D>::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = io.total_q > 0 ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, dkdv, maps[0], maps[1], maps[2], maps[3], g, io);
+    if (e != cudaSuccess) return e;
   }
   return cudaGetLastError();
 }
