@@ -11,6 +11,12 @@ shaped [rows, heads, head_dim] with head_dim contiguous and the other
 strides multiples of 8 elements; offsets, lengths and block tables are
 int32.  Calls run on that GPU, on its current stream unless `stream` is
 given, whatever device is current.
+
+    prob = SeqProblem.make(heads=32, kv_heads=8, head_dim=128)
+    layer = PagedAttention(prob, n_pages=4096, page_size=16, max_seqs=64, max_pages_per_seq=64)
+    layer.block_table.copy_(pages)                      # which pages each sequence has
+    out = layer.prompt(q, k, v, cu, rope=table)         # caches the prompts, attends causally
+    out = layer.step(q1, k1, v1, rope=table)            # one new token per sequence
 """
 import ctypes
 import math
@@ -18,7 +24,7 @@ import struct
 
 import torch
 
-from . import _check, lib as _base_lib
+from . import BSAError, _check, lib as _base_lib
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 
@@ -156,19 +162,28 @@ def _lse_ptr(heads, t, rows, dev):
     return t.data_ptr()
 
 
+# the current stream's handle without a Stream object (1.1 us of a 10 us call)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _call(name, dev, stream, prob, args, dev_status):
     """The entry point on device `dev` and `stream` (its current one by default)."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        stream = _current_stream(dev)
     elif stream.device_index != dev:
         raise ValueError("stream belongs to cuda:%d, the tensors to cuda:%d"
                          % (stream.device_index, dev))
+    else:
+        stream = stream.cuda_stream
     f, st = _fn(name), _status_ptr(dev_status, dev)
     if torch.cuda.current_device() == dev:
-        _check(f(prob, args, st, stream.cuda_stream))
+        rc = f(prob, args, st, stream)
     else:
         with torch.cuda.device(dev):
-            _check(f(prob, args, st, stream.cuda_stream))
+            rc = f(prob, args, st, stream)
+    if rc:
+        _check(rc)
 
 
 def _query(name, *args):
@@ -272,5 +287,62 @@ def paged_attn_decode(prob, q, k_cache, v_cache, block_table, seq_lens, out, wor
     _call("bsa_paged_attn_decode", dev, stream, prob, args, dev_status)
 
 
-__all__ = ["SeqProblem", "packed_attn_fwd", "packed_bwd_workspace_bytes", "packed_attn_bwd",
+class PagedAttention:
+    """One attention layer's paged cache with its buffers, allocated once:
+    the pages, the block table and lengths of up to max_seqs sequences, the
+    decode workspace and a status word.  Pages are handed out by the caller:
+    write page numbers into `block_table` (int32 [max_seqs,
+    max_pages_per_seq]) before tokens reach them.
+
+    `seq_lens` holds the cached tokens of each sequence.  prompt() and step()
+    add the new tokens to it and run on every sequence of the cache in order,
+    as the model's batch does; a sequence without new tokens in a prompt()
+    call has length 0 in cu."""
+
+    def __init__(self, prob, n_pages, page_size, max_seqs, max_pages_per_seq, device="cuda"):
+        self.prob = prob
+        dev, dt = torch.device(device), prob.torch_dtype
+        shape = (n_pages, page_size, prob.kv_heads, prob.head_dim)
+        self.k_cache = torch.empty(shape, dtype=dt, device=dev)
+        self.v_cache = torch.empty(shape, dtype=dt, device=dev)
+        self.block_table = torch.zeros((max_seqs, max_pages_per_seq), dtype=torch.int32, device=dev)
+        self.seq_lens = torch.zeros(max_seqs, dtype=torch.int32, device=dev)
+        self.workspace = torch.empty(decode_workspace_bytes(prob), dtype=torch.uint8, device=dev)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self._step_cu = torch.arange(max_seqs + 1, dtype=torch.int32, device=dev)
+
+    def append(self, q, k, v, cu, rope=None, interleaved=False, rope_rows=None, k_out=None):
+        """Add packed tokens to the sequences; returns the rotated q."""
+        self.seq_lens += cu[1:] - cu[:-1]
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        kv_append(self.prob, k, v, self.k_cache, self.v_cache, self.block_table, cu, self.seq_lens,
+                  rope=rope, interleaved=interleaved, rope_rows=rope_rows, q=q, q_out=q_out,
+                  k_out=k_out, dev_status=self.status)
+        return q_out
+
+    def prompt(self, q, k, v, cu, rope=None, interleaved=False, rope_rows=None):
+        """Whole prompts of sequences that were empty: cache their keys and
+        values and return their causal attention (as prob.causal says)."""
+        k_rot = torch.empty_like(k, memory_format=torch.contiguous_format)
+        q_rot = self.append(q, k, v, cu, rope, interleaved, rope_rows, k_out=k_rot)
+        out = torch.empty_like(q_rot)
+        packed_attn_fwd(self.prob, q_rot, k_rot, v, cu, cu, out, dev_status=self.status)
+        return out
+
+    def step(self, q, k, v, rope=None, interleaved=False, rope_rows=None):
+        """One new token per sequence, q [max_seqs, heads, head_dim]: cache it
+        and return its attention over its sequence."""
+        q_rot = self.append(q, k, v, self._step_cu, rope, interleaved, rope_rows)
+        out = torch.empty_like(q_rot)
+        paged_attn_decode(self.prob, q_rot, self.k_cache, self.v_cache, self.block_table,
+                          self.seq_lens, out, self.workspace, dev_status=self.status)
+        return out
+
+    def check_status(self):
+        v = int(self.status.item())
+        if v:
+            raise BSAError(v, "device-side error reported by a sequence kernel")
+
+
+__all__ = ["SeqProblem", "PagedAttention", "packed_attn_fwd", "packed_bwd_workspace_bytes", "packed_attn_bwd",
            "kv_append", "decode_workspace_bytes", "paged_attn_decode"]

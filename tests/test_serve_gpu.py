@@ -1,0 +1,150 @@
+"""The sequence operators as a serving or training program uses them: prompts
+into the cache, then tokens one by one, against one 64-bit pass over the whole
+text; the steps captured once and replayed; and a training step's gradients
+against differences of its own forward."""
+import math
+
+import pytest
+import torch
+
+import block_sparse_attention_47_b200 as bsa
+from seq_helpers import HALF, assert_within, attention64, cu_of, output_bound, rope_table
+
+pytestmark = pytest.mark.gpu
+
+
+def turned(x, rope, pos):
+    """The rotation in 64 bits, rounded as the cache rounds it."""
+    half = rope.shape[1] // 2
+    c, s = rope.double()[pos][:, None, :half], rope.double()[pos][:, None, half:]
+    y = x.double().clone()
+    a, b = y[..., :half].clone(), y[..., half:2 * half].clone()
+    y[..., :half], y[..., half:2 * half] = a * c - b * s, b * c + a * s
+    return y
+
+
+def layer(prob, n_seqs, page=16, pages_each=40, seed=0):
+    n_pages = n_seqs * pages_each + 5
+    at = bsa.PagedAttention(prob, n_pages, page, n_seqs, pages_each)
+    at.k_cache.fill_(math.nan)
+    at.v_cache.fill_(math.nan)
+    order = torch.randperm(n_pages, generator=torch.Generator().manual_seed(seed))
+    at.block_table.copy_(order[:n_seqs * pages_each].reshape(n_seqs, pages_each).int())
+    return at
+
+
+def check_text(text, outs, prompts, rope, scale):
+    """outs[b]: attention outputs of every token of sequence b, in order."""
+    for b, (q, k, v) in enumerate(text):
+        n, H, K = outs[b].shape[0], q.shape[1], k.shape[1]
+        pos = torch.arange(n, device=q.device)
+        qr, kr = turned(q[:n], rope, pos), turned(k[:n], rope, pos)
+        # the rotated operands are themselves rounded: half a step of each of
+        # q and k moves a score by up to 2 u scale sum |q_c k_c|
+        u = HALF[q.dtype]
+        for h in range(H):
+            kk, vv = kr[:, h // (H // K)], v[:n, h // (H // K)]
+            o, _, p, g = attention64(qr[:, h], kk, vv, pos.cpu() + 1, scale)
+            g = g + 2.02 * u * scale * float((qr[:, h].abs() @ kk.abs().t()).max())
+            assert_within(outs[b][:, h], o, output_bound(o, p, vv, g, q.dtype), "sequence %d head %d" % (b, h))
+
+
+@pytest.mark.parametrize("H,K,d,dt", [(8, 2, 128, torch.bfloat16), (6, 6, 64, torch.float16)])
+def test_prompts_then_tokens(cuda_ok, H, K, d, dt):
+    prompts, steps = [130, 1, 300], 20
+    gen = torch.Generator().manual_seed(4)
+    text = [tuple(torch.randn(n + steps, x, d, generator=gen).to(dt).cuda() for x in (H, K, K)) for n in prompts]
+    prob = bsa.SeqProblem.make(H, K, d, dt)
+    at, rope = layer(prob, len(prompts)), rope_table(512, d)
+    cu = cu_of(prompts)
+    first = [torch.cat([t[i][:n] for t, n in zip(text, prompts)]) for i in range(3)]
+    out = at.prompt(*first, cu, rope=rope)
+    outs = [[o] for o in out.split(prompts)]
+    # the generation step is captured once and replayed
+    q1, k1, v1 = (torch.empty(len(prompts), x, d, dtype=dt, device="cuda") for x in (H, K, K))
+
+    def feed(i):
+        for src, dst in zip(range(3), (q1, k1, v1)):
+            dst.copy_(torch.stack([t[src][n + i] for t, n in zip(text, prompts)]))
+
+    feed(0)
+    outs = [o + [s[None].clone()] for o, s in zip(outs, at.step(q1, k1, v1, rope=rope))]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        one = at.step(q1, k1, v1, rope=rope)
+    for i in range(1, steps):
+        feed(i)
+        g.replay()
+        outs = [o + [s[None].clone()] for o, s in zip(outs, one)]
+    at.check_status()
+    assert at.seq_lens.tolist() == [n + steps for n in prompts]
+    check_text(text, [torch.cat(o) for o in outs], prompts, rope, 1 / math.sqrt(d))
+
+
+def test_pages_run_out(cuda_ok):
+    """Tokens behind a sequence's last page are refused through the status."""
+    prob = bsa.SeqProblem.make(2, 2, 64)
+    at = layer(prob, 1, page=4, pages_each=2)
+    x = torch.randn(8, 2, 64, device="cuda").bfloat16()
+    at.prompt(x, x, x, cu_of([8]))
+    at.check_status()
+    at.step(x[:1], x[:1], x[:1])
+    with pytest.raises(bsa.BSAError, match="INVALID_ARG"):
+        at.check_status()
+
+
+def test_other_stream(cuda_ok):
+    """Calls on a stream that is not the current one."""
+    prob = bsa.SeqProblem.make(4, 2, 128)
+    q = torch.randn(500, 4, 128, device="cuda").bfloat16()
+    k, v = (torch.randn(500, 2, 128, device="cuda").bfloat16() for _ in range(2))
+    cu, want, got = cu_of([200, 300]), torch.empty_like(q), torch.empty_like(q)
+    bsa.packed_attn_fwd(prob, q, k, v, cu, cu, want)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    bsa.packed_attn_fwd(prob, q, k, v, cu, cu, got, stream=s)
+    s.synchronize()
+    assert torch.equal(want, got)
+
+
+def test_gradients_against_differences(cuda_ok):
+    """sum(w * out) of the forward itself, in fp16, moved along a direction:
+    the central difference against the gradients' inner product.  A difference
+    of two rounded sums is off by at most 2 u sum |w out| / (2 h), and the
+    third-order term is removed by halving h (Richardson)."""
+    lens, H, K, d, dt = [70, 129], 4, 2, 64, torch.float16
+    gen = torch.Generator().manual_seed(9)
+    q, k, v, w = (torch.randn(sum(lens), x, d, generator=gen).to(dt).cuda() for x in (H, K, K, H))
+    prob, cu = bsa.SeqProblem.make(H, K, d, dt), cu_of(lens)
+    out, lse = torch.empty_like(q), torch.empty(H, sum(lens), device="cuda")
+    bsa.packed_attn_fwd(prob, q, k, v, cu, cu, out, lse)
+    grads = [torch.empty_like(t) for t in (q, k, v)]
+    ws = torch.empty(bsa.packed_bwd_workspace_bytes(prob, sum(lens), 2), dtype=torch.uint8, device="cuda")
+    bsa.packed_attn_bwd(prob, q, k, v, out, w, lse, cu, cu, *grads, ws)
+
+    def loss(a, b, c):
+        o = torch.empty_like(q)
+        bsa.packed_attn_fwd(prob, a, b, c, cu, cu, o)
+        return float((o.double() * w.double()).sum())
+
+    u = HALF[dt]
+    for i, gr in enumerate(grads):
+        base = [q, k, v]
+        # a direction along the gradient: its inner product is far above the noise
+        way = gr.double() / gr.double().norm() * 8.0
+        ds, moved = [], []
+        for h in (0.5, 0.25):
+            up, down = [list(base) for _ in range(2)]
+            up[i], down[i] = (base[i].double() + h * way).to(dt), (base[i].double() - h * way).to(dt)
+            ds.append((loss(*up) - loss(*down)) / (2 * h))
+            # the step actually taken, after rounding the moved operand
+            moved.append(float((gr.double() * (up[i].double() - down[i].double())).sum()) / (2 * h))
+        exact = float((gr.double() * way).sum())
+        # outputs are rounded independently: the noise of a sum of n products
+        # w o with errors up to 2 u |o| is within 4 sqrt(n) of its rms terms
+        n = q.numel()
+        noise = 4 * math.sqrt(n) * 2 * u * float((w.double() * out.double()).pow(2).mean().sqrt()) / (2 * 0.25)
+        slack = abs(ds[0] - ds[1]) + noise + 4 * u * abs(exact) + max(abs(m - exact) for m in moved)
+        assert abs(ds[1] - moved[1]) <= slack, (i, ds, moved, slack)
+        assert slack <= 0.2 * abs(exact), (i, slack, exact)
