@@ -9,7 +9,9 @@
 // the lengths, so one long sequence uses the whole GPU and a ragged batch
 // leaves no SM idle.  A share that covers a (sequence, head group) whole
 // writes its output; the others leave (max, sum, O) in the workspace, two
-// slots per CTA, and a second kernel joins them in position order.
+// slots per CTA, and a second kernel joins them in position order.  Where no
+// sequence can be longer than 512 keys and the (sequence, head group) pairs
+// fit the SMs, each takes a CTA whole and there is nothing to join.
 //
 // In a CTA four warps take every fourth unit.  Each has its own ring of
 // 16-byte asynchronous copies (K and V rows, zero-filled behind the length, so
@@ -27,6 +29,9 @@ constexpr int kDecWarps = 4;
 constexpr int kUnit = 32;       // keys
 constexpr int kMaxCtas = 160;   // workspace slots are sized for this many
 constexpr int kHeadTile = 16;   // query heads of one kv head per CTA pass
+// up to here one CTA a (sequence, head group): 4 units a warp cost less than
+// the second kernel (300 keys, 2 kv heads: 5.4 against 7.9 us)
+constexpr int kWholeKeys = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
@@ -126,9 +131,24 @@ __device__ __forceinline__ int64_t active_ctas(int64_t total, int64_t n) {
   return a < 1 ? 1 : (a < n ? a : n);
 }
 
+// a (sequence, head group) without a key: its output is 0
+template <typename T, int D>
+__device__ __forceinline__ void zero_output(const SeqGeo& g, const DecodeIO& io, int b, int hg) {
+  const int hsub = (g.group + kHeadTile - 1) / kHeadTile;
+  const int kvh = hg / hsub, row0 = (hg - kvh * hsub) * kHeadTile;
+  const int rows = min(kHeadTile, g.group - row0);
+  T* out = static_cast<T*>(io.o.p) + int64_t(b) * io.o.sn +
+           (int64_t(kvh) * g.group + row0) * io.o.sh;
+  for (int i = threadIdx.x; i < rows * (D / 8); i += blockDim.x) {
+    const int r = i / (D / 8);
+    *reinterpret_cast<uint4*>(out + r * io.o.sh + (i - r * (D / 8)) * 8) =
+        make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kDecWarps, 1)
-    paged_decode_kernel(SeqGeo g, PagedCache c, const DecodeIO io, Shape sh) {
+    paged_decode_kernel(SeqGeo g, PagedCache c, const DecodeIO io, Shape sh, bool whole) {
   using C = DecCfg<D>;
   constexpr int kThreads = 32 * kDecWarps;
   constexpr int CH = D / 8;  // 16-byte chunks of a row
@@ -142,38 +162,57 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
   cudaTriggerProgrammaticLaunchCompletion();
 
   // ---- this CTA's share [s, e) of the units, and where s lies
-  const int per = (sh.n_seqs + kThreads - 1) / kThreads;
-  const int b_lo = min(sh.n_seqs, int(threadIdx.x) * per), b_hi = min(sh.n_seqs, b_lo + per);
-  int64_t mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) {
-    mine += int64_t(sh.units(b)) * sh.hgroups;
-    if (blockIdx.x == 0) {
-      const int n = __ldg(sh.lens + b);
-      if (n < 0 || n > sh.max_len) report_invalid(io.status);
-    }
-  }
-  int64_t total;
-  const int64_t before = block_scan<kThreads>(mine, scratch, total);
-  const int64_t active = active_ctas(total, gridDim.x);
+  int b0, hg0;
+  int64_t s, e, rem0;
   const int64_t cta = blockIdx.x;
-  const int64_t s = cta < active ? total * cta / active : total;
-  const int64_t e = cta < active ? total * (cta + 1) / active : total;
-  if (s >= e) return;
-  int* where = reinterpret_cast<int*>(scratch + kDecWarps);  // b, then units before it
-  if (before <= s && s < before + mine) {
-    int64_t at = before;
-    int b = b_lo;
-    for (;; ++b) {
-      const int64_t u = int64_t(sh.units(b)) * sh.hgroups;
-      if (s < at + u) break;
-      at += u;
+  if (whole) {
+    b0 = int(blockIdx.x) / sh.hgroups;
+    hg0 = int(blockIdx.x) - b0 * sh.hgroups;
+    const int n = __ldg(sh.lens + b0);
+    if (threadIdx.x == 0 && (n < 0 || n > sh.max_len)) report_invalid(io.status);
+    s = 0;
+    e = sh.units(b0);
+    rem0 = 0;
+    if (e == 0) {
+      zero_output<T, D>(g, io, b0, hg0);
+      return;
     }
-    where[0] = b;
-    *reinterpret_cast<int64_t*>(where + 2) = at;
+  } else {
+    const int per = (sh.n_seqs + kThreads - 1) / kThreads;
+    const int b_lo = min(sh.n_seqs, int(threadIdx.x) * per), b_hi = min(sh.n_seqs, b_lo + per);
+    int64_t mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) {
+      mine += int64_t(sh.units(b)) * sh.hgroups;
+      if (blockIdx.x == 0) {
+        const int n = __ldg(sh.lens + b);
+        if (n < 0 || n > sh.max_len) report_invalid(io.status);
+      }
+    }
+    int64_t total;
+    const int64_t before = block_scan<kThreads>(mine, scratch, total);
+    const int64_t active = active_ctas(total, gridDim.x);
+    s = cta < active ? total * cta / active : total;
+    e = cta < active ? total * (cta + 1) / active : total;
+    if (s >= e) return;
+    int* where = reinterpret_cast<int*>(scratch + kDecWarps);  // b, then units before it
+    if (before <= s && s < before + mine) {
+      int64_t at = before;
+      int b = b_lo;
+      for (;; ++b) {
+        const int64_t u = int64_t(sh.units(b)) * sh.hgroups;
+        if (s < at + u) break;
+        at += u;
+      }
+      where[0] = b;
+      *reinterpret_cast<int64_t*>(where + 2) = at;
+    }
+    __syncthreads();
+    b0 = where[0];
+    rem0 = s - *reinterpret_cast<int64_t*>(where + 2);
+    const int n = sh.units(b0);
+    hg0 = int(rem0 / n);
+    rem0 -= int64_t(hg0) * n;
   }
-  __syncthreads();
-  const int b0 = where[0];
-  const int64_t rem0 = s - *reinterpret_cast<int64_t*>(where + 2);
 
   // ---- the copies: this warp's units s + warp, s + warp + 4, .. of the list
   struct {
@@ -198,8 +237,8 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
   p.b = b0;
   p.len = sh.len(b0);
   p.n_units = (p.len + kUnit - 1) / kUnit;
-  p.hg = int(rem0 / p.n_units);
-  p.unit = int(rem0 - int64_t(p.hg) * p.n_units) + warp;
+  p.hg = hg0;
+  p.unit = int(rem0) + warp;
   if (p.idx < e) settle();
   // the page of this lane's key in the next unit, fetched one unit ahead
   int page = 0, tok = 0;
@@ -251,8 +290,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
   int get = 0;
   int64_t idx = s, widx = s + warp;
   int b = b0, len = sh.len(b0), n_units = (len + kUnit - 1) / kUnit;
-  int hg = int(rem0 / n_units);
-  int unit0 = int(rem0 - int64_t(hg) * n_units);
+  int hg = hg0, unit0 = int(rem0);
   while (idx < e) {
     const int64_t pe = min(e, idx + (n_units - unit0));
     const int kvh = hg / hsub, row0 = (hg - kvh * hsub) * kHeadTile;
@@ -377,7 +415,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
         *reinterpret_cast<float2*>(row + 8 * i) = make_float2(acc[i][2 * hf], acc[i][2 * hf + 1]);
     }
     __syncthreads();
-    const bool whole = unit0 == 0 && pe - idx == n_units;
+    const bool entire = unit0 == 0 && pe - idx == n_units;
     // slot 0: a share that began in an earlier CTA; slot 1: one that goes on in the next
     float* slot = static_cast<float*>(io.workspace) + (cta * 2 + (unit0 == 0 ? 1 : 0)) * C::SLOT;
     for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
@@ -398,7 +436,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
         o.z = fmaf(x.z, f, o.z);
         o.w = fmaf(x.w, f, o.w);
       }
-      if (whole) {
+      if (entire) {
         const float inv = 1.f / ll;
         T* dst = static_cast<T*>(io.o.p) + int64_t(b) * io.o.sn + (head0 + r) * io.o.sh + col;
         *reinterpret_cast<uint2*>(dst) =
@@ -454,12 +492,8 @@ __global__ void __launch_bounds__(128)
   const int rows = min(kHeadTile, g.group - row0);
   T* out = static_cast<T*>(io.o.p) + int64_t(b) * io.o.sn +
            (int64_t(kvh) * g.group + row0) * io.o.sh;
-  if (n_units == 0) {  // no key: the output is 0
-    for (int i = threadIdx.x; i < rows * (D / 8); i += kThreads) {
-      const int r = i / (D / 8);
-      *reinterpret_cast<uint4*>(out + r * io.o.sh + (i - r * (D / 8)) * 8) =
-          make_uint4(0u, 0u, 0u, 0u);
-    }
+  if (n_units == 0) {
+    zero_output<T, D>(g, io, b, hg);
     return;
   }
   s0 += int64_t(hg) * n_units;
@@ -524,9 +558,12 @@ cudaError_t launch_t(const SeqGeo& g, const PagedCache& c, const DecodeIO& io, c
   static std::atomic<uint64_t> seen{0};
   cudaError_t e = allow_smem(kern, C::SMEM, seen);
   if (e != cudaSuccess) return e;
-  kern<<<ctas, 32 * kDecWarps, C::SMEM, st>>>(g, c, io, sh);
+  const int64_t pairs = int64_t(io.n_seqs) * sh.hgroups;
+  const bool whole = pairs <= ctas && sh.max_len <= kWholeKeys;
+  kern<<<whole ? unsigned(pairs) : unsigned(ctas), 32 * kDecWarps, C::SMEM, st>>>(g, c, io, sh,
+                                                                                  whole);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || whole) return e;
   // the join's launch overlaps the first kernel; it waits for its results itself
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(unsigned(io.n_seqs) * unsigned(sh.hgroups));
