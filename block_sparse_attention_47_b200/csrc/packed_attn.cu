@@ -220,8 +220,10 @@ __global__ void __launch_bounds__(384, 1)
     tmem_relinquish();
   } else if (warp == 8 && lane == 0) {
     tma_prefetch_desc(&mq);
-    tma_prefetch_desc(&mk);
-    tma_prefetch_desc(&mv);
+    if (io.total_k > 0) {  // else there are no maps
+      tma_prefetch_desc(&mk);
+      tma_prefetch_desc(&mv);
+    }
   }
   // the first entry is found during the set-up
   Tile next{};

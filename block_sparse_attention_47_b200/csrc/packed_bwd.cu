@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(384, 1)
   } else if (warp == 8) {
     tmem_alloc(smem_u32(tmem_holder), C::TMEM_COLS);
     tmem_relinquish();
-  } else if (warp == 11 && lane == 0) {
+  } else if (warp == 11 && lane == 0 && io.total_q > 0 && io.total_k > 0) {  // else no maps
     tma_prefetch_desc(&mq);
     tma_prefetch_desc(&mk);
     tma_prefetch_desc(&mv);
@@ -689,7 +689,7 @@ __global__ void __launch_bounds__(384, 1)
   } else if (warp == 8) {
     tmem_alloc(smem_u32(tmem_holder), C::TMEM_COLS);
     tmem_relinquish();
-  } else if (warp == 11 && lane == 0) {
+  } else if (warp == 11 && lane == 0 && io.total_q > 0 && io.total_k > 0) {  // else no maps
     tma_prefetch_desc(&mq);
     tma_prefetch_desc(&mk);
     tma_prefetch_desc(&mv);

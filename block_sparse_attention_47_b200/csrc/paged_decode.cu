@@ -3,17 +3,22 @@
 //
 // Bound by HBM: K and V are read once, 2 * len * kv_heads * d * 2 bytes.
 //
-// Split.  The work of a batch is the list of its 32-key units, ordered by
-// (sequence, group of up to 16 query heads that share a kv head, position).
-// The CTAs, one per SM, take equal consecutive shares of that list whatever
-// the lengths, so one long sequence uses the whole GPU and a ragged batch
-// leaves no SM idle.  A share that covers a (sequence, head group) whole
-// writes its output; the others leave (max, sum, O) in the workspace, two
-// slots per CTA, and a second kernel joins them in position order.  Where no
+// Split.  A head group is up to 16 query heads that share a kv head.  The work
+// of a batch is the list of its 32-key units, ordered by (sequence, set of
+// one, two or four head groups, position).  The CTAs, one per SM, take equal
+// consecutive shares of that list whatever the lengths, so one long sequence
+// uses the whole GPU and a ragged batch leaves no SM idle.  A share that
+// covers a (sequence, set) whole writes its output; the others leave (max,
+// sum, O) in the workspace, two slots per CTA and head group, and a second
+// kernel joins them in position order.  Where no
 // sequence can be longer than 512 keys and the (sequence, head group) pairs
 // fit the SMs, each takes a CTA whole and there is nothing to join.
 //
-// In a CTA four warps take every fourth unit.  Each has its own ring of
+// In a CTA the four warps take the same unit of the set's head groups, whose
+// rows lie side by side in token-major pages: with 16-token pages this reads
+// 6.03 TB/s where four warps on four units of one head group read 5.74 (with
+// 64-token pages 6.44 against 6.40).  Sets of fewer than four leave several
+// warps to a head group, on successive units.  Each warp has its own ring of
 // 16-byte asynchronous copies (K and V rows, zero-filled behind the length, so
 // whatever a page's tail holds is never read), and runs ahead over unit and
 // sequence borders.  Scores and P V go through m16n8k16 matrix instructions
@@ -30,7 +35,7 @@ constexpr int kUnit = 32;       // keys
 constexpr int kMaxCtas = 160;   // workspace slots are sized for this many
 constexpr int kHeadTile = 16;   // query heads of one kv head per CTA pass
 // up to here one CTA a (sequence, head group): 4 units a warp cost less than
-// the second kernel (300 keys, 2 kv heads: 5.4 against 7.9 us)
+// the second kernel (300 keys, 2 kv heads: 5.4 to 6.1 against 7.9 us)
 constexpr int kWholeKeys = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -94,6 +99,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 // ---- the list of units ---------------------------------------------------------
 struct Shape {
   int n_seqs, hgroups, max_len;  // hgroups: head groups per sequence
+  int hw, sets;                  // head groups of a set; sets per sequence
   const int32_t* lens;
   __device__ __forceinline__ int len(int b) const {
     const int n = __ldg(lens + b);
@@ -125,9 +131,10 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scratch, int64
   return base + x - v;
 }
 
-// CTAs that take part: at least four units each (one per warp)
-__device__ __forceinline__ int64_t active_ctas(int64_t total, int64_t n) {
-  const int64_t a = (total + kDecWarps - 1) / kDecWarps;
+// CTAs that take part: at least two units a warp
+__device__ __forceinline__ int64_t active_ctas(int64_t total, int64_t n, int hw) {
+  const int64_t least = 2 * kDecWarps / hw;
+  const int64_t a = (total + least - 1) / least;
   return a < 1 ? 1 : (a < n ? a : n);
 }
 
@@ -162,19 +169,21 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
   cudaTriggerProgrammaticLaunchCompletion();
 
   // ---- this CTA's share [s, e) of the units, and where s lies
-  int b0, hg0;
+  const int hw = sh.hw, pw = kDecWarps / hw;  // head groups; warps on one
+  const int hl = warp % hw, pl = warp / hw;
+  int b0, hg0;  // sequence and set
   int64_t s, e, rem0;
   const int64_t cta = blockIdx.x;
   if (whole) {
-    b0 = int(blockIdx.x) / sh.hgroups;
-    hg0 = int(blockIdx.x) - b0 * sh.hgroups;
+    b0 = int(blockIdx.x) / sh.sets;
+    hg0 = int(blockIdx.x) - b0 * sh.sets;
     const int n = __ldg(sh.lens + b0);
     if (threadIdx.x == 0 && (n < 0 || n > sh.max_len)) report_invalid(io.status);
     s = 0;
     e = sh.units(b0);
     rem0 = 0;
     if (e == 0) {
-      zero_output<T, D>(g, io, b0, hg0);
+      for (int i = 0; i < hw; ++i) zero_output<T, D>(g, io, b0, hg0 * hw + i);
       return;
     }
   } else {
@@ -182,7 +191,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
     const int b_lo = min(sh.n_seqs, int(threadIdx.x) * per), b_hi = min(sh.n_seqs, b_lo + per);
     int64_t mine = 0;
     for (int b = b_lo; b < b_hi; ++b) {
-      mine += int64_t(sh.units(b)) * sh.hgroups;
+      mine += int64_t(sh.units(b)) * sh.sets;
       if (blockIdx.x == 0) {
         const int n = __ldg(sh.lens + b);
         if (n < 0 || n > sh.max_len) report_invalid(io.status);
@@ -190,7 +199,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
     }
     int64_t total;
     const int64_t before = block_scan<kThreads>(mine, scratch, total);
-    const int64_t active = active_ctas(total, gridDim.x);
+    const int64_t active = active_ctas(total, gridDim.x, hw);
     s = cta < active ? total * cta / active : total;
     e = cta < active ? total * (cta + 1) / active : total;
     if (s >= e) return;
@@ -199,7 +208,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
       int64_t at = before;
       int b = b_lo;
       for (;; ++b) {
-        const int64_t u = int64_t(sh.units(b)) * sh.hgroups;
+        const int64_t u = int64_t(sh.units(b)) * sh.sets;
         if (s < at + u) break;
         at += u;
       }
@@ -214,7 +223,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
     rem0 -= int64_t(hg0) * n;
   }
 
-  // ---- the copies: this warp's units s + warp, s + warp + 4, .. of the list
+  // ---- the copies: this warp's units s + pl, s + pl + pw, .. of the list
   struct {
     int64_t idx;
     int b, hg, unit, n_units, len;
@@ -222,7 +231,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
   auto settle = [&] {  // unit may lie behind its (sequence, head group): move on
     while (p.unit >= p.n_units) {
       p.unit -= p.n_units;
-      if (++p.hg == sh.hgroups) {
+      if (++p.hg == sh.sets) {
         p.hg = 0;
         do {
           ++p.b;
@@ -233,12 +242,12 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
       }
     }
   };
-  p.idx = s + warp;
+  p.idx = s + pl;
   p.b = b0;
   p.len = sh.len(b0);
   p.n_units = (p.len + kUnit - 1) / kUnit;
   p.hg = hg0;
-  p.unit = int(rem0) + warp;
+  p.unit = int(rem0) + pl;
   if (p.idx < e) settle();
   // the page of this lane's key in the next unit, fetched one unit ahead
   int page = 0, tok = 0;
@@ -260,7 +269,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
         live = false;
       }
       const int64_t off = live ? int64_t(page) * c.sp + int64_t(tok) * c.st : -1;
-      const int64_t head = int64_t(p.hg / hsub) * c.sh;
+      const int64_t head = int64_t((p.hg * hw + hl) / hsub) * c.sh;
       const uint32_t dst0 = ring + put * C::STAGE;
       const int ch = lane % CH;
 #pragma unroll
@@ -272,8 +281,8 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
         cp_async16(dst, static_cast<const T*>(c.k) + src, o >= 0);
         cp_async16(dst + C::HALF, static_cast<const T*>(c.v) + src, o >= 0);
       }
-      p.idx += kDecWarps;
-      p.unit += kDecWarps;
+      p.idx += pw;
+      p.unit += pw;
       if (p.idx < e) {
         settle();
         look_up();
@@ -288,12 +297,12 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
   // ---- the shares of one (sequence, head group) after the other
   const float sl2 = g.scale * kLog2e;
   int get = 0;
-  int64_t idx = s, widx = s + warp;
+  int64_t idx = s, widx = s + pl;
   int b = b0, len = sh.len(b0), n_units = (len + kUnit - 1) / kUnit;
   int hg = hg0, unit0 = int(rem0);
   while (idx < e) {
     const int64_t pe = min(e, idx + (n_units - unit0));
-    const int kvh = hg / hsub, row0 = (hg - kvh * hsub) * kHeadTile;
+    const int hgi = hg * hw + hl, kvh = hgi / hsub, row0 = (hgi - kvh * hsub) * kHeadTile;
     const int rows = min(kHeadTile, g.group - row0);
     const int64_t head0 = int64_t(kvh) * g.group + row0;
     // Q as the A operand: rows lane/4 and +8, zero behind the group
@@ -317,7 +326,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
 
-    for (; widx < pe; widx += kDecWarps) {
+    for (; widx < pe; widx += pw) {
       cp_async_wait<C::STAGES - 2>();
       __syncwarp();
       produce();  // into the stage read in the previous turn
@@ -399,7 +408,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
       }
     }
 
-    // ---- the four warps' parts of this share
+    // ---- the parts of this share: pw warps each have one of a head group's
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 1);
@@ -414,20 +423,23 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
       for (int i = 0; i < D / 8; ++i)
         *reinterpret_cast<float2*>(row + 8 * i) = make_float2(acc[i][2 * hf], acc[i][2 * hf + 1]);
     }
-    __syncthreads();
+    if (pw > 1)
+      __syncthreads();
+    else
+      __syncwarp();
     const bool entire = unit0 == 0 && pe - idx == n_units;
     // slot 0: a share that began in an earlier CTA; slot 1: one that goes on in the next
-    float* slot = static_cast<float*>(io.workspace) + (cta * 2 + (unit0 == 0 ? 1 : 0)) * C::SLOT;
-    for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
+    float* slot = static_cast<float*>(io.workspace) +
+                  ((cta * 2 + (unit0 == 0 ? 1 : 0)) * hw + hl) * C::SLOT;
+    // this warp's turn: every pw-th 16 bytes of its head group's rows
+    for (int i = pl * 32 + lane; i < rows * (D / 4); i += pw * 32) {
       const int r = i / (D / 4), col = (i - r * (D / 4)) * 4;
       float mm = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) mm = fmaxf(mm, sML[(w * kHeadTile + r) * 2]);
+      for (int w = hl; w < kDecWarps; w += hw) mm = fmaxf(mm, sML[(w * kHeadTile + r) * 2]);
       const float ref = mm == -INFINITY ? 0.f : mm;
       float ll = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) {
+      for (int w = hl; w < kDecWarps; w += hw) {
         const float f = ex2_approx(sML[(w * kHeadTile + r) * 2] - ref);
         ll = fmaf(sML[(w * kHeadTile + r) * 2 + 1], f, ll);
         const float4 x = *reinterpret_cast<const float4*>(sO + (w * kHeadTile + r) * C::OPAD + col);
@@ -449,11 +461,14 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
         }
       }
     }
-    __syncthreads();
-    // the next (sequence, head group)
+    if (pw > 1)
+      __syncthreads();
+    else
+      __syncwarp();
+    // the next (sequence, set)
     idx = pe;
     unit0 = 0;
-    if (idx < e && ++hg == sh.hgroups) {
+    if (idx < e && ++hg == sh.sets) {
       hg = 0;
       do {
         ++b;
@@ -477,7 +492,7 @@ __global__ void __launch_bounds__(128)
   const int b = blockIdx.x / sh.hgroups, hg = blockIdx.x - b * sh.hgroups;
   int64_t before = 0, all = 0;
   for (int i = threadIdx.x; i < sh.n_seqs; i += kThreads) {
-    const int64_t u = int64_t(sh.units(i)) * sh.hgroups;
+    const int64_t u = int64_t(sh.units(i)) * sh.sets;
     all += u;
     if (i < b) before += u;
   }
@@ -496,16 +511,19 @@ __global__ void __launch_bounds__(128)
     zero_output<T, D>(g, io, b, hg);
     return;
   }
-  s0 += int64_t(hg) * n_units;
+  const int set = hg / sh.hw, hl = hg - set * sh.hw;
+  s0 += int64_t(set) * n_units;
   const int64_t s1 = s0 + n_units;
-  const int64_t active = active_ctas(total, n_ctas);
+  const int64_t active = active_ctas(total, n_ctas, sh.hw);
   // the CTA whose share holds unit i
   const int c0 = int(((s0 + 1) * active + total - 1) / total) - 1;
   const int c1 = int((s1 * active + total - 1) / total) - 1;
   if (c0 == c1) return;
   const int parts = c1 - c0 + 1;
   const float* ws = static_cast<const float*>(io.workspace);
-  auto slot = [&](int i) { return ws + ((c0 + i) * 2 + (i == 0 ? 1 : 0)) * int64_t(C::SLOT); };
+  auto slot = [&](int i) {
+    return ws + (((c0 + i) * 2 + (i == 0 ? 1 : 0)) * sh.hw + hl) * int64_t(C::SLOT);
+  };
   for (int i = threadIdx.x; i < parts * rows; i += kThreads) {
     const int p = i / rows, r = i - p * rows;
     sml[0][p][r] = slot(p)[kHeadTile * D + r];
@@ -560,6 +578,8 @@ cudaError_t launch_t(const SeqGeo& g, const PagedCache& c, const DecodeIO& io, c
   if (e != cudaSuccess) return e;
   const int64_t pairs = int64_t(io.n_seqs) * sh.hgroups;
   const bool whole = pairs <= ctas && sh.max_len <= kWholeKeys;
+  sh.hw = whole ? 1 : (sh.hgroups % 4 == 0 ? 4 : (sh.hgroups % 2 == 0 ? 2 : 1));
+  sh.sets = sh.hgroups / sh.hw;
   kern<<<whole ? unsigned(pairs) : unsigned(ctas), 32 * kDecWarps, C::SMEM, st>>>(g, c, io, sh,
                                                                                   whole);
   e = cudaGetLastError();
@@ -580,7 +600,7 @@ cudaError_t launch_t(const SeqGeo& g, const PagedCache& c, const DecodeIO& io, c
 }  // namespace
 
 size_t decode_workspace_bytes(const SeqGeo& g) {
-  return sizeof(float) * 2 * kMaxCtas * (g.d == 128 ? DecCfg<128>::SLOT : DecCfg<64>::SLOT);
+  return sizeof(float) * 2 * kMaxCtas * kDecWarps * (g.d == 128 ? DecCfg<128>::SLOT : DecCfg<64>::SLOT);
 }
 
 cudaError_t launch_paged_decode(const SeqGeo& g, const PagedCache& c, const DecodeIO& io,

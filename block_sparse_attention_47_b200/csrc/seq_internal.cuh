@@ -189,9 +189,7 @@ __device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* m
 struct Span {
   int start, len;
 };
-__device__ __forceinline__ Span span_of(const int32_t* __restrict__ cu, int b, int64_t total,
-                                        int32_t* status) {
-  const int a = __ldg(cu + b), z = __ldg(cu + b + 1);
+__device__ __forceinline__ Span checked_span(int a, int z, int64_t total, int32_t* status) {
   if (a < 0 || z < a || z > total) {
     report_invalid(status);
     return {0, 0};
@@ -244,13 +242,24 @@ __device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ cu_a, int6
                                           int lane, int32_t* status) {
   Tile t{};
   int64_t before = 0;
+  // the offsets of the next 32 sequences, loaded one turn ahead: four
+  // independent loads a turn
+  int next[4] = {0, 0, 0, 0};
+  auto fetch = [&](int s) {
+    if (s < n_seqs) {
+      next[0] = __ldg(cu_a + s), next[1] = __ldg(cu_a + s + 1);
+      next[2] = __ldg(cu_b + s), next[3] = __ldg(cu_b + s + 1);
+    }
+  };
+  fetch(lane);
   for (int base = 0; base < n_seqs; base += 32) {
     const int s = base + lane;
     Span a{0, 0}, b{0, 0};
-    if (s < n_seqs) {  // four independent loads: one latency
-      a = span_of(cu_a, s, total_a, status);
-      b = span_of(cu_b, s, total_b, status);
+    if (s < n_seqs) {
+      a = checked_span(next[0], next[1], total_a, status);
+      b = checked_span(next[2], next[3], total_b, status);
     }
+    fetch(s + 32);
     const int n_all = (a.len + rows - 1) / rows;
     int longest = a.len > 0 ? (b.len + 127) / 128 : 0;
     int classes = 1;

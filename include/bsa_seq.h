@@ -116,6 +116,7 @@ typedef struct bsa_decode_args {
  *   q, o        [total_q, heads, head_dim];  k, v [total_k, kv_heads, head_dim];
  *               the strides of q, k and v must not be 0 (no broadcast views)
  *   cu_q, cu_k  int32 [n_seqs + 1]
+ *   o           must not overlap an input
  *   lse         fp32 [heads, total_q] or NULL: each row's log-sum-exp in the
  *               exp2 domain, log2 sum_j exp2(softmax_scale log2(e) q.k_j)
  *               (-inf for a row that sees nothing), for the backward

@@ -138,6 +138,61 @@ def test_fwd_long_sequence_sampled(cuda_ok):
         assert bool(((lse[h, rows.cuda()].double() - lse2).abs() <= 2e-3).all())
 
 
+def test_rows_in_front_of_the_first_offset(cuda_ok):
+    """Offsets that begin behind row 0: the rows in front are not a sequence's."""
+    q, k, v = inputs([5, 200, 130], [9, 200, 130], 4, 2, 64, FP, tail=3)
+    for t, n in ((q, 5), (k, 9), (v, 9)):
+        t[:n] = math.nan
+    dout = torch.randn(q.shape, device="cuda").half()
+    dout[:5], dout[335:] = math.nan, math.nan
+    cq = torch.tensor([5, 205, 335], dtype=torch.int32, device="cuda")
+    ck = torch.tensor([9, 209, 339], dtype=torch.int32, device="cuda")
+    prob, st = bsa.SeqProblem.make(4, 2, 64, FP), status_word()
+    out, lse = torch.full_like(q, 5.0), torch.full((4, q.shape[0]), 5.0, device="cuda")
+    bsa.packed_attn_fwd(prob, q, k, v, cq, ck, out, lse, dev_status=st)
+    assert int(st) == 0
+    check_fwd(q[5:335], k[9:339], v[9:339], [200, 130], [200, 130], True, out[5:335], None, 1 / 8)
+    assert bool((out[:5] == 5.0).all()) and bool((out[335:] == 5.0).all())
+    assert bool((lse[:, :5] == 5.0).all()) and bool((lse[:, 335:] == 5.0).all())
+    dq, dk, dv, bufs = backward(prob, q, k, v, dout, cq, ck)
+    check_bwd(q[5:335], k[9:339], v[9:339], dout[5:335], [200, 130], [200, 130], True, dq[5:335],
+              dk[9:339], dv[9:339], 1 / 8)
+    for x, a, b in ((bufs[0], 5, 335), (bufs[1], 9, 339), (bufs[2], 9, 339)):
+        assert bool((x[:a] == 5.0).all()) and bool((x[b:] == 5.0).all())
+
+
+def test_no_keys_and_no_queries(cuda_ok):
+    """Tensors without a row: the outputs that exist are 0."""
+    prob = bsa.SeqProblem.make(4, 2, 128)
+    some, none = torch.randn(70, 4, 128, device="cuda").bfloat16(), torch.empty(0, 4, 128, dtype=BF, device="cuda")
+    kv, no_kv = torch.randn(70, 2, 128, device="cuda").bfloat16(), torch.empty(0, 2, 128, dtype=BF, device="cuda")
+    full, empty = cu_of([30, 40]), cu_of([0, 0])
+    for q, k, cq, ck in ((some, no_kv, full, empty), (none, kv, empty, full), (none, no_kv, empty, empty)):
+        out, lse, st = torch.full_like(q, 5.0), torch.full((4, q.shape[0]), 5.0, device="cuda"), status_word()
+        bsa.packed_attn_fwd(prob, q, k, k, cq, ck, out, lse, dev_status=st)
+        assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+        grads = [torch.full_like(t, 5.0) for t in (q, k, k)]
+        ws = torch.empty(bsa.packed_bwd_workspace_bytes(prob, q.shape[0], 2), dtype=torch.uint8, device="cuda")
+        bsa.packed_attn_bwd(prob, q, k, k, out, q, lse, cq, ck, *grads, ws, dev_status=st)
+        assert all(bool((x == 0).all()) for x in grads) and int(st) == 0
+
+
+def test_fwd_timeout_path_of_a_cluster(cuda_ok):
+    """The same where a cluster shares the keys."""
+    q, k, v = inputs([64], [3000], 4, 2, 64, BF, tail=0)
+    prob, st = bsa.SeqProblem.make(4, 2, 64), status_word()
+    out, cq, ck = torch.empty_like(q), cu_of([64]), cu_of([3000])
+    bsa.debug_stall_pv(True)
+    try:
+        bsa.packed_attn_fwd(prob, q, k, v, cq, ck, out, dev_status=st)
+        torch.cuda.synchronize()
+    finally:
+        bsa.debug_stall_pv(False)
+    assert int(st) == 6
+    bsa.packed_attn_fwd(prob, q, k, v, cq, ck, out)
+    check_fwd(q, k, v, [64], [3000], True, out, None, 1 / 8)
+
+
 def test_fwd_reports_bad_offsets(cuda_ok):
     """Offsets that descend or leave the tensor: reported, read as empty; the
     other sequences are right."""
