@@ -26,6 +26,13 @@
 // row 128 (cu[b] / 128 + b), which keeps tiles apart and 512-byte aligned for
 // bulk copies.
 //
+// D.  rowsum(dO * O) from the 16-bit O is off by half a step of O, and where a
+// row sees few keys dP - D nearly cancels: dQ and dK came out up to four times
+// less exact than their rounding.  dQ therefore takes query tiles of up to
+// kExactSteps key steps twice: a first sweep sums D = sum_j P_ij dP_ij in
+// fp32 (no accumulation), and the corrected D also serves dK/dV.  Longer rows
+// average that error out and keep rowsum(dO * O).
+//
 // Tiles that run into a neighbour's rows: as the B operand of an accumulation
 // (K in dQ; Q and dO in dK/dV) their foreign rows are zeroed in shared
 // memory, since 0 times a NaN would reach the sums; as rows of the CTA's own
@@ -43,6 +50,12 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPShift = 13.f;
+// 128-key steps up to which D is summed from P and dP.  Relative errors of dQ
+// over that of rounding an exact result, bf16, at 5, 128, 1,500 and 4,000
+// causal tokens: none 2.41, 1.71, 1.59, 1.55; 8 steps 1.33, 1.41, 1.45, 1.47;
+// all 1.33, 1.41, 1.44, 1.43.  Forward and backward of 7,555 tokens x 24
+// heads: 660, 695 and 834 us.
+constexpr int kExactSteps = 8;
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
                                           uint32_t bar) {
@@ -230,10 +243,11 @@ struct DqCfg {
   static constexpr int OFF_V = OFF_K + NK * TILE;
   static constexpr int OFF_BAR = OFF_V + NV * TILE;
   // kfull[NK] kempty[NK] vfull[NV] vempty[NV] sd_ready read x_ready[2]
-  // x_free own q do fix_go fixed done drain[2]
-  static constexpr int N_BARS = 2 * NK + 2 * NV + 13;
+  // x_free own q do fix_go fixed sums done drain[2]
+  static constexpr int N_BARS = 2 * NK + 2 * NV + 14;
   static constexpr int OFF_MISC = OFF_BAR + 8 * N_BARS;
-  static constexpr int SMEM = OFF_MISC + 64 + 1024;
+  static constexpr int OFF_SUM = OFF_MISC + 64;  // float [group][128]: D of the two halves
+  static constexpr int SMEM = OFF_SUM + 1024 + 1024;
   static constexpr uint32_t TMEM_COLS = 512;
   // dO (A of dP) at 0, S at 64 (group w's half at 64 + 64 w), dP at 192, dS
   // at 320 (32 packed columns per group), dQ at 384
@@ -258,8 +272,8 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t vfull = kempty + 8 * NK, vempty = vfull + 8 * NV;
   const uint32_t sd_ready = vempty + 8 * NV, read = sd_ready + 8, x_ready = read + 8;
   const uint32_t x_free = x_ready + 16, own = x_free + 8, bar_q = own + 8;
-  const uint32_t bar_do = bar_q + 8, fix_go = bar_do + 8, fixed = fix_go + 8, done = fixed + 8;
-  const uint32_t drain = done + 8;
+  const uint32_t bar_do = bar_q + 8, fix_go = bar_do + 8, fixed = fix_go + 8, sums = fixed + 8;
+  const uint32_t done = sums + 8, drain = done + 8;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 4);
   int* found = reinterpret_cast<int*>(sm + C::OFF_MISC + 8);
@@ -295,6 +309,7 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(bar_do, 1);
       mbar_init(fix_go, 1);
       mbar_init(fixed, 1);
+      mbar_init(sums, 8);
       mbar_init(done, 2);
       mbar_init(drain, 1);
       mbar_init(drain + 8, 1);
@@ -343,13 +358,18 @@ __global__ void __launch_bounds__(384, 1)
     plan();
   }
   const bool has_tail = np > 0 && np * 128 > Lk;
+  // steps: a first sweep for D, then the one that accumulates (a single step
+  // stays in tensor memory for the second)
+  const bool exact = np > 0 && np <= kExactSteps;
+  const int lead = exact && np > 1 ? np : 0, nt = lead + np;
 
   if (warp == 9) {
     // ---- the copies: K and V tiles into their rings
     if (lane == 0 && np > 0) {
       bool ok = true;
       int kl = 0, vl = 0;  // tiles whose K / V copies have been issued
-      for (int p = 0; p < np; ++p) {
+      for (int p = 0; p < nt; ++p) {
+        const int row = k0 + (p < lead ? p : p - lead) * 128;
         // (the third K slot is free once dO has been taken out of it)
         if ((p >= NK && !mbar_wait(kempty + 8 * (p % NK), ((p - NK) / NK) & 1, abort_flag)) ||
             (p == 2 && !mbar_wait(own, 0, abort_flag))) {
@@ -357,14 +377,14 @@ __global__ void __launch_bounds__(384, 1)
           break;
         }
         mbar_arrive_expect_tx(kfull + 8 * (p % NK), C::TILE);
-        tma_load_rows(kslot(p), &mk, kfull + 8 * (p % NK), k0 + p * 128, kvh);
+        tma_load_rows(kslot(p), &mk, kfull + 8 * (p % NK), row, kvh);
         kl = p + 1;
         if (p >= NV && !mbar_wait(vempty + 8 * (p % NV), ((p - NV) / NV) & 1, abort_flag)) {
           ok = false;
           break;
         }
         mbar_arrive_expect_tx(vfull + 8 * (p % NV), C::TILE);
-        tma_load_rows(vslot(p), &mv, vfull + 8 * (p % NV), k0 + p * 128, kvh);
+        tma_load_rows(vslot(p), &mv, vfull + 8 * (p % NV), row, kvh);
         vl = p + 1;
       }
       if (!ok) report_timeout(abort_flag, io.status);
@@ -383,8 +403,8 @@ __global__ void __launch_bounds__(384, 1)
     // ---- the last tile's foreign K rows, once it has landed
     if (has_tail) {
       if (__all_sync(0xffffffffu, mbar_wait(fix_go, 0, abort_flag,
-                                            2000000000ull + uint64_t(np) * 10000ull))) {
-        zero_rows(kslot(np - 1), C::KB, Lk - (np - 1) * 128, lane);
+                                            2000000000ull + uint64_t(nt) * 10000ull))) {
+        zero_rows(kslot(nt - 1), C::KB, Lk - (np - 1) * 128, lane);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(fixed);
@@ -398,14 +418,14 @@ __global__ void __launch_bounds__(384, 1)
     if (lane == 0 && np > 0) {
       constexpr uint32_t idesc_s = idesc_f32<T>(128, 128, false);
       bool ok = mbar_wait(own, 0, abort_flag) && mbar_wait(bar_q, 0, abort_flag);
-      for (int p = 0; ok && p < np; ++p) {
+      for (int p = 0; ok && p < nt; ++p) {
         if (!mbar_wait(kfull + 8 * (p % NK), (p / NK) & 1, abort_flag) ||
             !mbar_wait(vfull + 8 * (p % NV), (p / NV) & 1, abort_flag) ||
             (p > 0 && !mbar_wait(read, (p - 1) & 1, abort_flag))) {
           ok = false;
           break;
         }
-        if (has_tail && p == np - 1) {
+        if (has_tail && p == nt - 1) {
           mbar_arrive(fix_go);
           if (!mbar_wait(fixed, 0, abort_flag)) {
             ok = false;
@@ -423,6 +443,7 @@ __global__ void __launch_bounds__(384, 1)
         }
         tc_commit(sd_ready);
         tc_commit(vempty + 8 * (p % NV));
+        if (p < lead) tc_commit(kempty + 8 * (p % NK));  // no accumulation reads it
       }
       if (!ok) report_timeout(abort_flag, io.status);
       tc_commit(done);
@@ -436,9 +457,9 @@ __global__ void __launch_bounds__(384, 1)
       constexpr uint32_t idesc_acc = idesc_f32<T>(128, D, true);
       bool ok = true;
       // test hook: with `stall` set no accumulation is issued (the timeout path)
-      for (int p = 0; ok && p < np && !io.stall; ++p) {
+      for (int p = lead; ok && p < nt && !io.stall; ++p) {
         for (int h = 0; h < 2; ++h) {
-          if (!mbar_wait(x_ready + 8 * h, p & 1, abort_flag)) {
+          if (!mbar_wait(x_ready + 8 * h, (p - lead) & 1, abort_flag)) {
             ok = false;
             break;
           }
@@ -447,7 +468,7 @@ __global__ void __launch_bounds__(384, 1)
           for (int kk = 0; kk < 4; ++kk)
             tc_mma_ts(tmem + C::COL_ACC, tmem + C::COL_DS + 32u * h + 8u * kk,
                       sdesc_sw128(kslot(p) + h * 8192 + kk * 2048, C::BOX, 1024), idesc_acc,
-                      (p > 0 || h > 0 || kk > 0) ? 1u : 0u);
+                      (p > lead || h > 0 || kk > 0) ? 1u : 0u);
         }
         if (!ok) break;
         tc_commit(x_free);
@@ -498,13 +519,50 @@ __global__ void __launch_bounds__(384, 1)
       dlt = __ldg(io.stat_delta + at);
       if constexpr (kHalf) fac = ds_factor(io.norms, kvh, g.kv_heads);
     }
-    const float dlt_f = dlt * fac;
     const float sl2 = g.scale * kLog2e;
     const uint32_t tS = tmem + C::COL_S + 64u * grp + lane_base;
     const uint32_t tDP = tmem + C::COL_DP + 64u * grp + lane_base;
     const uint32_t tDS = tmem + C::COL_DS + 32u * grp + lane_base;
+    if (exact) {
+      // ---- D = sum_j P_ij dP_ij over this group's columns, then both groups'
+      float part = 0.f;
+      for (int p = 0; ok && p < np; ++p) {
+        ok = __all_sync(0xffffffffu, mbar_wait(sd_ready, p & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        const int seen = lim - 128 * p - 64 * grp;
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h2 = 0; h2 < 2; ++h2) {
+          uint32_t sv[32], dp[32];
+          BSA_TMEM_LD32(tS + 32u * h2, sv);
+          BSA_TMEM_LD32(tDP + 32u * h2, dp);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const float pr = ex2_approx(fmaf(__uint_as_float(sv[c]), sl2, -lse2));
+            // masked columns may hold anything
+            acc[c & 3] = 32 * h2 + c < seen ? fmaf(pr, __uint_as_float(dp[c]), acc[c & 3])
+                                            : acc[c & 3];
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && lead) mbar_arrive(read);  // a single step is read again
+        part += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+      }
+      volatile float* buf = reinterpret_cast<volatile float*>(sm + C::OFF_SUM);
+      buf[128 * grp + row] = part;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sums);
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(sums, 0, abort_flag));
+      dlt = buf[row] + buf[128 + row];
+      if (ok && grp == 0 && exists)
+        io.stat_delta[int64_t(head) * stat_rows(io.total_q, io.n_seqs) + stat_start(q0, seq) + r] =
+            dlt;
+    }
+    const float dlt_f = dlt * fac;
     for (int p = 0; ok && p < np; ++p) {
-      ok = __all_sync(0xffffffffu, mbar_wait(sd_ready, p & 1, abort_flag));
+      ok = __all_sync(0xffffffffu, mbar_wait(sd_ready, (lead + p) & 1, abort_flag));
       if (!ok) break;
       tc_fence_after();
       uint32_t sv[64], dp[64];
@@ -711,6 +769,8 @@ __global__ void __launch_bounds__(384, 1)
       mbar_arrive_expect_tx(own, 2 * C::TILE);
       tma_load_rows(sK, &mk, own, k0 + first, kvh);
       tma_load_rows(sV, &mv, own, k0 + first, kvh);
+      // dQ writes the row statistics that come with the queries
+      cudaGridDependencySynchronize();
       load();
     }
     __syncwarp();
@@ -967,7 +1027,7 @@ __global__ void __launch_bounds__(384, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
-  cudaGridDependencySynchronize();  // dQ has finished, too
+  cudaGridDependencySynchronize();  // whatever a tile did: dQ has finished, too
 }
 
 template <typename T, int D>
@@ -1000,9 +1060,8 @@ cudaError_t launch_t(const SeqGeo& g, const CUtensorMap* maps, const PackedBwdIO
     static std::atomic<uint64_t> seen{0};
     e = allow_smem(dkdv, DkdvCfg<D>::SMEM, seen);
     if (e != cudaSuccess) return e;
-    // dK/dV needs the preparation's results, not dQ's: it may start when the
-    // last dQ tiles have started (which was after the preparation), on the SMs
-    // that dQ leaves idle, and ends after dQ
+    // dK/dV may set itself up on the SMs that dQ's last tiles leave idle; it
+    // waits for dQ before it reads the row statistics
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};

@@ -130,9 +130,10 @@ bsa_status bsa_query_packed_bwd_workspace(const bsa_seq_problem* prob, int32_t n
                                           int64_t total_q, size_t* bytes);
 
 /* Gradients of bsa_packed_attn_fwd:
- *   dV = P^T dO,  dP = dO V^T,  D = rowsum(dO * O),  dS = P * (dP - D),
+ *   dV = P^T dO,  dP = dO V^T,  D_i = sum_j P_ij dP_ij,  dS = P * (dP - D),
  *   dQ = softmax_scale dS K,  dK = softmax_scale dS^T Q,
- * dK and dV summed over the query heads of their kv head; P is recomputed
+ * (D is rowsum(dO * O), and taken as that from the rounded o for query tiles
+ * that see more than 1,024 keys), dK and dV summed over the query heads of their kv head; P is recomputed
  * from lse.  Every row of a sequence is written (0 where nothing was seen),
  * rows no sequence owns are left as they were.  Sums are fp32, in a fixed
  * order without atomics, so gradients do not vary from run to run; P and dS

@@ -89,12 +89,14 @@ def rope_table(rows, rot, device="cuda"):
 def grads64(q, k, v, dout, lim, scale, dtype, factor_bound=None):
     """One head in float64: (dq, dk, dv) and their error bounds.
 
-    The kernels recompute p from the rounded row statistics, round p and dS
-    to the element type (half a step u), and form D = rowsum(dO * O) from the
-    forward's rounded output:
+    The kernels recompute p from the rounded row statistics and round p and dS
+    to the element type (half a step u):
         e_p  <= p gp,  gp = 2 g + 6e-6 + 2^-22 (1 + |lse2|)
-        e_dS <= |dS| (u + gp) + p (e_dP + e_D),
-        e_dP <= d 2^-24 |dO| |V|,  e_D <= |dO| (bound of O) + d 2^-24 |dO| |O|
+        e_dS <= |dS| (u + gp) + p (e_dP + e_D),  e_dP <= d 2^-24 |dO| |V|
+    D is sum_j p_j dP_j in fp32 for rows of up to 1,024 keys,
+        e_D <= sum_j p_j (gp |dP_j| + e_dP_j) + n 2^-24 sum_j p_j |dP_j|,
+    and rowsum(dO * O) of the forward's rounded output beyond,
+        e_D <= |dO| (bound of O) + d 2^-24 |dO| |O|,
     and the products add n fp32 roundings and the final half step.  In fp16
     p and dS are scaled to 2^13 and at most 2^15, so that a value below fp16's
     normal range adds at most 2^-25 of that scale."""
@@ -108,9 +110,12 @@ def grads64(q, k, v, dout, lim, scale, dtype, factor_bound=None):
     dq, dk, dv = scale * ds @ k, scale * ds.t() @ q, p.t() @ do
     finite = torch.where(torch.isinf(lse2), torch.zeros_like(lse2), lse2)
     gp = 2 * g + 6e-6 + 2.0 ** -22 * (1 + finite.abs())[:, None]
-    e_o = output_bound(o, p, v, g, dtype)
-    e_d = (do.abs() * e_o).sum(dim=1, keepdim=True) + d * 2.0 ** -24 * (do * o).abs().sum(dim=1, keepdim=True)
     e_dp = d * 2.0 ** -24 * (do.abs() @ v.abs().t())
+    if k.shape[0] <= 1024:
+        e_d = (p * (gp * dp.abs() + e_dp) + n * 2.0 ** -24 * p * dp.abs()).sum(dim=1, keepdim=True)
+    else:
+        e_o = output_bound(o, p, v, g, dtype)
+        e_d = (do.abs() * e_o).sum(dim=1, keepdim=True) + d * 2.0 ** -24 * (do * o).abs().sum(dim=1, keepdim=True)
     e_ds = ds.abs() * (u + gp) + p * (e_dp + e_d)
     e_p = p * (u + gp)
     if dtype == torch.float16:

@@ -321,6 +321,9 @@ BWD = [
     ([700], [700], 3, 1, 128, BF, True, 1.0),
     ([500, 257], [500, 257], 2, 2, 64, BF, False, 1.0),
     ([5] * 40 + [200], [5] * 40 + [200], 2, 1, 64, FP, True, 1.0),
+    ([2, 4, 1], [2, 4, 9], 6, 3, 64, BF, True, 1.0),            # rows of a few keys: dS cancels
+    ([1100, 1024], [1100, 1024], 2, 1, 64, BF, True, 1.0),      # around where D changes its form
+    ([300], [1300], 2, 2, 128, FP, False, 1.0),
 ]
 
 
