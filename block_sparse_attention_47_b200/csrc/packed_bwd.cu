@@ -74,9 +74,14 @@ __device__ __forceinline__ int64_t stat_start(int cu, int b) {
   return 128 * (int64_t(cu >> 7) + b);
 }
 
+// 128-key steps of a query tile whose last row is `last`
+__device__ __forceinline__ int key_steps(bool causal, int last, int lq, int lk) {
+  return ((causal ? min(lk, max(0, last + 1 + lk - lq)) : lk) + 127) >> 7;
+}
+
 // the power of two of dS for one kv head (fp16), from the largest squared norms
 __device__ __forceinline__ float ds_factor(const float* __restrict__ norms, int kvh, int kv_heads) {
-  const float bound = 2.f * sqrtf(__ldg(norms + kvh)) * sqrtf(__ldg(norms + kv_heads + kvh));
+  const float bound = 2.f * sqrtf(__ldcg(norms + kvh)) * sqrtf(__ldcg(norms + kv_heads + kvh));
   if (!(bound > 0.f) || isinf(bound)) return 1.f;
   return exp2f(fminf(fmaxf(floorf(15.f - log2f(bound)), -60.f), 60.f));
 }
@@ -151,6 +156,7 @@ __device__ __forceinline__ void v_norms(const SeqGeo& g, const PackedBwdIO& io, 
 template <typename T, int D>
 __global__ void __launch_bounds__(256) bwd_prepare_kernel(SeqGeo g, const PackedBwdIO io,
                                                           int tiles) {
+  cudaTriggerProgrammaticLaunchCompletion();  // dQ may set itself up
   if constexpr (std::is_same<T, __half>::value) {
     // the blocks behind the tiles' look at V
     if (int(blockIdx.x) >= tiles) {
@@ -160,19 +166,25 @@ __global__ void __launch_bounds__(256) bwd_prepare_kernel(SeqGeo g, const Packed
     }
   }
   constexpr int TPR = D / 8;  // threads per row, 16 bytes each
-  __shared__ int where[5];    // any, sequence, tile, first row, length
+  __shared__ int where[6];    // any, sequence, tile, first row, length, keys
   __shared__ float top[8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (warp == 0) {
     const Tile f = find_tile<kWalkQ>(io.cu_q, io.total_q, io.cu_k, io.total_k, io.n_seqs, g.causal,
                                      128, blockIdx.x, lane, io.status);
     if (lane == 0)
-      where[0] = f.any, where[1] = f.seq, where[2] = f.tile, where[3] = f.a.start, where[4] = f.a.len;
+      where[0] = f.any, where[1] = f.seq, where[2] = f.tile, where[3] = f.a.start,
+      where[4] = f.a.len, where[5] = f.b.len;
   }
   __syncthreads();
   if (!where[0]) return;
   const int b = where[1], t = where[2], head = blockIdx.y;
   const Span q{where[3], where[4]};
+  // D of tiles of few key steps comes from dQ: there O and (but for its norms
+  // in fp16) dO need not be read
+  const bool summed =
+      !std::is_same<T, __half>::value &&
+      key_steps(g.causal, min(t * 128 + 128, q.len) - 1, q.len, where[5]) <= kExactSteps;
   const int64_t stats = stat_rows(io.total_q, io.n_seqs);
   const int64_t out0 = int64_t(head) * stats + stat_start(q.start, b) + int64_t(t) * 128;
   float most = 0.f;
@@ -180,7 +192,7 @@ __global__ void __launch_bounds__(256) bwd_prepare_kernel(SeqGeo g, const Packed
   for (int r = threadIdx.x / TPR; r < 128; r += 256 / TPR) {
     const int row = t * 128 + r;
     float acc = 0.f, sq = 0.f;
-    if (row < q.len) {
+    if (row < q.len && !summed) {
       const int64_t at = q.start + row;
       const int c = (threadIdx.x % TPR) * 8;
       const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const T*>(io.o.p) + at * io.o.sn +
@@ -286,8 +298,7 @@ __global__ void __launch_bounds__(384, 1)
   int q0 = 0, Lq = 0, k0 = 0, Lk = 0, first = 0, seq = 0, np = 0;
   bool any = false;
   auto plan = [&] {  // np: key tiles that the tile's last row sees
-    const int last = min(first + 128, Lq) - 1;
-    np = any ? ((g.causal ? min(Lk, max(0, last + 1 + Lk - Lq)) : Lk) + 127) >> 7 : 0;
+    np = any ? key_steps(g.causal, min(first + 128, Lq) - 1, Lq, Lk) : 0;
   };
   if (warp == 10) {
     if (lane == 0) {
@@ -513,10 +524,11 @@ __global__ void __launch_bounds__(384, 1)
       if (lane == 0 && ok) mbar_arrive(own);
     }
     float lse2 = INFINITY, dlt = 0.f, fac = 1.f;
+    cudaGridDependencySynchronize();  // the preparation has finished
     if (exists && np > 0) {
       const int64_t at = int64_t(head) * stat_rows(io.total_q, io.n_seqs) + stat_start(q0, seq) + r;
-      lse2 = __ldg(io.stat_lse + at);
-      dlt = __ldg(io.stat_delta + at);
+      lse2 = __ldcg(io.stat_lse + at);
+      dlt = __ldcg(io.stat_delta + at);
       if constexpr (kHalf) fac = ds_factor(io.norms, kvh, g.kv_heads);
     }
     const float sl2 = g.scale * kLog2e;
@@ -911,6 +923,7 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t lane_base = uint32_t(quad * 32) << 16;
     const bool exists = any && kr < Lk;
     const float sl2 = g.scale * kLog2e;
+    if (kHalf) cudaGridDependencySynchronize();  // the norms
     const float fac = kHalf && np > 0 ? ds_factor(io.norms, kvh, g.kv_heads) : 1.f;
     const float fac_p = kHalf ? fac * exp2f(-kPShift) : 1.f;
     const float shift = kHalf ? kPShift : 0.f;
@@ -1030,6 +1043,24 @@ __global__ void __launch_bounds__(384, 1)
   cudaGridDependencySynchronize();  // whatever a tile did: dQ has finished, too
 }
 
+// A launch that may set itself up on the SMs that the kernel before it leaves
+// idle; it waits for that kernel before it reads the row statistics.
+template <typename K, typename... A>
+cudaError_t launch_after(K kern, unsigned ctas, int threads, int smem, bool early, cudaStream_t st,
+                         A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 template <typename T, int D>
 cudaError_t launch_t(const SeqGeo& g, const CUtensorMap* maps, const PackedBwdIO& io,
                      cudaStream_t st) {
@@ -1052,32 +1083,22 @@ cudaError_t launch_t(const SeqGeo& g, const CUtensorMap* maps, const PackedBwdIO
     static std::atomic<uint64_t> seen{0};
     e = allow_smem(dq, DqCfg<D>::SMEM, seen);
     if (e != cudaSuccess) return e;
-    dq<<<unsigned(tiles(io.total_q) * g.heads), DqCfg<D>::kThreads, DqCfg<D>::SMEM, st>>>(
-        maps[0], maps[1], maps[2], maps[3], g, io);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    e = launch_after(dq, unsigned(n_tiles * g.heads), DqCfg<D>::kThreads, DqCfg<D>::SMEM, true, st,
+                     maps[0], maps[1], maps[2], maps[3], g, io);
+    if (e != cudaSuccess) return e;
   }
   if (io.total_k > 0) {
     auto dkdv = packed_dkdv_kernel<T, D>;
     static std::atomic<uint64_t> seen{0};
     e = allow_smem(dkdv, DkdvCfg<D>::SMEM, seen);
     if (e != cudaSuccess) return e;
-    // dK/dV may set itself up on the SMs that dQ's last tiles leave idle; it
-    // waits for dQ before it reads the row statistics
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(tiles(io.total_k) * g.kv_heads));
-    cfg.blockDim = dim3(DkdvCfg<D>::kThreads);
-    cfg.dynamicSmemBytes = DkdvCfg<D>::SMEM;
-    cfg.stream = st;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = io.total_q > 0 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, dkdv, maps[0], maps[1], maps[2], maps[3], g, io);
+    e = launch_after(dkdv, unsigned(tiles(io.total_k) * g.kv_heads), DkdvCfg<D>::kThreads,
+                     DkdvCfg<D>::SMEM, io.total_q > 0, st, maps[0], maps[1], maps[2], maps[3], g, io);
     if (e != cudaSuccess) return e;
   }
-  return cudaGetLastError();
+  return cudaSuccess;
 }
 
 }  // namespace
