@@ -31,7 +31,7 @@
 // warp finds the next tile and loads its first operands while the last steps
 // of the current one run, and a warpgroup writes its rows while the pipe is
 // on the other tile's or the next one's products: at 4 steps a tile (cross
-// attention to a short text) the set-up was 60 % of the time.
+// attention to a short text) the set-up was two fifths of the time.
 //
 // Few tiles and many keys (the next part of a long text): a cluster of CTAs
 // shares a tile's key steps; each leaves its maxima, sums and unnormalised O
@@ -39,7 +39,8 @@
 // order, so no workspace is needed and results do not vary.
 //
 // Tensor memory (512 columns): S_u/P_u at 128 u, O_u at 256 + 128 u.
-// Every wait is bounded (2 s) and reports BSA_ERR_TIMEOUT.
+// Every wait is bounded and reports BSA_ERR_TIMEOUT: 2 s, 20 s where it may last
+// as long as another tile's walk.
 #include "seq_internal.cuh"
 
 namespace bsa {
@@ -47,10 +48,6 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMinShare = 4;  // key steps a CTA of a cluster takes at least
-// CTAs that clusters may ask for: at 72 tiles of 512 keys to 5,000 (8 heads
-// pairs) two, four and eight CTAs a tile took 44.9, 40.8 and 72 us, one 76 us;
-// few clusters of eight find room at a time
-constexpr int kSplitCtas = 300;
 
 template <int D>
 struct FwdCfg {
@@ -85,42 +82,6 @@ struct Plan {
   int q0, Lq, k0, Lk, first, hp;
   int kb, n0, n1, n;  // first key tile, steps of the two tiles, their maximum
 };
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-}
-__device__ __forceinline__ uint32_t peer_smem(uint32_t addr, int rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
-               : "=f"(v.x), "=f"(v.y)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
 
 template <typename T, int D, bool HEADS, bool SPLIT>
 __global__ void __launch_bounds__(384, 1)
@@ -643,6 +604,25 @@ cudaError_t launch_t(const SeqGeo& g, const CUtensorMap* maps, const PackedIO& i
   return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], g, io, units);
 }
 
+// CTAs that share a tile's keys, where a CTA per tile leaves half of the 148 SMs
+// idle.  us with 1 | 2 | 4 | 8 CTAs a tile (d = 128, bf16; queries x keys):
+//   32 tiles, 512 x 5,000 of 16 heads:     80 |  51 |  37 |  84
+//   64 tiles, 512 x 8,000 of 32/8 heads:  121 |  70 |  88 | 165
+//   12 tiles, 384 x 5,000 of 8/2 heads:    79 |  49 |  33 |  30
+//   16 tiles, 512 x 30,000 of 8 heads:    427 | 218 | 119 | 145
+// so one wave of CTAs for one sequence, and no more than 112 in clusters of
+// eight, of which few find room at a time.  Sequences of several lengths even
+// out over two waves (256, 511 and 64 queries to 5,000, 511 and 2,113 keys: 76 |
+// 45 | 41 | 72).
+int split_ranks(const PackedIO& io, int64_t rows, int slots) {
+  // the sequences' last tiles are half full on average
+  const int64_t units = ((io.total_q + rows - 1) / rows + io.n_seqs / 2) * slots;
+  if (units > 74 || io.total_k <= 2 * kMinShare * 128) return 1;
+  int ranks = io.total_k > 4 * kMinShare * 128 && units * 8 <= 112 ? 8 : 4;
+  if (ranks == 4 && units * 4 > (io.n_seqs > 1 ? 300 : 148)) ranks = 2;
+  return ranks;
+}
+
 template <typename T, int D>
 cudaError_t launch_d(const SeqGeo& g, const CUtensorMap* maps, const PackedIO& io,
                      cudaStream_t st) {
@@ -651,13 +631,7 @@ cudaError_t launch_d(const SeqGeo& g, const CUtensorMap* maps, const PackedIO& i
   const int64_t rows = heads ? 128 : 256;
   const int64_t tiles = io.total_q / rows + (io.n_seqs < io.total_q ? io.n_seqs : io.total_q);
   const int units = int(tiles * (heads ? g.heads / 2 : g.heads));
-  // a tile per CTA fills less than half of the 148 SMs and some sequence may
-  // have keys enough for two shares: split the keys
-  int ranks = 1;
-  if (units <= 74 && io.total_k > 2 * kMinShare * 128) {
-    ranks = 8;
-    while (ranks > 2 && units * ranks > kSplitCtas) ranks /= 2;
-  }
+  const int ranks = split_ranks(io, rows, heads ? g.heads / 2 : g.heads);
   if (ranks > 1)
     return heads ? launch_t<T, D, true, true>(g, maps, io, units, ranks, st)
                  : launch_t<T, D, false, true>(g, maps, io, units, ranks, st);

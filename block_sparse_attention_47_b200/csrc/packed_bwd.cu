@@ -11,15 +11,17 @@
 //   dQ     CTA = 128 query rows of a head, walking the key tiles they see.
 //   dK/dV  CTA = 128 keys of a kv head, walking the query tiles that see them
 //          of every head of the group, so shared heads are summed in the
-//          accumulators.
+//          accumulators.  Where there are few such tiles a cluster of CTAs
+//          shares a tile's steps and adds its sums up in rank order.
 // Per step the two score-like products are one N=128 burst each, two row
 // groups of 128 threads take 64 of the 128 columns each, and the results
 // return to tensor memory as A operands of the accumulations.  In dK/dV two
 // 128-column regions change roles from step to step: S^T in one, dP^T in the
 // other; P^T and dS^T go over S^T, so the next S^T can follow into dP^T's
-// region as soon as the groups have read it, under their remaining work (with
-// P^T over S^T and dS^T over dP^T a step took 3,450 cycles, now about 2,300
-// of which the products fill 2,048).
+// region as soon as the groups have read it, under their remaining work (a batch
+// of 4,096, 2,048, 1,111 and 300 tokens, 24/8 heads, d = 128: 279 us, with P^T
+// over S^T and dS^T over dP^T 311; its products alone take 2,048 cycles a step,
+// some 130 us).
 //
 // Preparation: lse2 and D are written per 128-row tile of a sequence (rows
 // behind its end get lse2 = +inf, D = 0, so that P = 0 there), sequence b at
@@ -674,9 +676,12 @@ struct DkdvCfg {
   // at 256 + D
   static constexpr uint32_t COL_DV = 256, COL_DK = 256 + D;
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
+  static_assert(2 * 128 * D * 4 <= OFF_VEC, "the join lies over the tiles");
 };
 
-template <typename T, int D>
+// SPLIT: a cluster shares a tile's steps; each CTA's sums stay in its own
+// shared memory and the cluster adds them from there in rank order.
+template <typename T, int D, bool SPLIT>
 __global__ void __launch_bounds__(384, 1)
     packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq,
                        const __grid_constant__ CUtensorMap mk,
@@ -699,20 +704,28 @@ __global__ void __launch_bounds__(384, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 4);
   int* found = reinterpret_cast<int*>(sm + C::OFF_MISC + 8);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kvh = int(blockIdx.x % uint32_t(g.kv_heads));
+  const int rank = SPLIT ? int(cluster_rank()) : 0, ranks = SPLIT ? int(cluster_size()) : 1;
+  const uint32_t unit = blockIdx.x / uint32_t(ranks);
+  const int kvh = int(unit % uint32_t(g.kv_heads));
   auto qslot = [&](int p) { return base + C::OFF_STG + (p % NR) * 2 * C::TILE; };
   auto doslot = [&](int p) { return qslot(p) + C::TILE; };
   auto vecslot = [&](int p) { return base + C::OFF_VEC + (p % NR) * 1024; };
 
   int q0 = 0, Lq = 0, k0 = 0, Lk = 0, first = 0, seq = 0;
   // query tiles qt0 .. qt0+per-1 of each of the group's heads, head after head
-  int qt0 = 0, per = 0, np = 0;
+  int qt0 = 0, per = 1, np = 0;
+  int skip = 0;  // steps of the tile that lower ranks take; np are this CTA's
   bool any = false;
   auto plan = [&] {
     if (any && Lq > 0) {
       if (g.causal) qt0 = max(0, first + Lq - Lk) >> 7;
       per = ((Lq + 127) >> 7) - qt0;
       np = per * g.group;
+      if (SPLIT) {
+        const int share = (np + ranks - 1) / ranks;
+        skip = min(np, rank * share);
+        np = min(np, skip + share) - skip;
+      }
     }
   };
   // Q and dO tiles of step p with their rows' lse2 and D
@@ -766,7 +779,7 @@ __global__ void __launch_bounds__(384, 1)
     tma_prefetch_desc(&mdo);
   } else if (warp == 9) {
     const Tile t = find_tile<kWalkK>(io.cu_k, io.total_k, io.cu_q, io.total_q, io.n_seqs, g.causal,
-                                     128, blockIdx.x / uint32_t(g.kv_heads), lane, io.status);
+                                     128, unit / uint32_t(g.kv_heads), lane, io.status);
     any = t.any, q0 = t.b.start, Lq = t.b.len, k0 = t.a.start, Lk = t.a.len;
     first = t.tile * 128, seq = t.seq;
     if (lane == 0) {
@@ -774,7 +787,8 @@ __global__ void __launch_bounds__(384, 1)
       found[5] = first, found[6] = seq;
     }
     plan();
-    lt = qt0;
+    lh += skip / per;
+    lt = qt0 + skip % per;
     named_bar_sync(1, 64);  // the barriers are set up
     // the first copies start before the rest of the set-up
     if (lane == 0 && np > 0) {
@@ -796,7 +810,7 @@ __global__ void __launch_bounds__(384, 1)
     q0 = found[1], Lq = found[2], k0 = found[3], Lk = found[4], first = found[5], seq = found[6];
     plan();
   }
-  const bool has_tail = np > 0 && (Lq & 127) != 0;  // every per-th step's tile is partial
+  const bool has_tail = np > 0 && (Lq & 127) != 0;  // a head's last tile is partial
 
   if (warp == 9) {
     // ---- the copies: step p into the slot of step p - 2 once its
@@ -819,9 +833,9 @@ __global__ void __launch_bounds__(384, 1)
   } else if (warp == 11) {
     // ---- the foreign rows of the heads' last Q and dO tiles
     if (has_tail) {
-      for (int h = 0; h < g.group; ++h) {
-        const int p = (h + 1) * per - 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(fix_go, h & 1, abort_flag,
+      int tails = 0;
+      for (int p = per - 1 - skip % per; p < np; p += per) {
+        if (!__all_sync(0xffffffffu, mbar_wait(fix_go, tails++ & 1, abort_flag,
                                                2000000000ull + uint64_t(np) * 10000ull))) {
           if (lane == 0) report_timeout(abort_flag, io.status);
           break;
@@ -837,7 +851,7 @@ __global__ void __launch_bounds__(384, 1)
     // ---- S^T and dP^T of each step
     if (lane == 0 && np > 0) {
       constexpr uint32_t idesc_s = idesc_f32<T>(128, 128, false);
-      int in_head = 0, tails = 0;
+      int in_head = skip % per, tails = 0;
       bool ok = mbar_wait(own, 0, abort_flag);
       for (int p = 0; ok && p < np; ++p) {
         const uint32_t cS = 128u * (p & 1), cDP = 128u - cS;
@@ -928,7 +942,7 @@ __global__ void __launch_bounds__(384, 1)
     const float fac_p = kHalf ? fac * exp2f(-kPShift) : 1.f;
     const float shift = kHalf ? kPShift : 0.f;
     bool ok = true;
-    int qt = qt0;
+    int qt = qt0 + skip % per;
     for (int p = 0; p < np; ++p) {
       const uint32_t tS = tmem + 128u * (p & 1) + 64u * grp + lane_base;
       const uint32_t tDP = tmem + 128u * ((p & 1) ^ 1) + 64u * grp + lane_base;
@@ -1018,7 +1032,7 @@ __global__ void __launch_bounds__(384, 1)
     if (ok && np > 0) ok = __all_sync(0xffffffffu, mbar_wait(done, 0, abort_flag));
     if (!ok) {
       if (lane == 0) report_timeout(abort_flag, io.status);
-    } else {
+    } else if (!SPLIT) {
       // group 0 writes dV, group 1 dK; keys no query saw have zero gradients
       tc_fence_after();
       const Rows& out = grp ? io.dk : io.dv;
@@ -1036,28 +1050,103 @@ __global__ void __launch_bounds__(384, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
-    tc_fence_after();
-    tmem_dealloc(tmem, C::TMEM_COLS);
+  tc_fence_after();
+  if constexpr (SPLIT) {
+    // ---- the join: fp32 dV then dK of this CTA's steps, 128 rows each, 16-byte
+    // chunks swizzled by the row, over the tiles
+    if (warp < 8) {
+      const int grp = warp >> 2, row = (warp & 3) * 32 + lane;
+      const uint32_t mine = base + grp * (128 * D * 4) + row * (D * 4);
+#pragma unroll 1
+      for (int ch = 0; ch < D / 32; ++ch) {
+        uint32_t a[32];
+        BSA_TMEM_LD32(tmem + (grp ? C::COL_DK : C::COL_DV) + 32u * ch +
+                          (uint32_t((warp & 3) * 32) << 16), a);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          st_shared_v4(mine + (((8 * ch + j) ^ (row & 7)) << 4),
+                       np > 0 ? make_uint4(a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3])
+                              : make_uint4(0u, 0u, 0u, 0u));
+      }
+      tc_fence_before();
+    }
+    __syncwarp();
+    cluster_sync();
+    if (any && !*abort_flag) {
+      // rank c writes rows c, c + ranks, .. of both: 16-byte output chunks
+      constexpr int CH = D / 8;
+      const float fac = kHalf ? ds_factor(io.norms, kvh, g.kv_heads) : 1.f;
+      for (int i = threadIdx.x; i < 2 * (128 / ranks) * CH; i += C::kThreads) {
+        const int ch = i % CH, rr = (i / CH) * ranks + rank, grp = rr >> 7, row = rr & 127;
+        if (first + row >= Lk) continue;
+        float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int c = 0; c < ranks; ++c) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float4 v = ld_cluster_f4(peer_smem(base + grp * (128 * D * 4) + row * (D * 4) +
+                                                         (((2 * ch + x) ^ (row & 7)) << 4), c));
+            o[4 * x] += v.x, o[4 * x + 1] += v.y, o[4 * x + 2] += v.z, o[4 * x + 3] += v.w;
+          }
+        }
+        const float f = grp ? g.scale / fac : (kHalf ? exp2f(-kPShift) : 1.f);
+        const Rows& out = grp ? io.dk : io.dv;
+        *reinterpret_cast<uint4*>(static_cast<T*>(out.p) + int64_t(k0 + first + row) * out.sn +
+                                  int64_t(kvh) * out.sh + ch * 8) =
+            make_uint4(pack2<T>(o[0] * f, o[1] * f), pack2<T>(o[2] * f, o[3] * f),
+                       pack2<T>(o[4] * f, o[5] * f), pack2<T>(o[6] * f, o[7] * f));
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while its sums are read
   }
+  if (warp == 8) tmem_dealloc(tmem, C::TMEM_COLS);
   cudaGridDependencySynchronize();  // whatever a tile did: dQ has finished, too
+}
+
+// CTAs that share a key tile: a tile takes one step per query tile and head of
+// its group, and few kv heads leave SMs idle beside long chains of steps.  us of
+// the whole backward with 1 | 2 | 4 | 8 CTAs a tile (16 or 32 heads, bf16):
+//   1,024 queries, 1 kv head:   507 | 276 | 163 | 109
+//   512 queries, 8 kv heads:     54 |  43 |  39 |  76
+//   1,024 queries, 8 kv heads:   99 |  74 |  78 | 141
+//   2,048 queries, 4 kv heads:  313 | 199 | 160 | 227
+//   900 queries, 16 kv heads:    49 |  58 |  94 | 195
+// One wave pays from three steps a CTA, two waves from ten; few clusters of
+// eight find room at a time.
+int split_ranks(const SeqGeo& g, const PackedBwdIO& io) {
+  // the sequences' last tiles are half full on average
+  const int64_t units = (io.total_k / 128 + io.n_seqs / 2) * g.kv_heads;
+  const int64_t steps = (io.total_q + 127) / 128 * g.group;
+  if (units * 8 <= 148 && steps >= 64) return 8;
+  for (int r = 4; r > 1; r /= 2)
+    if (units * r <= 148 ? steps >= 3 * r : (units * r <= 300 && steps >= 10 * r)) return r;
+  return 1;
 }
 
 // A launch that may set itself up on the SMs that the kernel before it leaves
 // idle; it waits for that kernel before it reads the row statistics.
 template <typename K, typename... A>
-cudaError_t launch_after(K kern, unsigned ctas, int threads, int smem, bool early, cudaStream_t st,
-                         A... args) {
+cudaError_t launch_after(K kern, unsigned ctas, int ranks, int threads, int smem, bool early,
+                         cudaStream_t st, A... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = early ? 1 : 0;
+  cudaLaunchAttribute attr[2]{};
+  int n = 0;
+  if (early) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (ranks > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = unsigned(ranks);
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
@@ -1085,17 +1174,23 @@ cudaError_t launch_t(const SeqGeo& g, const CUtensorMap* maps, const PackedBwdIO
     if (e != cudaSuccess) return e;
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    e = launch_after(dq, unsigned(n_tiles * g.heads), DqCfg<D>::kThreads, DqCfg<D>::SMEM, true, st,
-                     maps[0], maps[1], maps[2], maps[3], g, io);
+    e = launch_after(dq, unsigned(n_tiles * g.heads), 1, DqCfg<D>::kThreads, DqCfg<D>::SMEM, true,
+                     st, maps[0], maps[1], maps[2], maps[3], g, io);
     if (e != cudaSuccess) return e;
   }
   if (io.total_k > 0) {
-    auto dkdv = packed_dkdv_kernel<T, D>;
-    static std::atomic<uint64_t> seen{0};
-    e = allow_smem(dkdv, DkdvCfg<D>::SMEM, seen);
-    if (e != cudaSuccess) return e;
-    e = launch_after(dkdv, unsigned(tiles(io.total_k) * g.kv_heads), DkdvCfg<D>::kThreads,
-                     DkdvCfg<D>::SMEM, io.total_q > 0, st, maps[0], maps[1], maps[2], maps[3], g, io);
+    const int ranks = split_ranks(g, io);
+    const int64_t units = tiles(io.total_k) * g.kv_heads;
+    auto go = [&](auto dkdv, std::atomic<uint64_t>& seen) {
+      const cudaError_t r = allow_smem(dkdv, DkdvCfg<D>::SMEM, seen);
+      if (r != cudaSuccess) return r;
+      return launch_after(dkdv, unsigned(units * ranks), ranks, DkdvCfg<D>::kThreads,
+                          DkdvCfg<D>::SMEM, io.total_q > 0, st, maps[0], maps[1], maps[2], maps[3],
+                          g, io);
+    };
+    static std::atomic<uint64_t> seen[2];
+    e = ranks > 1 ? go(packed_dkdv_kernel<T, D, true>, seen[1])
+                  : go(packed_dkdv_kernel<T, D, false>, seen[0]);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

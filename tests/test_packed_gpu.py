@@ -75,6 +75,8 @@ FWD += [
     ([130], [6001], 6, 2, 128, FP, False),
     ([5, 0, 300], [1030, 0, 40], 2, 1, 64, BF, True),   # a text with no key for its first rows
     ([700], [2000], 1, 1, 64, BF, True),
+    ([512], [2100], 16, 16, 64, BF, True),              # four and two CTAs a tile
+    ([1000], [1100], 16, 16, 64, FP, True),
 ]
 
 
@@ -324,6 +326,10 @@ BWD = [
     ([2, 4, 1], [2, 4, 9], 6, 3, 64, BF, True, 1.0),            # rows of a few keys: dS cancels
     ([1100, 1024], [1100, 1024], 2, 1, 64, BF, True, 1.0),      # around where D changes its form
     ([300], [1300], 2, 2, 128, FP, False, 1.0),
+    ([200, 77, 300], [200, 77, 300], 20, 20, 64, BF, True, 1.0),  # a CTA per key tile
+    ([130, 257], [130, 300], 44, 22, 128, FP, False, 1.0),
+    ([1100], [1100], 8, 1, 128, BF, True, 1.0),                  # several CTAs per key tile
+    ([1000, 130], [900, 140], 8, 1, 64, FP, True, 1.0),
 ]
 
 
@@ -381,13 +387,14 @@ def test_bwd_captured_and_replayed(cuda_ok):
             x.zero_()
 
 
-def test_bwd_timeout_path(cuda_ok):
+@pytest.mark.parametrize("heads", [(2, 1), (32, 32)])  # key tiles shared by CTAs or not
+def test_bwd_timeout_path(cuda_ok, heads):
     lens = [300]
-    q, k, v = inputs(lens, lens, 2, 1, 64, BF, tail=0)
+    q, k, v = inputs(lens, lens, *heads, 64, BF, tail=0)
     dout = torch.randn(q.shape, device="cuda").bfloat16()
-    prob, cu, st = bsa.SeqProblem.make(2, 1, 64), cu_of(lens), status_word()
+    prob, cu, st = bsa.SeqProblem.make(*heads, 64), cu_of(lens), status_word()
     want = backward(prob, q, k, v, dout, cu, cu)
-    out, lse = torch.empty_like(q), torch.empty(2, 300, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(heads[0], 300, device="cuda")
     bsa.packed_attn_fwd(prob, q, k, v, cu, cu, out, lse)
     grads = [torch.empty_like(t) for t in (q, k, v)]
     ws = torch.empty(bsa.packed_bwd_workspace_bytes(prob, 300, 1), dtype=torch.uint8, device="cuda")
