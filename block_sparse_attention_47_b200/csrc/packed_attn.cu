@@ -188,15 +188,18 @@ __global__ void __launch_bounds__(384, 1)
   }
   // the first entry is found during the set-up
   Tile next{};
-  auto find = [&](int it) {
-    const int unit = unit_of(it);
-    Tile t{};
-    if (unit < n_units)
-      t = find_tile<kWalkQ>(io.cu_q, io.total_q, io.cu_k, io.total_k, io.n_seqs, g.causal,
-                            HEADS ? 128 : 256, unit / n_hp, lane, io.status);
-    return t;
+  int at = 0;  // its place in this CTA's share of the list
+  auto find = [&] {
+    for (; unit_of(at) < n_units; ++at) {
+      const Tile t = find_tile<kWalkQ>(io.cu_q, io.total_q, io.cu_k, io.total_k, io.n_seqs,
+                                       g.causal, HEADS ? 128 : 256, unit_of(at) / n_hp, lane,
+                                       io.status);
+      // only many sequences leave empty places in front of others
+      if (SPLIT || t.any || io.n_seqs <= kListed) return t;
+    }
+    return Tile{};
   };
-  if (warp == 8) next = find(0);
+  if (warp == 8) next = find();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -217,14 +220,17 @@ __global__ void __launch_bounds__(384, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     int c = 0, nq = 0;  // stages so far, entries with a walk so far
     for (int it = 0; !SPLIT || it < 1; ++it) {
-      if (it > 0) next = find(it);
+      if (it > 0) {
+        ++at;
+        next = find();
+      }
       if (it >= 2) {
         ok = __all_sync(0xffffffffu, mbar_wait(info_free + 8 * (it & 1), ((it >> 1) - 1) & 1,
                                                abort_flag, kLong));
         if (!ok) break;
       }
       const Plan w = plan({next.any, next.a.start, next.a.len, next.b.start, next.b.len,
-                           next.tile * (HEADS ? 128 : 256), unit_of(it) % n_hp, 0, 0, 0, 0});
+                           next.tile * (HEADS ? 128 : 256), unit_of(at) % n_hp, 0, 0, 0, 0});
       if (lane == 0) {
         volatile int* e = info + 8 * (it & 1);
         e[0] = w.any, e[1] = w.q0, e[2] = w.Lq, e[3] = w.k0, e[4] = w.Lk, e[5] = w.first, e[6] = w.hp;
@@ -627,9 +633,8 @@ template <typename T, int D>
 cudaError_t launch_d(const SeqGeo& g, const CUtensorMap* maps, const PackedIO& io,
                      cudaStream_t st) {
   const bool heads = g.group % 2 == 0;
-  // no more tiles than this whatever the lengths; the ones too many return
   const int64_t rows = heads ? 128 : 256;
-  const int64_t tiles = io.total_q / rows + (io.n_seqs < io.total_q ? io.n_seqs : io.total_q);
+  const int64_t tiles = tile_places(io.total_q, io.n_seqs, int(rows));
   const int units = int(tiles * (heads ? g.heads / 2 : g.heads));
   const int ranks = split_ranks(io, rows, heads ? g.heads / 2 : g.heads);
   if (ranks > 1)

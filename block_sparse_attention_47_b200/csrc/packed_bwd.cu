@@ -1153,9 +1153,7 @@ cudaError_t launch_after(K kern, unsigned ctas, int ranks, int threads, int smem
 template <typename T, int D>
 cudaError_t launch_t(const SeqGeo& g, const CUtensorMap* maps, const PackedBwdIO& io,
                      cudaStream_t st) {
-  auto tiles = [&](int64_t rows) {
-    return rows / 128 + (io.n_seqs < rows ? io.n_seqs : rows);
-  };
+  auto tiles = [&](int64_t rows) { return tile_places(rows, io.n_seqs, 128); };
   cudaError_t e;
   if (io.total_q > 0) {
     const int64_t n_tiles = tiles(io.total_q);

@@ -124,10 +124,13 @@ bsa_status check_counts(int64_t n_seqs, int64_t rows, const char* what) {
   return BSA_OK;
 }
 
-// one CTA per 128-row tile and head at most
+// one CTA per 128-row tile and head at most; row counts that sums of two of
+// them stay within 32 bits
 bsa_status check_grid(int64_t rows, int64_t n_seqs, int heads) {
-  if ((rows / 128 + (n_seqs < rows ? n_seqs : rows)) * heads > INT32_MAX)
+  if (bsa::tile_places(rows, n_seqs, 128) * heads > INT32_MAX / 2)
     return fail(BSA_ERR_SHAPE, "too many (tile, head) pairs for one call");
+  if (rows > (int64_t(1) << 30))
+    return fail(BSA_ERR_SHAPE, "%lld rows; at most 2^30 in one call", (long long)rows);
   return BSA_OK;
 }
 
@@ -171,6 +174,7 @@ bsa_status bsa_packed_attn_fwd(const bsa_seq_problem* prob, const bsa_packed_arg
   SEQ_TRY(check_counts(a->n_seqs, tk, "total_k"));
   if (tq == 0 || a->n_seqs == 0) return BSA_OK;
   SEQ_TRY(check_grid(tq, a->n_seqs, g.heads));
+  SEQ_TRY(check_grid(tk, a->n_seqs, 1));
   bsa::PackedIO io{};
   bsa::Rows rq, rk{}, rv{};
   SEQ_TRY(check_ptr(a->cu_q, "cu_q", 4));

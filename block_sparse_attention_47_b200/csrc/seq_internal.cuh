@@ -267,71 +267,100 @@ __device__ __forceinline__ int tiles_beyond(const Span& a, const Span& b, bool c
   return reach <= 0 ? 0 : min(n, (reach + 127) / 128);
 }
 
-// The tile `target` of the list of all sequences' tiles of `rows` rows of a,
-// by a whole warp; any = false when the list is shorter.  Long walks come
-// first, so that the grid does not end on them: up to 32 sequences in four
-// classes (walks beyond 1/2, 1/4 and 1/8 of the longest, the others), more
-// sequences only each by itself.
+// The list of all sequences' tiles of `rows` rows has this many places.
+constexpr int kListed = 32;
+__host__ __device__ __forceinline__ int64_t tile_places(int64_t total, int64_t n_seqs, int rows) {
+  return total / rows + (n_seqs <= kListed && total < n_seqs ? total : n_seqs);
+}
+
+// Of more than kListed sequences: sequence b's tiles start at place
+// cu[b] / rows + b, which leaves room for every tile whatever the lengths and
+// up to n_seqs places empty, so a place's sequence is searched for, 32 ways a
+// turn, instead of counted up to (16,384 sequences of 20 tokens, 8 heads:
+// forward 88 ms by counting).  The place also checks the offsets of the
+// sequence of its own number, so that bad ones are reported wherever the
+// search went.
+template <int WALK>
+__device__ __forceinline__ Tile search_tile(const int32_t* __restrict__ cu_a, int64_t total_a,
+                                            const int32_t* __restrict__ cu_b, int64_t total_b,
+                                            int n_seqs, int rows, int64_t target, int lane,
+                                            int32_t* status) {
+  Tile t{};
+  if (target < n_seqs && lane == 0) {
+    checked_span(__ldg(cu_a + target), __ldg(cu_a + target + 1), total_a, status);
+    checked_span(__ldg(cu_b + target), __ldg(cu_b + target + 1), total_b, status);
+  }
+  __syncwarp();
+  auto place = [&](int s) { return max(__ldg(cu_a + s), 0) / rows + int64_t(s); };
+  int lo = 0, n = n_seqs;
+  while (n > 1) {
+    const int step = (n + 31) >> 5;
+    const int at = lo + lane * step;
+    const uint32_t m = __ballot_sync(0xffffffffu, at < lo + n && place(at) <= target);
+    if (m == 0u) return t;  // in front of the first sequence
+    const int top = 31 - __clz(m), end = lo + n;
+    lo += top * step;
+    n = min(step, end - lo);
+  }
+  t.seq = lo;
+  t.a = checked_span(__ldg(cu_a + lo), __ldg(cu_a + lo + 1), total_a, status);
+  t.b = checked_span(__ldg(cu_b + lo), __ldg(cu_b + lo + 1), total_b, status);
+  const int64_t i = target - place(lo), tiles = (int64_t(t.a.len) + rows - 1) / rows;
+  t.any = i >= 0 && i < tiles;
+  if (t.any) t.tile = int(WALK == kWalkQ ? tiles - 1 - i : i);
+  return t;
+}
+
+// The tile `target` of the list, by a whole warp; any = false where there is
+// none (behind the list's end, or an empty place of many sequences).  Up to
+// kListed sequences: without empty places, and long walks first, so that the
+// grid does not end on them, in four classes (walks beyond 1/2, 1/4 and 1/8
+// of the longest, the others).
 template <int WALK>
 __device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ cu_a, int64_t total_a,
                                           const int32_t* __restrict__ cu_b, int64_t total_b,
                                           int n_seqs, bool causal, int rows, int64_t target,
                                           int lane, int32_t* status) {
+  if (n_seqs > kListed)
+    return search_tile<WALK>(cu_a, total_a, cu_b, total_b, n_seqs, rows, target, lane, status);
   Tile t{};
   int64_t before = 0;
-  // the offsets of the next 32 sequences, loaded one turn ahead: four
-  // independent loads a turn
-  int next[4] = {0, 0, 0, 0};
-  auto fetch = [&](int s) {
-    if (s < n_seqs) {
-      next[0] = __ldg(cu_a + s), next[1] = __ldg(cu_a + s + 1);
-      next[2] = __ldg(cu_b + s), next[3] = __ldg(cu_b + s + 1);
-    }
-  };
-  fetch(lane);
-  for (int base = 0; base < n_seqs; base += 32) {
-    const int s = base + lane;
-    Span a{0, 0}, b{0, 0};
-    if (s < n_seqs) {
-      a = checked_span(next[0], next[1], total_a, status);
-      b = checked_span(next[2], next[3], total_b, status);
-    }
-    fetch(s + 32);
-    const int n_all = (a.len + rows - 1) / rows;
-    int longest = a.len > 0 ? (b.len + 127) / 128 : 0;
-    int classes = 1;
-    if (n_seqs > 1 && n_seqs <= 32) {
-      longest = __reduce_max_sync(0xffffffffu, longest);
-      classes = 4;
-    }
-    int done = 0;  // this sequence's tiles in the classes so far
-    for (int c = 0; c < classes; ++c) {
-      const int upto = c + 1 == classes
-                           ? n_all
-                           : tiles_beyond<WALK>(a, b, causal, rows, longest >> (c + 1));
-      const int n = upto - done;
-      int incl = n;
+  Span a{0, 0}, b{0, 0};
+  if (lane < n_seqs) {
+    a = checked_span(__ldg(cu_a + lane), __ldg(cu_a + lane + 1), total_a, status);
+    b = checked_span(__ldg(cu_b + lane), __ldg(cu_b + lane + 1), total_b, status);
+  }
+  const int n_all = (a.len + rows - 1) / rows;
+  const int longest =
+      __reduce_max_sync(0xffffffffu, a.len > 0 ? (b.len + 127) / 128 : 0);
+  const int classes = n_seqs > 1 ? 4 : 1;
+  int done = 0;  // this sequence's tiles in the classes so far
+  for (int c = 0; c < classes; ++c) {
+    const int upto = c + 1 == classes
+                         ? n_all
+                         : tiles_beyond<WALK>(a, b, causal, rows, longest >> (c + 1));
+    const int n = upto - done;
+    int incl = n;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      const uint32_t m = __ballot_sync(0xffffffffu, before + incl > target);
-      if (m) {
-        const int l = __ffs(m) - 1;
-        // its place among the sequence's tiles, longest walk first
-        const int p = __shfl_sync(0xffffffffu, done + int(target - (before + incl - n)), l);
-        const int n_l = __shfl_sync(0xffffffffu, n_all, l);
-        t.any = true;
-        t.seq = base + l;
-        t.tile = WALK == kWalkQ ? n_l - 1 - p : p;
-        t.a = {__shfl_sync(0xffffffffu, a.start, l), __shfl_sync(0xffffffffu, a.len, l)};
-        t.b = {__shfl_sync(0xffffffffu, b.start, l), __shfl_sync(0xffffffffu, b.len, l)};
-        return t;
-      }
-      before += __shfl_sync(0xffffffffu, incl, 31);
-      done = upto;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
     }
+    const uint32_t m = __ballot_sync(0xffffffffu, before + incl > target);
+    if (m) {
+      const int l = __ffs(m) - 1;
+      // its place among the sequence's tiles, longest walk first
+      const int p = __shfl_sync(0xffffffffu, done + int(target - (before + incl - n)), l);
+      const int n_l = __shfl_sync(0xffffffffu, n_all, l);
+      t.any = true;
+      t.seq = l;
+      t.tile = WALK == kWalkQ ? n_l - 1 - p : p;
+      t.a = {__shfl_sync(0xffffffffu, a.start, l), __shfl_sync(0xffffffffu, a.len, l)};
+      t.b = {__shfl_sync(0xffffffffu, b.start, l), __shfl_sync(0xffffffffu, b.len, l)};
+      return t;
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+    done = upto;
   }
   return t;
 }

@@ -27,7 +27,9 @@
  * behind cu[n_seqs] (or in front of cu[0]) are neither read as data nor
  * written and may hold anything, NaN included; rows of a sequence must be
  * finite.  Offsets that descend or leave the tensor are reported as
- * BSA_ERR_INVALID_ARG through the status word and read as an empty sequence.
+ * BSA_ERR_INVALID_ARG through the status word and read as an empty sequence;
+ * among more than 32 sequences they may leave rows of others unwritten.  At
+ * most 2^30 rows a tensor.
  *
  * Paged cache.  k_cache and v_cache share the strides (stride_page,
  * stride_token, stride_head), element strides that are multiples of 8, of a

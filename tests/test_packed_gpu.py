@@ -64,6 +64,9 @@ FWD = [
     ([1000, 700], [1000, 700], 5, 5, 64, FP, False),
     ([5] * 70 + [200], [5] * 70 + [200], 4, 4, 64, BF, True),    # more sequences than a warp
     ([2, 129] * 40, [129, 2] * 40, 2, 1, 128, FP, True),
+    ([0] * 30 + [3, 700, 0, 257] + [0] * 30, [9] * 31 + [600, 5, 300] + [1] * 30, 3, 1, 64, BF, True),
+    ([20] * 1100, [20] * 1100, 1, 1, 64, BF, True),
+    ([0] * 33, [5] * 33, 2, 2, 64, BF, True),
 ]
 
 
@@ -217,6 +220,23 @@ def test_fwd_reports_bad_offsets(cuda_ok):
         check_fwd(q[good], k[good], v[good], [n], [n], True, out[good], None, 1 / 8)
 
 
+def test_fwd_reports_bad_offsets_among_many(cuda_ok):
+    """Among many sequences, found by a search, a bad one is reported."""
+    lens = [7, 0, 3, 150] * 10
+    q, k, v = inputs(lens, lens, 2, 2, 64, BF, tail=0)
+    prob, good = bsa.SeqProblem.make(2, 2, 64), cu_of(lens)
+    for at, value in ((17, 10_000_000), (25, 0), (1, -5), (40, q.shape[0] + 1)):
+        cu, st = good.clone(), status_word()
+        cu[at] = value
+        out = torch.full_like(q, 3.0)
+        bsa.packed_attn_fwd(prob, q, k, v, cu, cu, out, dev_status=st)
+        assert int(st) == 1
+    out, st = torch.full_like(q, 3.0), status_word()
+    bsa.packed_attn_fwd(prob, q, k, v, good, good, out, dev_status=st)
+    assert int(st) == 0
+    check_fwd(q, k, v, lens, lens, True, out, None, 1 / 8)
+
+
 def test_fwd_captured_and_replayed(cuda_ok):
     lens = [130, 257]
     q, k, v = inputs(lens, lens, 4, 2, 128, FP, tail=0)
@@ -328,6 +348,8 @@ BWD = [
     ([300], [1300], 2, 2, 128, FP, False, 1.0),
     ([200, 77, 300], [200, 77, 300], 20, 20, 64, BF, True, 1.0),  # a CTA per key tile
     ([130, 257], [130, 300], 44, 22, 128, FP, False, 1.0),
+    ([0] * 30 + [3, 700, 0, 257] + [0] * 30, [9] * 31 + [600, 5, 300] + [1] * 30, 3, 1, 64, BF, True, 1.0),
+    ([20, 3] * 550, [20, 3] * 550, 1, 1, 64, FP, True, 1.0),
     ([1100], [1100], 8, 1, 128, BF, True, 1.0),                  # several CTAs per key tile
     ([1000, 130], [900, 140], 8, 1, 64, FP, True, 1.0),
 ]
