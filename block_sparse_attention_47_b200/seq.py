@@ -312,12 +312,19 @@ class PagedAttention:
         self._step_cu = torch.arange(max_seqs + 1, dtype=torch.int32, device=dev)
 
     def append(self, q, k, v, cu, rope=None, interleaved=False, rope_rows=None, k_out=None):
-        """Add packed tokens to the sequences; returns the rotated q."""
-        self.seq_lens += cu[1:] - cu[:-1]
+        """Add packed tokens to the sequences; returns the rotated q.  A call
+        that is refused leaves the lengths as they were."""
+        _ints(cu, self.seq_lens.shape[0] + 1, self.seq_lens.get_device(), "cu")
+        new = cu[1:] - cu[:-1]
         q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        kv_append(self.prob, k, v, self.k_cache, self.v_cache, self.block_table, cu, self.seq_lens,
-                  rope=rope, interleaved=interleaved, rope_rows=rope_rows, q=q, q_out=q_out,
-                  k_out=k_out, dev_status=self.status)
+        self.seq_lens += new
+        try:
+            kv_append(self.prob, k, v, self.k_cache, self.v_cache, self.block_table, cu,
+                      self.seq_lens, rope=rope, interleaved=interleaved, rope_rows=rope_rows, q=q,
+                      q_out=q_out, k_out=k_out, dev_status=self.status)
+        except Exception:
+            self.seq_lens -= new
+            raise
         return q_out
 
     def prompt(self, q, k, v, cu, rope=None, interleaved=False, rope_rows=None):

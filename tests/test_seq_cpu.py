@@ -253,3 +253,22 @@ def test_bwd_workspace():
     for tq, n in ((0, 0), (1, 1), (1000, 3), (127, 127)):
         assert bsa.packed_bwd_workspace_bytes(prob(), tq, n) == 4 * (2 * 8 * 128 * (tq // 128 + n + 1) + 2 * 2)
     assert call("bsa_packed_attn_bwd", seq._PACKED, bwd_args(tq=0, tk=0)) == 0
+
+
+def test_a_refused_append_leaves_the_lengths():
+    at = bsa.PagedAttention(prob_of(), n_pages=4, page_size=16, max_seqs=3, max_pages_per_seq=2, device="cpu")
+    x = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        at.step(x, x, x)
+    with pytest.raises(ValueError, match="cu must be"):
+        at.prompt(x, x, x, torch.tensor([0, 3], dtype=torch.int32))
+    assert at.seq_lens.tolist() == [0, 0, 0]
+
+
+def prob_of():
+    return bsa.SeqProblem.make(2, 2, 64)
+
+
+def test_rows_of_a_packed_call_are_limited():
+    rc = call("bsa_packed_attn_bwd", seq._PACKED, bwd_args(tk=(1 << 30) + 1, n_seqs=1))
+    assert rc == SHAPE and b"2^30" in bsa.lib().bsa_last_error()
