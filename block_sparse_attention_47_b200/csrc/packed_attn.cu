@@ -27,11 +27,14 @@
 // since 0 times a NaN would reach the output.
 //
 // The grid is one CTA per SM; a CTA takes every G-th tile of the list, longest
-// walks first and back and forth, so that shares come out alike.  The copy
-// warp finds the next tile and loads its first operands while the last steps
-// of the current one run, and a warpgroup writes its rows while the pipe is
-// on the other tile's or the next one's products: at 4 steps a tile (cross
-// attention to a short text) the set-up was two fifths of the time.
+// walks first and back and forth, so that shares come out alike.  The steps of
+// a CTA's entries form one sequence: the stage of an entry's last V holds the
+// next one's first K, and the turn that issues a tile's last PV issues its next
+// entry's first scores behind it, while the other tile is still at its softmax
+// (the copy warp has found that entry and loaded its Q by then).  A warpgroup
+// writes its rows under those products.  8,064 and 5,003 queries to 512 and 77
+// keys, 24 heads, d = 128: 77 us, 91 with an entry's scores issued once both
+// tiles of the previous one had finished.
 //
 // Few tiles and many keys (the next part of a long text): a cluster of CTAs
 // shares a tile's key steps; each leaves its maxima, sums and unnormalised O
@@ -63,11 +66,12 @@ struct FwdCfg {
   static constexpr int OFF_KV = 2 * TILE;
   static constexpr int OFF_STAGE = OFF_KV + RING * 2 * TILE;
   static constexpr int OFF_BAR = OFF_STAGE + 8 * STAGE;
-  // full[RING] empty[RING] q q_free info[2] info_free[2] s[2] p[2] o[2] fix_go
-  // fixed drain
-  static constexpr int N_BARS = 2 * RING + 15;
-  static constexpr int OFF_MISC = OFF_BAR + 8 * N_BARS;  // tmem, abort, then info[2][8]
-  static constexpr int SMEM = OFF_MISC + 16 + 64 + 1024;
+  static constexpr int INFO = 4;                  // entries that may be published at a time
+  // full[RING] empty[RING] q[2] q_free[2] info[INFO] info_free[INFO] s[2] p[2]
+  // o[2] fix_go fixed drain
+  static constexpr int N_BARS = 2 * RING + 2 * INFO + 13;
+  static constexpr int OFF_MISC = OFF_BAR + 8 * N_BARS;  // tmem, abort, then info[INFO][8]
+  static constexpr int SMEM = OFF_MISC + 16 + 32 * INFO + 1024;
   static constexpr uint32_t TMEM_COLS = 512, COL_O = 256;
   // a cluster's join: fp32 O [256][D], then (max, sum) [256]; over Q and the ring
   static constexpr int OFF_ML = 256 * D * 4;
@@ -96,12 +100,13 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t base = (raw + 1023u) & ~1023u;
   unsigned char* sm = smem_raw + (base - raw);
   const uint32_t full = base + C::OFF_BAR, empty = full + 8 * RING, bar_q = empty + 8 * RING;
-  const uint32_t q_free = bar_q + 8, bar_info = q_free + 8, info_free = bar_info + 16;
-  const uint32_t bar_s = info_free + 16, bar_p = bar_s + 16, bar_o = bar_p + 16;
+  const uint32_t q_free = bar_q + 16, bar_info = q_free + 16;
+  const uint32_t info_free = bar_info + 8 * C::INFO;
+  const uint32_t bar_s = info_free + 8 * C::INFO, bar_p = bar_s + 16, bar_o = bar_p + 16;
   const uint32_t fix_go = bar_o + 16, fixed = fix_go + 8, drain = fixed + 8;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 4);
-  volatile int* info = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 16);  // [2][8]
+  volatile int* info = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 16);  // [INFO][8]
   auto slot = [&](int j) { return base + C::OFF_KV + uint32_t(j % RING) * (2 * C::TILE); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_hp = HEADS ? g.heads >> 1 : g.heads;
@@ -137,9 +142,9 @@ __global__ void __launch_bounds__(384, 1)
   // A wait may last as long as another tile's walk.
   constexpr uint64_t kLong = 20000000000ull;
   auto take = [&](int it, bool whole_warp) {
-    const uint32_t b = uint32_t(it & 1);
+    const uint32_t b = uint32_t(it % C::INFO);
     Plan w{};
-    bool got = mbar_wait(bar_info + 8 * b, (it >> 1) & 1, abort_flag, kLong);
+    bool got = mbar_wait(bar_info + 8 * b, (it / C::INFO) & 1, abort_flag, kLong);
     if (whole_warp) got = __all_sync(0xffffffffu, got);
     if (!got) {  // some role has given up, or does now
       report_timeout(abort_flag, io.status);
@@ -159,11 +164,13 @@ __global__ void __launch_bounds__(384, 1)
         mbar_init(full + 8 * s, 1);
         mbar_init(empty + 8 * s, 1);
       }
-      mbar_init(bar_q, 1);
-      mbar_init(q_free, 1);
+      for (int b = 0; b < C::INFO; ++b) {
+        mbar_init(bar_info + 8 * b, 1);
+        mbar_init(info_free + 8 * b, 10);  // products, tails, 8 softmax warps
+      }
       for (int u = 0; u < 2; ++u) {
-        mbar_init(bar_info + 8 * u, 1);
-        mbar_init(info_free + 8 * u, 10);  // products, tails, 8 softmax warps
+        mbar_init(bar_q + 8 * u, 1);
+        mbar_init(q_free + 8 * u, 1);
         mbar_init(bar_s + 8 * u, 1);
         mbar_init(bar_p + 8 * u, 4);
         mbar_init(bar_o + 8 * u, 1);
@@ -214,89 +221,105 @@ __global__ void __launch_bounds__(384, 1)
   float m = -INFINITY, l = 0.f;
 
   // The softmax threads hold a row of 128 scores and take the other warps'
-  // registers: 256 * 216 + 128 * 72 = 384 * 168, those of the launch.
+  // registers: 256 * 200 + 128 * 104 = 384 * 168, those of the launch.
   if (warp == 8) {
     // ------------------------------------------------------------ copies
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    int c = 0, nq = 0;  // stages so far, entries with a walk so far
-    for (int it = 0; !SPLIT || it < 1; ++it) {
-      if (it > 0) {
-        ++at;
-        next = find();
-      }
-      if (it >= 2) {
-        ok = __all_sync(0xffffffffu, mbar_wait(info_free + 8 * (it & 1), ((it >> 1) - 1) & 1,
-                                               abort_flag, kLong));
-        if (!ok) break;
-      }
-      const Plan w = plan({next.any, next.a.start, next.a.len, next.b.start, next.b.len,
-                           next.tile * (HEADS ? 128 : 256), unit_of(at) % n_hp, 0, 0, 0, 0});
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    int x = 0, nq0 = 0, nq1 = 0;  // stages and Q tiles so far (lane 0)
+    auto entry = [&] {
+      return plan({next.any, next.a.start, next.a.len, next.b.start, next.b.len,
+                   next.tile * (HEADS ? 128 : 256), unit_of(at) % n_hp, 0, 0, 0, 0});
+    };
+    auto publish = [&](int it, const Plan& w) {
+      const uint32_t b = uint32_t(it % C::INFO);
+      if (it >= C::INFO &&
+          !__all_sync(0xffffffffu, mbar_wait(info_free + 8 * b, (it / C::INFO - 1) & 1, abort_flag,
+                                             kLong)))
+        return false;
       if (lane == 0) {
-        volatile int* e = info + 8 * (it & 1);
+        volatile int* e = info + 8 * b;
         e[0] = w.any, e[1] = w.q0, e[2] = w.Lq, e[3] = w.k0, e[4] = w.Lk, e[5] = w.first, e[6] = w.hp;
-        mbar_arrive(bar_info + 8 * (it & 1));
+        mbar_arrive(bar_info + 8 * b);
       }
       __syncwarp();
-      if (!w.any) break;
-      if (w.n == 0) continue;
-      if (lane == 0) {
-        const int head0 = HEADS ? 2 * w.hp : w.hp, kvh = head0 / g.group;
-        auto load_stage = [&](int j) {  // V_(j-1) (none for j = 0) and K_j (none for j = n)
-          const int x = c + j;
-          if (x >= RING && !mbar_wait(empty + 8 * (x % RING), ((x / RING) - 1) & 1, abort_flag))
-            return false;
-          const uint32_t bar = full + 8 * (x % RING);
-          const int row = w.k0 + (w.kb + j) * 128;
-          mbar_arrive_expect_tx(bar, ((j > 0) + (j < w.n)) * C::TILE);
-          if (j > 0) tma_load_rows(slot(x), &mv, bar, row - 128, kvh);
-          if (j < w.n) tma_load_rows(slot(x) + C::TILE, &mk, bar, row, kvh);
-          return true;
-        };
-        ok = load_stage(0);
-        // Q once the previous entry's last scores have read theirs
-        if (ok && nq > 0) ok = mbar_wait(q_free, (nq - 1) & 1, abort_flag, kLong);
-        if (ok) {
-          mbar_arrive_expect_tx(bar_q, ((w.n0 > 0) + (w.n1 > 0)) * C::TILE);
-          for (int t = 0; t < 2; ++t)
-            if ((t ? w.n1 : w.n0) > 0)
-              tma_load_rows(base + C::OFF_Q + t * C::TILE, &mq, bar_q,
-                            w.q0 + w.first + (HEADS ? 0 : 128 * t), head0 + (HEADS ? t : 0));
-          ++nq;
+      return true;
+    };
+    auto kv_head = [&](const Plan& w) { return (HEADS ? 2 * w.hp : w.hp) / g.group; };
+    // the next stage: V rows from vrow and K rows from krow on (none for < 0)
+    auto load_stage = [&](int vrow, int vhead, int krow, int khead) {
+      if (x >= RING && !mbar_wait(empty + 8 * (x % RING), ((x / RING) - 1) & 1, abort_flag))
+        return false;
+      const uint32_t bar = full + 8 * (x % RING);
+      mbar_arrive_expect_tx(bar, ((vrow >= 0) + (krow >= 0)) * C::TILE);
+      if (vrow >= 0) tma_load_rows(slot(x), &mv, bar, vrow, vhead);
+      if (krow >= 0) tma_load_rows(slot(x) + C::TILE, &mk, bar, krow, khead);
+      ++x;
+      return true;
+    };
+    // a tile's Q once the previous entry's last scores have read theirs
+    auto load_q = [&](const Plan& w, int t, int n, int& nq) {
+      if (n == 0) return true;
+      if (nq > 0 && !mbar_wait(q_free + 8 * t, (nq - 1) & 1, abort_flag, kLong)) return false;
+      ++nq;
+      mbar_arrive_expect_tx(bar_q + 8 * t, C::TILE);
+      tma_load_rows(base + C::OFF_Q + t * C::TILE, &mq, bar_q + 8 * t,
+                    w.q0 + w.first + (HEADS ? 0 : 128 * t), (HEADS ? 2 * w.hp + t : w.hp));
+      return true;
+    };
+    Plan w = entry();
+    ok = publish(0, w);
+    bool joined = false;  // K_0 came beside the previous entry's last V
+    for (int it = 1; ok && w.any; ++it) {
+      const bool walks = w.n > 0;
+      const int head = kv_head(w);
+      int row = w.k0 + w.kb * 128;  // K of the next step
+      if (walks && lane == 0) {
+        if (!joined) ok = load_stage(-1, 0, row, head);
+        ok = ok && load_q(w, 0, w.n0, nq0) && load_q(w, 1, w.n1, nq1);
+        for (int j = 1; ok && j < w.n; ++j) {
+          row += 128;
+          ok = load_stage(row - 128, head, row, head);
         }
-        for (int j = 1; ok && j <= w.n; ++j) ok = load_stage(j);
       }
-      c += w.n + 1;
       ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
       if (!ok) break;
+      w = Plan{};
+      if (!SPLIT) {
+        ++at;
+        next = find();
+        w = entry();
+        ok = publish(it, w);
+        if (!ok) break;
+      }
+      joined = walks && w.any && w.n > 0;
+      if (walks && lane == 0)
+        ok = load_stage(row, head, joined ? w.k0 + w.kb * 128 : -1, kv_head(w));
+      ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
     }
     if (lane == 0) {
       if (!ok) report_timeout(abort_flag, io.status);
-      // on an abort copies may still be landing: the newest into Q and each
-      // slot; a phase that never began ends the wait at its limit
+      // on an abort copies may still be landing: the newest into Q and each slot
       if (!ok || *abort_flag) {
-        if (nq > 0) mbar_wait(bar_q, (nq - 1) & 1, nullptr, 200000000ull);
-        for (int s = 0; s < RING; ++s) {
-          const int uses = c > s ? (c - s + RING - 1) / RING : 0;
-          for (int x = uses > 1 ? uses - 2 : 0; x < uses; ++x)
-            mbar_wait(full + 8 * s, x & 1, nullptr, 100000000ull);
-        }
+        if (nq0 > 0) mbar_wait(bar_q, (nq0 - 1) & 1, nullptr, 200000000ull);
+        if (nq1 > 0) mbar_wait(bar_q + 8, (nq1 - 1) & 1, nullptr, 200000000ull);
+        for (int i = x > RING ? x - RING : 0; i < x; ++i)
+          mbar_wait(full + 8 * (i % RING), (i / RING) & 1, nullptr, 200000000ull);
       }
     }
     __syncwarp();
   } else if (warp == 9) {
     // ---------------------------------------------------------- products
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (lane == 0) {
       constexpr uint32_t id_s = idesc_f32<T>(128, 128, false);
       constexpr uint32_t id_o = idesc_f32<T>(128, D, true);
-      int c = 0, nq = 0, tails = 0;
+      int c = 0, nq0 = 0, nq1 = 0, tails = 0;  // c: the stage of an entry's K_0
       int done0 = 0, done1 = 0;  // steps of each tile so far
-      auto wait_full = [&](int i) {
-        const int x = c + i;
+      auto wait_full = [&](int x) {
         return mbar_wait(full + 8 * (x % RING), (x / RING) & 1, abort_flag);
       };
-      auto scores = [&](int t, int i) {  // S_t = Q_t K_i^T
-        const uint32_t sq = base + C::OFF_Q + t * C::TILE, sk = slot(c + i) + C::TILE;
+      auto scores = [&](int t, int x) {  // S_t = Q_t K^T, K in stage x
+        const uint32_t sq = base + C::OFF_Q + t * C::TILE, sk = slot(x) + C::TILE;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (kk / 4) * C::BOX + (kk % 4) * 32;
@@ -305,56 +328,70 @@ __global__ void __launch_bounds__(384, 1)
         }
         tc_commit(bar_s + 8 * t);
       };
-      for (int it = 0; !SPLIT || it < 1; ++it) {
-        const Plan w = take(it, false);
-        if (!w.any) break;
-        const int n = w.n, n0 = w.n0, n1 = w.n1;
-        if (n == 0) continue;
-        const bool has_tail = (w.kb + n) * 128 > w.Lk;  // the walk ends in a partial key tile
-        ok = wait_full(0) && mbar_wait(bar_q, nq & 1, abort_flag);
-        ++nq;
-        if (!ok) break;
+      auto first_scores = [&](int t, int n, int& nq, int x) {  // of an entry
+        if (n == 0) return true;
+        if (!mbar_wait(bar_q + 8 * t, nq++ & 1, abort_flag)) return false;
         tc_fence_after();
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if ((t ? n1 : n0) > 0) scores(t, 0);
-        tc_commit(empty + 8 * (c % RING));
-        if (n == 1) tc_commit(q_free);
+        scores(t, x);
+        if (n == 1) tc_commit(q_free + 8 * t);
+        return true;
+      };
+      Plan w = take(0, false);
+      bool joined = false;  // the first scores were issued with the previous entry's last step
+      for (int it = 1; w.any;) {
+        if (w.n == 0) {
+          if (SPLIT) break;
+          w = take(it++, false);
+          continue;
+        }
+        const int n = w.n;
+        const bool has_tail = (w.kb + n) * 128 > w.Lk;  // the walk ends in a partial key tile
+        if (!joined) {
+          ok = wait_full(c) && first_scores(0, w.n0, nq0, c) && first_scores(1, w.n1, nq1, c);
+          if (!ok) break;
+          tc_commit(empty + 8 * (c % RING));
+        }
         // test hook: with `stall` set no PV is issued and the softmax's wait runs out
         if (io.stall) break;
+        Plan nx{};
         for (int i = 0; i < n; ++i) {
-          ok = wait_full(i + 1);
-          if (ok && has_tail && i == n - 1) {
+          const bool last = i == n - 1;
+          if (last && !SPLIT) nx = take(it++, false);
+          joined = last && nx.any && nx.n > 0;
+          ok = wait_full(c + i + 1);
+          if (ok && has_tail && last) {
             mbar_arrive(fix_go);  // the tail rows of V are zeroed by warp 10
             ok = mbar_wait(fixed, tails & 1, abort_flag);
             ++tails;
           }
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            const int nt = t ? n1 : n0;
-            if (!ok || i >= nt) continue;
-            ok = mbar_wait(bar_p + 8 * t, ((t ? done1 : done0) + i) & 1, abort_flag);
-            if (!ok) continue;
-            tc_fence_after();
-            const uint32_t sv = slot(c + i + 1);
+            const int nt = t ? w.n1 : w.n0;
+            if (ok && i < nt) {
+              ok = mbar_wait(bar_p + 8 * t, (t ? done1 : done0)++ & 1, abort_flag);
+              if (!ok) continue;
+              tc_fence_after();
+              const uint32_t sv = slot(c + i + 1);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              tc_mma_ts(tmem + C::COL_O + 128u * t, tmem + 128u * t + 8u * kk,
-                        sdesc_sw128(sv + kk * 2048, C::BOX, 1024), id_o,
-                        (i > 0 || kk > 0) ? 1u : 0u);
-            if (i + 1 < nt)
-              scores(t, i + 1);
-            else
-              tc_commit(bar_o + 8 * t);
+              for (int kk = 0; kk < 8; ++kk)
+                tc_mma_ts(tmem + C::COL_O + 128u * t, tmem + 128u * t + 8u * kk,
+                          sdesc_sw128(sv + kk * 2048, C::BOX, 1024), id_o,
+                          (i > 0 || kk > 0) ? 1u : 0u);
+              if (i + 1 < nt) {
+                scores(t, c + i + 1);
+                if (i + 2 == nt) tc_commit(q_free + 8 * t);
+              } else {
+                tc_commit(bar_o + 8 * t);
+              }
+            }
+            if (ok && joined) ok = first_scores(t, t ? nx.n1 : nx.n0, t ? nq1 : nq0, c + n);
           }
           if (!ok) break;
           tc_commit(empty + 8 * ((c + i + 1) % RING));
-          if (i + 2 == n) tc_commit(q_free);
         }
         if (!ok) break;
-        done0 += n0;
-        done1 += n1;
-        c += n + 1;
+        c += joined ? n : n + 1;
+        w = nx;
       }
       if (!ok) report_timeout(abort_flag, io.status);
       // every MMA this thread issued has completed once the drain barrier flips
@@ -364,30 +401,33 @@ __global__ void __launch_bounds__(384, 1)
     __syncwarp();
   } else if (warp == 10) {
     // ----------------------------------------------------------- V tails
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     int c = 0, tails = 0;
-    for (int it = 0; !SPLIT || it < 1; ++it) {
-      const Plan w = take(it, true);
-      if (!w.any) break;
-      c += w.n > 0 ? w.n + 1 : 0;
-      if (w.n == 0 || (w.kb + w.n) * 128 <= w.Lk) continue;
-      ok = __all_sync(0xffffffffu, mbar_wait(fix_go, tails & 1, abort_flag, kLong));
-      if (!ok) break;
-      ++tails;
-      const uint32_t sv = slot(c - 1);
-      for (int bx = 0; bx < C::KB; ++bx)
-        for (int o = (w.Lk & 127) * 128 + lane * 16; o < C::BOX; o += 512)
-          st_shared_v4(sv + bx * C::BOX + o, make_uint4(0u, 0u, 0u, 0u));
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(fixed);
+    Plan w = take(0, true);
+    for (int it = 1; w.any; ++it) {
+      Plan nx{};
+      if (!SPLIT) nx = take(it, true);
+      if (w.n > 0 && (w.kb + w.n) * 128 > w.Lk) {
+        ok = __all_sync(0xffffffffu, mbar_wait(fix_go, tails & 1, abort_flag, kLong));
+        if (!ok) break;
+        ++tails;
+        const uint32_t sv = slot(c + w.n);
+        for (int bx = 0; bx < C::KB; ++bx)
+          for (int o = (w.Lk & 127) * 128 + lane * 16; o < C::BOX; o += 512)
+            st_shared_v4(sv + bx * C::BOX + o, make_uint4(0u, 0u, 0u, 0u));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(fixed);
+      }
+      if (w.n > 0) c += nx.any && nx.n > 0 ? w.n : w.n + 1;
+      w = nx;
     }
     if (!ok && lane == 0) report_timeout(abort_flag, io.status);
   } else if (warp == 11) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   } else {
     // ----------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const uint32_t tS = tmem + 128u * u + lane_base;
     const float sl2 = g.scale * kLog2e;
     int done = 0, tiles = 0;  // steps and tiles with a walk so far
