@@ -31,7 +31,7 @@
 // a CTA's entries form one sequence: the stage of an entry's last V holds the
 // next one's first K, and the turn that issues a tile's last PV issues its next
 // entry's first scores behind it, while the other tile is still at its softmax
-// (the copy warp has found that entry and loaded its Q by then).  A warpgroup
+// (that entry has been found and its Q loaded by then).  A warpgroup
 // writes its rows under those products.  8,064 and 5,003 queries to 512 and 77
 // keys, 24 heads, d = 128: 77 us, 91 with an entry's scores issued once both
 // tiles of the previous one had finished.
@@ -54,8 +54,8 @@ constexpr int kMinShare = 4;  // key steps a CTA of a cluster takes at least
 
 template <int D>
 struct FwdCfg {
-  // warps 0-3 / 4-7: softmax of tile 0 / 1; 8: finds the tiles, copies;
-  // 9: products; 10: the V tails
+  // warps 0-3 / 4-7: softmax of tile 0 / 1; 8: copies; 9: products; 10: the V
+  // tails; 11: finds the entries
   static constexpr int kThreads = 384;
   static constexpr int KB = D / 64;               // 64-column boxes
   static constexpr int BOX = 128 * 128;           // one box of 128 rows
@@ -85,6 +85,7 @@ struct Plan {
   bool any;
   int q0, Lq, k0, Lk, first, hp;
   int kb, n0, n1, n;  // first key tile, steps of the two tiles, their maximum
+  int off0, off1;     // where their rows start, from `first` on
 };
 
 template <typename T, int D, bool HEADS, bool SPLIT>
@@ -116,15 +117,20 @@ __global__ void __launch_bounds__(384, 1)
   auto unit_of = [&](int it) { return it * ctas + ((it & 1) ? ctas - 1 - cta : cta); };
 
   // (by value throughout: nothing of a role may live in local memory)
-  auto plan = [&](Plan w) {
+  // Two tiles of one head change places in every other entry, so that a run of
+  // sequences of up to 128 queries, one tile each, serves both warpgroups
+  // (4,096 of 64 tokens, 8 heads: 820 us, 1,026 on one warpgroup).
+  auto plan = [&](Plan w, int it) {
+    w.off0 = !HEADS && (it & 1) ? 128 : 0;
+    w.off1 = HEADS ? 0 : 128 - w.off0;
     auto steps = [&](int r) {  // key tiles that a tile's last row sees
       if (r >= w.Lq) return 0;
       const int last = min(r + 128, w.Lq) - 1;
       const int lim = g.causal ? min(w.Lk, max(0, last + 1 + w.Lk - w.Lq)) : w.Lk;
       return (lim + 127) >> 7;
     };
-    w.n0 = steps(w.first);
-    w.n1 = HEADS ? w.n0 : steps(w.first + 128);
+    w.n0 = steps(w.first + w.off0);
+    w.n1 = HEADS ? w.n0 : steps(w.first + w.off1);
     w.n = max(w.n0, w.n1);
     w.kb = 0;
     if (SPLIT) {
@@ -137,7 +143,7 @@ __global__ void __launch_bounds__(384, 1)
     }
     return w;
   };
-  // The entry `it` as published by the copy warp; false at the list's end or
+  // The entry `it` as published by the finder; false at the list's end or
   // on an abort.  All lanes of the calling warp, or one thread alone (mask).
   // A wait may last as long as another tile's walk.
   constexpr uint64_t kLong = 20000000000ull;
@@ -155,7 +161,7 @@ __global__ void __launch_bounds__(384, 1)
     w.q0 = e[1], w.Lq = e[2], w.k0 = e[3], w.Lk = e[4], w.first = e[5], w.hp = e[6];
     if (whole_warp) __syncwarp();
     if (!whole_warp || lane == 0) mbar_arrive(info_free + 8 * b);
-    return w.any ? plan(w) : w;
+    return w.any ? plan(w, it) : w;
   };
 
   if (warp == 10) {
@@ -166,7 +172,7 @@ __global__ void __launch_bounds__(384, 1)
       }
       for (int b = 0; b < C::INFO; ++b) {
         mbar_init(bar_info + 8 * b, 1);
-        mbar_init(info_free + 8 * b, 10);  // products, tails, 8 softmax warps
+        mbar_init(info_free + 8 * b, 11);  // every warp but the finder
       }
       for (int u = 0; u < 2; ++u) {
         mbar_init(bar_q + 8 * u, 1);
@@ -206,7 +212,7 @@ __global__ void __launch_bounds__(384, 1)
     }
     return Tile{};
   };
-  if (warp == 8) next = find();
+  if (warp == 11) next = find();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -226,24 +232,6 @@ __global__ void __launch_bounds__(384, 1)
     // ------------------------------------------------------------ copies
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     int x = 0, nq0 = 0, nq1 = 0;  // stages and Q tiles so far (lane 0)
-    auto entry = [&] {
-      return plan({next.any, next.a.start, next.a.len, next.b.start, next.b.len,
-                   next.tile * (HEADS ? 128 : 256), unit_of(at) % n_hp, 0, 0, 0, 0});
-    };
-    auto publish = [&](int it, const Plan& w) {
-      const uint32_t b = uint32_t(it % C::INFO);
-      if (it >= C::INFO &&
-          !__all_sync(0xffffffffu, mbar_wait(info_free + 8 * b, (it / C::INFO - 1) & 1, abort_flag,
-                                             kLong)))
-        return false;
-      if (lane == 0) {
-        volatile int* e = info + 8 * b;
-        e[0] = w.any, e[1] = w.q0, e[2] = w.Lq, e[3] = w.k0, e[4] = w.Lk, e[5] = w.first, e[6] = w.hp;
-        mbar_arrive(bar_info + 8 * b);
-      }
-      __syncwarp();
-      return true;
-    };
     auto kv_head = [&](const Plan& w) { return (HEADS ? 2 * w.hp : w.hp) / g.group; };
     // the next stage: V rows from vrow and K rows from krow on (none for < 0)
     auto load_stage = [&](int vrow, int vhead, int krow, int khead) {
@@ -263,11 +251,10 @@ __global__ void __launch_bounds__(384, 1)
       ++nq;
       mbar_arrive_expect_tx(bar_q + 8 * t, C::TILE);
       tma_load_rows(base + C::OFF_Q + t * C::TILE, &mq, bar_q + 8 * t,
-                    w.q0 + w.first + (HEADS ? 0 : 128 * t), (HEADS ? 2 * w.hp + t : w.hp));
+                    w.q0 + w.first + (t ? w.off1 : w.off0), (HEADS ? 2 * w.hp + t : w.hp));
       return true;
     };
-    Plan w = entry();
-    ok = publish(0, w);
+    Plan w = take(0, true);
     bool joined = false;  // K_0 came beside the previous entry's last V
     for (int it = 1; ok && w.any; ++it) {
       const bool walks = w.n > 0;
@@ -284,13 +271,7 @@ __global__ void __launch_bounds__(384, 1)
       ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
       if (!ok) break;
       w = Plan{};
-      if (!SPLIT) {
-        ++at;
-        next = find();
-        w = entry();
-        ok = publish(it, w);
-        if (!ok) break;
-      }
+      if (!SPLIT) w = take(it, true);
       joined = walks && w.any && w.n > 0;
       if (walks && lane == 0)
         ok = load_stage(row, head, joined ? w.k0 + w.kb * 128 : -1, kv_head(w));
@@ -424,7 +405,27 @@ __global__ void __launch_bounds__(384, 1)
     }
     if (!ok && lane == 0) report_timeout(abort_flag, io.status);
   } else if (warp == 11) {
+    // ----------------------------------------------------------- entries
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    for (int it = 0;; ++it) {
+      const uint32_t b = uint32_t(it % C::INFO);
+      if (it >= C::INFO) {
+        ok = __all_sync(0xffffffffu, mbar_wait(info_free + 8 * b, (it / C::INFO - 1) & 1,
+                                               abort_flag, kLong));
+        if (!ok) break;
+      }
+      if (lane == 0) {
+        volatile int* e = info + 8 * b;
+        e[0] = next.any, e[1] = next.a.start, e[2] = next.a.len, e[3] = next.b.start;
+        e[4] = next.b.len, e[5] = next.tile * (HEADS ? 128 : 256), e[6] = unit_of(at) % n_hp;
+        mbar_arrive(bar_info + 8 * b);
+      }
+      __syncwarp();
+      if (SPLIT || !next.any) break;
+      ++at;
+      next = find();
+    }
+    if (!ok && lane == 0) report_timeout(abort_flag, io.status);
   } else {
     // ----------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
@@ -435,7 +436,7 @@ __global__ void __launch_bounds__(384, 1)
       const Plan w = take(it, true);
       if (!w.any) break;
       nu = u ? w.n1 : w.n0;
-      const int r = w.first + (HEADS ? 0 : 128 * u) + quad * 32 + lane;  // row within the sequence
+      const int r = w.first + (u ? w.off1 : w.off0) + quad * 32 + lane;  // row within the sequence
       const bool exists = r < w.Lq;
       const int lim = !exists ? 0 : (g.causal ? min(w.Lk, max(0, r + 1 + w.Lk - w.Lq)) : w.Lk);
       m = -INFINITY;
