@@ -257,8 +257,8 @@ struct DqCfg {
   static constexpr int OFF_V = OFF_K + NK * TILE;
   static constexpr int OFF_BAR = OFF_V + NV * TILE;
   // kfull[NK] kempty[NK] vfull[NV] vempty[NV] sd_ready read x_ready[2]
-  // x_free own q do fix_go fixed sums done drain[2]
-  static constexpr int N_BARS = 2 * NK + 2 * NV + 14;
+  // x_free own q do fix_go fixed sums done drain[2] s_ready[2] s_read[2]
+  static constexpr int N_BARS = 2 * NK + 2 * NV + 18;
   static constexpr int OFF_MISC = OFF_BAR + 8 * N_BARS;
   static constexpr int OFF_SUM = OFF_MISC + 64;  // float [group][128]: D of the two halves
   static constexpr int SMEM = OFF_SUM + 1024 + 1024;
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t sd_ready = vempty + 8 * NV, read = sd_ready + 8, x_ready = read + 8;
   const uint32_t x_free = x_ready + 16, own = x_free + 8, bar_q = own + 8;
   const uint32_t bar_do = bar_q + 8, fix_go = bar_do + 8, fixed = fix_go + 8, sums = fixed + 8;
-  const uint32_t done = sums + 8, drain = done + 8;
+  const uint32_t done = sums + 8, drain = done + 8, s_ready = drain + 16, s_read = s_ready + 16;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 4);
   int* found = reinterpret_cast<int*>(sm + C::OFF_MISC + 8);
@@ -326,6 +326,10 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(done, 2);
       mbar_init(drain, 1);
       mbar_init(drain + 8, 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(s_ready + 8 * b, 1);
+        mbar_init(s_read + 8 * b, 8);
+      }
       *abort_flag = 0;
       fence_mbar_init();
       fence_proxy_async_smem();
@@ -431,7 +435,35 @@ __global__ void __launch_bounds__(384, 1)
     if (lane == 0 && np > 0) {
       constexpr uint32_t idesc_s = idesc_f32<T>(128, 128, false);
       bool ok = mbar_wait(own, 0, abort_flag) && mbar_wait(bar_q, 0, abort_flag);
-      for (int p = 0; ok && p < nt; ++p) {
+      // the first sweep's S alternate between their columns and the idle sum's,
+      // so that P is formed under the next products (2,500 cycles a step with
+      // S and dP handed over together)
+      for (int p = 0; ok && p < lead; ++p) {
+        ok = mbar_wait(kfull + 8 * (p % NK), (p / NK) & 1, abort_flag) &&
+             (p < 2 || mbar_wait(s_read + 8 * (p & 1), ((p >> 1) - 1) & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk / 4) * C::BOX + (kk % 4) * 32;
+          tc_mma_ss(tmem + (p & 1 ? C::COL_ACC : C::COL_S), sdesc_sw128(sQ + off, 16, 1024),
+                    sdesc_sw128(kslot(p) + off, 16, 1024), idesc_s, kk > 0);
+        }
+        tc_commit(s_ready + 8 * (p & 1));
+        tc_commit(kempty + 8 * (p % NK));  // no accumulation reads it
+        ok = mbar_wait(vfull + 8 * (p % NV), (p / NV) & 1, abort_flag) &&
+             (p == 0 || mbar_wait(read, (p - 1) & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc_mma_ts(tmem + C::COL_DP, tmem + C::COL_DO + 8u * kk,
+                    sdesc_sw128(vslot(p) + (kk / 4) * C::BOX + (kk % 4) * 32, 16, 1024), idesc_s,
+                    kk > 0);
+        tc_commit(sd_ready);
+        tc_commit(vempty + 8 * (p % NV));
+      }
+      for (int p = lead; ok && p < nt; ++p) {
         if (!mbar_wait(kfull + 8 * (p % NK), (p / NK) & 1, abort_flag) ||
             !mbar_wait(vfull + 8 * (p % NV), (p / NV) & 1, abort_flag) ||
             (p > 0 && !mbar_wait(read, (p - 1) & 1, abort_flag))) {
@@ -456,7 +488,6 @@ __global__ void __launch_bounds__(384, 1)
         }
         tc_commit(sd_ready);
         tc_commit(vempty + 8 * (p % NV));
-        if (p < lead) tc_commit(kempty + 8 * (p % NK));  // no accumulation reads it
       }
       if (!ok) report_timeout(abort_flag, io.status);
       tc_commit(done);
@@ -541,27 +572,44 @@ __global__ void __launch_bounds__(384, 1)
       // ---- D = sum_j P_ij dP_ij over this group's columns, then both groups'
       float part = 0.f;
       for (int p = 0; ok && p < np; ++p) {
-        ok = __all_sync(0xffffffffu, mbar_wait(sd_ready, p & 1, abort_flag));
+        // (a single step's S and dP come together and are read again)
+        ok = __all_sync(0xffffffffu, lead ? mbar_wait(s_ready + 8 * (p & 1), (p >> 1) & 1, abort_flag)
+                                          : mbar_wait(sd_ready, 0, abort_flag));
         if (!ok) break;
         tc_fence_after();
         const int seen = lim - 128 * p - 64 * grp;
+        uint32_t sv[64];
+        BSA_TMEM_LD64((p & 1 ? tmem + C::COL_ACC + 64u * grp + lane_base : tS), sv);
+        if (lead) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_read + 8 * (p & 1));
+        }
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          float x0, x1;
+          fma_f32x2(x0, x1, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]), sl2, sl2, -lse2,
+                    -lse2);
+          sv[c] = __float_as_uint(ex2_approx(x0));
+          sv[c + 1] = __float_as_uint(ex2_approx(x1));
+        }
+        if (lead) ok = __all_sync(0xffffffffu, mbar_wait(sd_ready, p & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t dp[64];
+        BSA_TMEM_LD64(tDP, dp);
+        if (lead) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(read);
+        }
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int h2 = 0; h2 < 2; ++h2) {
-          uint32_t sv[32], dp[32];
-          BSA_TMEM_LD32(tS + 32u * h2, sv);
-          BSA_TMEM_LD32(tDP + 32u * h2, dp);
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const float pr = ex2_approx(fmaf(__uint_as_float(sv[c]), sl2, -lse2));
-            // masked columns may hold anything
-            acc[c & 3] = 32 * h2 + c < seen ? fmaf(pr, __uint_as_float(dp[c]), acc[c & 3])
-                                            : acc[c & 3];
-          }
+        for (int c = 0; c < 64; ++c) {
+          // masked columns may hold anything
+          const float x = fmaf(__uint_as_float(sv[c]), __uint_as_float(dp[c]), acc[c & 3]);
+          acc[c & 3] = c < seen ? x : acc[c & 3];
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0 && lead) mbar_arrive(read);  // a single step is read again
         part += (acc[0] + acc[1]) + (acc[2] + acc[3]);
       }
       volatile float* buf = reinterpret_cast<volatile float*>(sm + C::OFF_SUM);

@@ -324,7 +324,6 @@ __device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ cu_a, int6
   if (n_seqs > kListed)
     return search_tile<WALK>(cu_a, total_a, cu_b, total_b, n_seqs, rows, target, lane, status);
   Tile t{};
-  int64_t before = 0;
   Span a{0, 0}, b{0, 0};
   if (lane < n_seqs) {
     a = checked_span(__ldg(cu_a + lane), __ldg(cu_a + lane + 1), total_a, status);
@@ -333,35 +332,42 @@ __device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ cu_a, int6
   const int n_all = (a.len + rows - 1) / rows;
   const int longest =
       __reduce_max_sync(0xffffffffu, a.len > 0 ? (b.len + 127) / 128 : 0);
-  const int classes = n_seqs > 1 ? 4 : 1;
-  int done = 0;  // this sequence's tiles in the classes so far
-  for (int c = 0; c < classes; ++c) {
-    const int upto = c + 1 == classes
-                         ? n_all
-                         : tiles_beyond<WALK>(a, b, causal, rows, longest >> (c + 1));
-    const int n = upto - done;
-    int incl = n;
+  // this sequence's tiles of each class and of those before it, and the scans
+  // of all four over the sequences side by side
+  int upto[4], incl[4];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    const uint32_t m = __ballot_sync(0xffffffffu, before + incl > target);
-    if (m) {
-      const int l = __ffs(m) - 1;
-      // its place among the sequence's tiles, longest walk first
-      const int p = __shfl_sync(0xffffffffu, done + int(target - (before + incl - n)), l);
-      const int n_l = __shfl_sync(0xffffffffu, n_all, l);
-      t.any = true;
-      t.seq = l;
-      t.tile = WALK == kWalkQ ? n_l - 1 - p : p;
-      t.a = {__shfl_sync(0xffffffffu, a.start, l), __shfl_sync(0xffffffffu, a.len, l)};
-      t.b = {__shfl_sync(0xffffffffu, b.start, l), __shfl_sync(0xffffffffu, b.len, l)};
-      return t;
-    }
-    before += __shfl_sync(0xffffffffu, incl, 31);
-    done = upto;
+  for (int c = 0; c < 4; ++c) {
+    upto[c] = c == 3 ? n_all : tiles_beyond<WALK>(a, b, causal, rows, longest >> (c + 1));
+    incl[c] = upto[c] - (c ? upto[c - 1] : 0);
   }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int v = __shfl_up_sync(0xffffffffu, incl[c], o);
+      if (lane >= o) incl[c] += v;
+    }
+  }
+  int64_t before = 0;
+  int in = 0, up = 0;  // the scans of the class that holds the place
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int total = __shfl_sync(0xffffffffu, incl[c], 31);
+    if (!t.any) {
+      t.any = before + total > target;
+      in = incl[c], up = upto[c];
+      if (!t.any) before += total;
+    }
+  }
+  if (!t.any) return t;
+  const int l = __ffs(__ballot_sync(0xffffffffu, before + in > target)) - 1;
+  // its place among the sequence's tiles, longest walk first
+  const int p = __shfl_sync(0xffffffffu, int(target - before) - in + up, l);
+  const int n_l = __shfl_sync(0xffffffffu, n_all, l);
+  t.seq = l;
+  t.tile = WALK == kWalkQ ? n_l - 1 - p : p;
+  t.a = {__shfl_sync(0xffffffffu, a.start, l), __shfl_sync(0xffffffffu, a.len, l)};
+  t.b = {__shfl_sync(0xffffffffu, b.start, l), __shfl_sync(0xffffffffu, b.len, l)};
   return t;
 }
 
