@@ -256,9 +256,9 @@ struct DqCfg {
   static constexpr int OFF_K = TILE;
   static constexpr int OFF_V = OFF_K + NK * TILE;
   static constexpr int OFF_BAR = OFF_V + NV * TILE;
-  // kfull[NK] kempty[NK] vfull[NV] vempty[NV] sd_ready read x_ready[2]
+  // kfull[NK] kempty[NK] vfull[NV] vempty[NV] sd_ready read x_ready
   // x_free own q do fix_go fixed sums done drain[2] s_ready[2] s_read[2]
-  static constexpr int N_BARS = 2 * NK + 2 * NV + 18;
+  static constexpr int N_BARS = 2 * NK + 2 * NV + 17;
   static constexpr int OFF_MISC = OFF_BAR + 8 * N_BARS;
   static constexpr int OFF_SUM = OFF_MISC + 64;  // float [group][128]: D of the two halves
   static constexpr int SMEM = OFF_SUM + 1024 + 1024;
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t kfull = base + C::OFF_BAR, kempty = kfull + 8 * NK;
   const uint32_t vfull = kempty + 8 * NK, vempty = vfull + 8 * NV;
   const uint32_t sd_ready = vempty + 8 * NV, read = sd_ready + 8, x_ready = read + 8;
-  const uint32_t x_free = x_ready + 16, own = x_free + 8, bar_q = own + 8;
+  const uint32_t x_free = x_ready + 8, own = x_free + 8, bar_q = own + 8;
   const uint32_t bar_do = bar_q + 8, fix_go = bar_do + 8, fixed = fix_go + 8, sums = fixed + 8;
   const uint32_t done = sums + 8, drain = done + 8, s_ready = drain + 16, s_read = s_ready + 16;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);
@@ -314,8 +314,7 @@ __global__ void __launch_bounds__(384, 1)
       }
       mbar_init(sd_ready, 1);
       mbar_init(read, 8);
-      mbar_init(x_ready, 4);
-      mbar_init(x_ready + 8, 4);
+      mbar_init(x_ready, 8);
       mbar_init(x_free, 1);
       mbar_init(own, 4);
       mbar_init(bar_q, 1);
@@ -496,25 +495,20 @@ __global__ void __launch_bounds__(384, 1)
     }
     __syncwarp();
   } else if (warp == 10) {
-    // ---- dQ += dS_w K_w as each group's dS is in; B = its 64 K rows, N-major
+    // ---- dQ += dS K once both groups' dS is in; B = K, N-major
     if (lane == 0 && np > 0) {
       constexpr uint32_t idesc_acc = idesc_f32<T>(128, D, true);
       bool ok = true;
       // test hook: with `stall` set no accumulation is issued (the timeout path)
       for (int p = lead; ok && p < nt && !io.stall; ++p) {
-        for (int h = 0; h < 2; ++h) {
-          if (!mbar_wait(x_ready + 8 * h, (p - lead) & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_ts(tmem + C::COL_ACC, tmem + C::COL_DS + 32u * h + 8u * kk,
-                      sdesc_sw128(kslot(p) + h * 8192 + kk * 2048, C::BOX, 1024), idesc_acc,
-                      (p > lead || h > 0 || kk > 0) ? 1u : 0u);
-        }
+        ok = mbar_wait(x_ready, (p - lead) & 1, abort_flag);
         if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          tc_mma_ts(tmem + C::COL_ACC, tmem + C::COL_DS + 8u * kk,
+                    sdesc_sw128(kslot(p) + kk * 2048, C::BOX, 1024), idesc_acc,
+                    (p > lead || kk > 0) ? 1u : 0u);
         tc_commit(x_free);
         tc_commit(kempty + 8 * (p % NK));
       }
@@ -671,7 +665,7 @@ __global__ void __launch_bounds__(384, 1)
       BSA_TMEM_ST32(tDS, pk);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(x_ready + 8 * grp);
+      if (lane == 0) mbar_arrive(x_ready);
     }
     if (ok && np > 0) ok = __all_sync(0xffffffffu, mbar_wait(done, 0, abort_flag));
     if (!ok) {
@@ -713,9 +707,9 @@ struct DkdvCfg {
   static constexpr int OFF_STG = 2 * TILE;     // [slot][Q | dO]
   static constexpr int OFF_VEC = OFF_STG + NR * 2 * TILE;  // [slot][lse2 128 | D 128] fp32
   static constexpr int OFF_BAR = OFF_VEC + NR * 1024;
-  // full[NR] s_ready dp_ready dp_read st_issued p_ready[2] ds_ready[2] x_free own
+  // full[NR] s_ready dp_ready dp_read st_issued p_ready ds_ready x_free own
   // fix_go fixed done drain[2]
-  static constexpr int N_BARS = NR + 15;
+  static constexpr int N_BARS = NR + 13;
   static constexpr int OFF_MISC = OFF_BAR + 8 * N_BARS;
   static constexpr int SMEM = OFF_MISC + 64 + 1024;
   static constexpr uint32_t TMEM_COLS = 512;
@@ -745,8 +739,8 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t sK = base + C::OFF_K, sV = base + C::OFF_V;
   const uint32_t full = base + C::OFF_BAR, s_ready = full + 8 * NR, dp_ready = s_ready + 8;
   const uint32_t dp_read = dp_ready + 8, st_issued = dp_read + 8;
-  const uint32_t p_ready = st_issued + 8, ds_ready = p_ready + 16;
-  const uint32_t x_free = ds_ready + 16, own = x_free + 8;
+  const uint32_t p_ready = st_issued + 8, ds_ready = p_ready + 8;
+  const uint32_t x_free = ds_ready + 8, own = x_free + 8;
   const uint32_t fix_go = own + 8, fixed = fix_go + 8, done = fixed + 8, drain = done + 8;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 4);
@@ -800,10 +794,8 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(dp_ready, 1);
       mbar_init(dp_read, 8);
       mbar_init(st_issued, 1);
-      for (int w = 0; w < 2; ++w) {
-        mbar_init(p_ready + 8 * w, 4);
-        mbar_init(ds_ready + 8 * w, 4);
-      }
+      mbar_init(p_ready, 8);
+      mbar_init(ds_ready, 8);
       mbar_init(x_free, 1);
       mbar_init(own, 1);
       mbar_init(fix_go, 1);
@@ -945,31 +937,31 @@ __global__ void __launch_bounds__(384, 1)
     }
     __syncwarp();
   } else if (warp == 10) {
-    // ---- dV += P^T_w dO_w as each group's P^T is in, then dK += dS^T_w Q_w;
-    // B read N-major
+    // ---- dV += P^T dO once both groups' P^T is in, then dK += dS^T Q; B read
+    // N-major.  (All products by one thread, which needs no wait between dK and
+    // the next dP^T, took 270 us where two threads take 260.)
     if (lane == 0 && np > 0) {
       constexpr uint32_t idesc_acc = idesc_f32<T>(128, D, true);
       bool ok = true;
       // test hook: with `stall` set no accumulation is issued (the timeout path)
       for (int p = 0; ok && p < np && !io.stall; ++p) {
         const uint32_t cS = 128u * (p & 1);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {  // dV of the two groups, dK of the two
-          const int h = x & 1;
-          // dK is queued behind the next S^T, which the groups wait for first
-          if (x == 2 && p + 1 < np) ok = ok && mbar_wait(st_issued, (p + 1) & 1, abort_flag);
-          ok = ok && mbar_wait((x < 2 ? p_ready : ds_ready) + 8 * h, p & 1, abort_flag);
-          if (!ok) break;
+        auto sums = [&](uint32_t acc, uint32_t col, uint32_t rows) {
           tc_fence_after();
-          const uint32_t rows = (x < 2 ? doslot(p) : qslot(p)) + h * 8192;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_ts(tmem + (x < 2 ? C::COL_DV : C::COL_DK),
-                      tmem + cS + 64u * h + (x < 2 ? 0u : 32u) + 8u * kk,
+          for (int kk = 0; kk < 8; ++kk)
+            tc_mma_ts(tmem + acc, tmem + col + 64u * (kk >> 2) + 8u * (kk & 3),
                       sdesc_sw128(rows + kk * 2048, C::BOX, 1024), idesc_acc,
-                      (p > 0 || h > 0 || kk > 0) ? 1u : 0u);
-        }
+                      (p > 0 || kk > 0) ? 1u : 0u);
+        };
+        ok = mbar_wait(p_ready, p & 1, abort_flag);
         if (!ok) break;
+        sums(C::COL_DV, cS, doslot(p));
+        // dK is queued behind the next S^T, which the groups wait for first
+        ok = (p + 1 == np || mbar_wait(st_issued, (p + 1) & 1, abort_flag)) &&
+             mbar_wait(ds_ready, p & 1, abort_flag);
+        if (!ok) break;
+        sums(C::COL_DK, cS + 32u, qslot(p));
         tc_commit(x_free);
       }
       if (!ok) report_timeout(abort_flag, io.status);
@@ -1040,7 +1032,7 @@ __global__ void __launch_bounds__(384, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_ready + 8 * grp);
+      if (lane == 0) mbar_arrive(p_ready);
       // dS^T = P^T * (dP^T - D) beside P^T, 32 columns at a time
       ok = __all_sync(0xffffffffu, mbar_wait(dp_ready, p & 1, abort_flag));
       if (!ok) break;
@@ -1075,7 +1067,7 @@ __global__ void __launch_bounds__(384, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ds_ready + 8 * grp);
+      if (lane == 0) mbar_arrive(ds_ready);
     }
     if (ok && np > 0) ok = __all_sync(0xffffffffu, mbar_wait(done, 0, abort_flag));
     if (!ok) {
