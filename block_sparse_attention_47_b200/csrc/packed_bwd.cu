@@ -18,10 +18,10 @@
 // return to tensor memory as A operands of the accumulations.  In dK/dV two
 // 128-column regions change roles from step to step: S^T in one, dP^T in the
 // other; P^T and dS^T go over S^T, so the next S^T can follow into dP^T's
-// region as soon as the groups have read it, under their remaining work (a batch
-// of 4,096, 2,048, 1,111 and 300 tokens, 24/8 heads, d = 128: 279 us, with P^T
-// over S^T and dS^T over dP^T 311; its products alone take 2,048 cycles a step,
-// some 130 us).
+// region as soon as the groups have read it, under their remaining work.  A
+// batch of 4,096, 2,048, 1,111 and 300 tokens, 24/8 heads, d = 128: dK/dV 261 us
+// (3,340 cycles a step, 2,048 of them products), dQ 223 us (2,200 a step, 1,536
+// of them products).
 //
 // Preparation: lse2 and D are written per 128-row tile of a sequence (rows
 // behind its end get lse2 = +inf, D = 0, so that P = 0 there), sequence b at
@@ -56,7 +56,7 @@ constexpr float kPShift = 13.f;
 // over that of rounding an exact result, bf16, at 5, 128, 1,500 and 4,000
 // causal tokens: none 2.41, 1.71, 1.59, 1.55; 8 steps 1.33, 1.41, 1.45, 1.47;
 // all 1.33, 1.41, 1.44, 1.43.  Forward and backward of 7,555 tokens x 24
-// heads: 660, 695 and 834 us.
+// heads: 633, 660 and 769 us.
 constexpr int kExactSteps = 8;
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
