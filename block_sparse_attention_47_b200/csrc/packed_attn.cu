@@ -50,7 +50,7 @@ namespace bsa {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kMinShare = 4;  // key steps a CTA of a cluster takes at least
+constexpr int kMinShare = 2;  // key steps a CTA of a cluster takes at least
 
 template <int D>
 struct FwdCfg {
@@ -660,12 +660,15 @@ cudaError_t launch_t(const SeqGeo& g, const CUtensorMap* maps, const PackedIO& i
 // so one wave of CTAs for one sequence, and no more than 112 in clusters of
 // eight, of which few find room at a time.  Sequences of several lengths even
 // out over two waves (256, 511 and 64 queries to 5,000, 511 and 2,113 keys: 76 |
-// 45 | 41 | 72).
+// 45 | 41 | 72).  Short walks: 1 query to 1,000 keys of 8/2 heads 21 us by one, 12
+// by four; 513 to 513 of 16/8 heads 16.6 and 18.5; 384 to 1,500 of 8/2 heads 20.7
+// by four, 23.0 by eight; 130 to 2,000 18.0 and 16.5.
 int split_ranks(const PackedIO& io, int64_t rows, int slots) {
   // the sequences' last tiles are half full on average
   const int64_t units = ((io.total_q + rows - 1) / rows + io.n_seqs / 2) * slots;
-  if (units > 74 || io.total_k <= 2 * kMinShare * 128) return 1;
-  int ranks = io.total_k > 4 * kMinShare * 128 && units * 8 <= 112 ? 8 : 4;
+  const int64_t steps = io.total_k / 128;  // of a walk at most
+  if (units > 74 || steps < 6) return 1;
+  int ranks = steps >= 15 && units * 8 <= 112 ? 8 : 4;
   if (ranks == 4 && units * 4 > (io.n_seqs > 1 ? 300 : 148)) ranks = 2;
   return ranks;
 }
