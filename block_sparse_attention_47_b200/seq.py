@@ -292,7 +292,9 @@ class PagedAttention:
     the pages, the block table and lengths of up to max_seqs sequences, the
     decode workspace and a status word.  Pages are handed out by the caller:
     write page numbers into `block_table` (int32 [max_seqs,
-    max_pages_per_seq]) before tokens reach them.
+    max_pages_per_seq]) before tokens reach them.  It starts at -1, which is
+    no page: a token that reaches such an entry is reported through the status
+    word (check_status) and written nowhere.
 
     `seq_lens` holds the cached tokens of each sequence.  prompt() and step()
     add the new tokens to it and run on every sequence of the cache in order,
@@ -305,7 +307,7 @@ class PagedAttention:
         shape = (n_pages, page_size, prob.kv_heads, prob.head_dim)
         self.k_cache = torch.empty(shape, dtype=dt, device=dev)
         self.v_cache = torch.empty(shape, dtype=dt, device=dev)
-        self.block_table = torch.zeros((max_seqs, max_pages_per_seq), dtype=torch.int32, device=dev)
+        self.block_table = torch.full((max_seqs, max_pages_per_seq), -1, dtype=torch.int32, device=dev)
         self.seq_lens = torch.zeros(max_seqs, dtype=torch.int32, device=dev)
         self.workspace = torch.empty(decode_workspace_bytes(prob), dtype=torch.uint8, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)

@@ -148,3 +148,31 @@ def test_gradients_against_differences(cuda_ok):
         slack = abs(ds[0] - ds[1]) + noise + 4 * u * abs(exact) + max(abs(m - exact) for m in moved)
         assert abs(ds[1] - moved[1]) <= slack, (i, ds, moved, slack)
         assert slack <= 0.2 * abs(exact), (i, slack, exact)
+
+
+def test_pages_that_nobody_assigned(cuda_ok):
+    """A row of the table that nobody filled and a sequence's next page that is
+    not there yet name no page: their tokens are reported, page 0 (another
+    sequence's) stays as it was and the sequences beside them are right."""
+    prob = bsa.SeqProblem.make(4, 2, 64)
+    at = bsa.PagedAttention(prob, 8, 4, 3, 4)
+    at.k_cache.zero_()
+    at.v_cache.zero_()
+    at.block_table[0, 0] = 0  # 3 tokens and the next: one page
+    at.block_table[1, 0] = 5  # 4 tokens: the next one needs a page it does not have
+    gen = torch.Generator().manual_seed(1)
+    q, k, v = (torch.randn(7, x, 64, generator=gen).bfloat16().cuda() for x in (4, 2, 2))
+    at.prompt(q, k, v, cu_of([3, 4, 0]))
+    at.check_status()
+    before = [at.k_cache.clone(), at.v_cache.clone()]
+    q1, k1, v1 = (torch.randn(3, x, 64, generator=gen).bfloat16().cuda() for x in (4, 2, 2))
+    out = at.step(q1, k1, v1)
+    with pytest.raises(bsa.BSAError, match="INVALID_ARG"):
+        at.check_status()
+    for c, b, new in ((at.k_cache, before[0], k1), (at.v_cache, before[1], v1)):
+        b[0, 3] = new[0]
+        assert torch.equal(c, b)
+    for h in range(4):
+        kk, vv = (torch.cat([t[:3, h // 2], n[:1, h // 2]]) for t, n in ((k, k1), (v, v1)))
+        o, _, p, g = attention64(q1[:1, h], kk, vv, torch.tensor([4]), 1 / 8)
+        assert_within(out[:1, h], o, output_bound(o, p, vv, g, torch.bfloat16))
