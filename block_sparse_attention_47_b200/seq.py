@@ -313,39 +313,56 @@ class PagedAttention:
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         self._step_cu = torch.arange(max_seqs + 1, dtype=torch.int32, device=dev)
 
+    def _add(self, lens, new, q, k, v, cu, table, rope, interleaved, rope_rows, k_out=None,
+             attend=None):
+        """Append `new` tokens and attend to them: the rotated q, or what
+        `attend` makes of it.  Whatever is refused, the lengths are taken back
+        (slots behind them may hold anything)."""
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        lens += new
+        try:
+            kv_append(self.prob, k, v, self.k_cache, self.v_cache, table, cu, lens, rope=rope,
+                      interleaved=interleaved, rope_rows=rope_rows, q=q, q_out=q_out, k_out=k_out,
+                      dev_status=self.status)
+            return q_out if attend is None else attend(q_out)
+        except Exception:
+            lens -= new
+            raise
+
+    def _new(self, cu):
+        _ints(cu, self.seq_lens.shape[0] + 1, self.seq_lens.get_device(), "cu")
+        return cu[1:] - cu[:-1]
+
     def append(self, q, k, v, cu, rope=None, interleaved=False, rope_rows=None, k_out=None):
         """Add packed tokens to the sequences; returns the rotated q.  A call
-        that is refused leaves the lengths as they were."""
-        _ints(cu, self.seq_lens.shape[0] + 1, self.seq_lens.get_device(), "cu")
-        new = cu[1:] - cu[:-1]
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        self.seq_lens += new
-        try:
-            kv_append(self.prob, k, v, self.k_cache, self.v_cache, self.block_table, cu,
-                      self.seq_lens, rope=rope, interleaved=interleaved, rope_rows=rope_rows, q=q,
-                      q_out=q_out, k_out=k_out, dev_status=self.status)
-        except Exception:
-            self.seq_lens -= new
-            raise
-        return q_out
+        that is refused leaves the lengths as they were, here and below."""
+        return self._add(self.seq_lens, self._new(cu), q, k, v, cu, self.block_table, rope,
+                         interleaved, rope_rows, k_out)
 
     def prompt(self, q, k, v, cu, rope=None, interleaved=False, rope_rows=None):
         """Whole prompts of sequences that were empty: cache their keys and
         values and return their causal attention (as prob.causal says)."""
         k_rot = torch.empty_like(k, memory_format=torch.contiguous_format)
-        q_rot = self.append(q, k, v, cu, rope, interleaved, rope_rows, k_out=k_rot)
-        out = torch.empty_like(q_rot)
-        packed_attn_fwd(self.prob, q_rot, k_rot, v, cu, cu, out, dev_status=self.status)
-        return out
+
+        def attend(q_rot):
+            out = torch.empty_like(q_rot)
+            packed_attn_fwd(self.prob, q_rot, k_rot, v, cu, cu, out, dev_status=self.status)
+            return out
+
+        return self._add(self.seq_lens, self._new(cu), q, k, v, cu, self.block_table, rope,
+                         interleaved, rope_rows, k_rot, attend)
 
     def step(self, q, k, v, rope=None, interleaved=False, rope_rows=None):
         """One new token per sequence, q [max_seqs, heads, head_dim]: cache it
         and return its attention over its sequence."""
-        q_rot = self.append(q, k, v, self._step_cu, rope, interleaved, rope_rows)
-        out = torch.empty_like(q_rot)
-        paged_attn_decode(self.prob, q_rot, self.k_cache, self.v_cache, self.block_table,
-                          self.seq_lens, out, self.workspace, dev_status=self.status)
-        return out
+        def attend(q_rot):
+            out = torch.empty_like(q_rot)
+            paged_attn_decode(self.prob, q_rot, self.k_cache, self.v_cache, self.block_table,
+                              self.seq_lens, out, self.workspace, dev_status=self.status)
+            return out
+
+        return self._add(self.seq_lens, 1, q, k, v, self._step_cu, self.block_table, rope,
+                         interleaved, rope_rows, attend=attend)
 
     def check_status(self):
         v = int(self.status.item())

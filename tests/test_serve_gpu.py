@@ -176,3 +176,25 @@ def test_pages_that_nobody_assigned(cuda_ok):
         kk, vv = (torch.cat([t[:3, h // 2], n[:1, h // 2]]) for t, n in ((k, k1), (v, v1)))
         o, _, p, g = attention64(q1[:1, h], kk, vv, torch.tensor([4]), 1 / 8)
         assert_within(out[:1, h], o, output_bound(o, p, vv, g, torch.bfloat16))
+
+
+def test_a_refused_call_leaves_the_lengths(cuda_ok):
+    """Whatever part of a call is refused, the lengths are as before it, and
+    the corrected call writes where the refused one did."""
+    prob = bsa.SeqProblem.make(4, 2, 64)
+    at, other = layer(prob, 2, page=4), layer(prob, 2, page=4)
+    gen = torch.Generator().manual_seed(2)
+    q, k, v = (torch.randn(9, x, 64, generator=gen).bfloat16().cuda() for x in (4, 2, 2))
+    cu = cu_of([5, 4])
+    for bad in (v[:, :1].expand(9, 2, 64), v[:1].expand(9, 2, 64)):  # appended as they are, but not attended to
+        with pytest.raises(bsa.BSAError, match="broadcast"):
+            at.prompt(q, k, bad, cu)
+        assert at.seq_lens.tolist() == [0, 0]
+    assert torch.equal(at.prompt(q, k, v, cu), other.prompt(q, k, v, cu))
+    for bad in ((q[:3], k[:3], v[:3]), (q[:2], k[:3], v[:3]), (q[:2, :2], k[:2], v[:2])):
+        with pytest.raises(ValueError):
+            at.step(*bad)
+        assert at.seq_lens.tolist() == [5, 4]
+    assert torch.equal(at.step(q[:2], k[:2], v[:2]), other.step(q[:2], k[:2], v[:2]))
+    at.check_status()
+    assert at.seq_lens.tolist() == [6, 5]
