@@ -296,10 +296,10 @@ class PagedAttention:
     no page: a token that reaches such an entry is reported through the status
     word (check_status) and written nowhere.
 
-    `seq_lens` holds the cached tokens of each sequence.  prompt() and step()
-    add the new tokens to it and run on every sequence of the cache in order,
-    as the model's batch does; a sequence without new tokens in a prompt()
-    call has length 0 in cu."""
+    `seq_lens` holds the cached tokens of each sequence; prompt() and step()
+    add the new tokens to it.  prompt() runs on every sequence of the cache in
+    order, one without new tokens having length 0 in cu; step() on the first
+    ones, as many as it gets tokens."""
 
     def __init__(self, prob, n_pages, page_size, max_seqs, max_pages_per_seq, device="cuda"):
         self.prob = prob
@@ -353,16 +353,23 @@ class PagedAttention:
                          interleaved, rope_rows, k_rot, attend)
 
     def step(self, q, k, v, rope=None, interleaved=False, rope_rows=None):
-        """One new token per sequence, q [max_seqs, heads, head_dim]: cache it
-        and return its attention over its sequence."""
+        """One new token for each of the first n sequences, q [n, heads,
+        head_dim], n up to max_seqs: cache it and return its attention over its
+        sequence.  The sequences behind them rest; what is served changes
+        places by its block_table row and its length."""
+        n = _shape3(q, "q")
+        if n > self.seq_lens.shape[0]:
+            raise ValueError("%d tokens for %d sequences" % (n, self.seq_lens.shape[0]))
+        lens, table = self.seq_lens[:n], self.block_table[:n]
+
         def attend(q_rot):
             out = torch.empty_like(q_rot)
-            paged_attn_decode(self.prob, q_rot, self.k_cache, self.v_cache, self.block_table,
-                              self.seq_lens, out, self.workspace, dev_status=self.status)
+            paged_attn_decode(self.prob, q_rot, self.k_cache, self.v_cache, table, lens, out,
+                              self.workspace, dev_status=self.status)
             return out
 
-        return self._add(self.seq_lens, 1, q, k, v, self._step_cu, self.block_table, rope,
-                         interleaved, rope_rows, attend=attend)
+        return self._add(lens, 1, q, k, v, self._step_cu[:n + 1], table, rope, interleaved,
+                         rope_rows, attend=attend)
 
     def check_status(self):
         v = int(self.status.item())

@@ -198,3 +198,25 @@ def test_a_refused_call_leaves_the_lengths(cuda_ok):
     assert torch.equal(at.step(q[:2], k[:2], v[:2]), other.step(q[:2], k[:2], v[:2]))
     at.check_status()
     assert at.seq_lens.tolist() == [6, 5]
+
+
+def test_the_first_sequences_take_a_step(cuda_ok):
+    """A layer made for more sequences than there are: those behind the rows
+    rest, with tokens or without."""
+    prob, n = bsa.SeqProblem.make(4, 2, 64), 64
+    at, small = layer(prob, 5, page=4), layer(prob, 2, page=4)
+    small.block_table.copy_(at.block_table[:2])
+    small.k_cache, small.v_cache = torch.zeros_like(at.k_cache), torch.zeros_like(at.v_cache)
+    gen = torch.Generator().manual_seed(3)
+    q, k, v = (torch.randn(12, x, n, generator=gen).bfloat16().cuda() for x in (4, 2, 2))
+    at.prompt(q, k, v, cu_of([5, 4, 0, 3, 0]))
+    small.prompt(q[:9], k[:9], v[:9], cu_of([5, 4]))
+    cache = at.k_cache.clone()
+    for i in range(3):
+        x = (q[i:i + 2], k[i:i + 2], v[i:i + 2])
+        assert torch.equal(at.step(*x), small.step(*x))
+    assert at.seq_lens.tolist() == [8, 7, 0, 3, 0]
+    assert at.step(q[:0], k[:0], v[:0]).shape == (0, 4, 64)
+    at.check_status()
+    third = at.block_table[3].long()
+    assert torch.equal(at.k_cache[third].nan_to_num(7.0), cache[third].nan_to_num(7.0))
