@@ -341,15 +341,22 @@ class PagedAttention:
 
     def prompt(self, q, k, v, cu, rope=None, interleaved=False, rope_rows=None):
         """Whole prompts of sequences that were empty: cache their keys and
-        values and return their causal attention (as prob.causal says)."""
+        values and return their causal attention (as prob.causal says).  New
+        tokens of a sequence that holds some are cached, too, but their
+        attention lacks the earlier ones: that is reported as INVALID_ARG
+        through the status word (check_status), the output being meaningless."""
+        new = self._new(cu)
+        # the host does not know the lengths: 1 (INVALID_ARG) where a sequence has both
+        both = torch.minimum(new, self.seq_lens).amax().clamp_(0, 1)
         k_rot = torch.empty_like(k, memory_format=torch.contiguous_format)
 
         def attend(q_rot):
             out = torch.empty_like(q_rot)
             packed_attn_fwd(self.prob, q_rot, k_rot, v, cu, cu, out, dev_status=self.status)
+            torch.maximum(self.status, both, out=self.status)
             return out
 
-        return self._add(self.seq_lens, self._new(cu), q, k, v, cu, self.block_table, rope,
+        return self._add(self.seq_lens, new, q, k, v, cu, self.block_table, rope,
                          interleaved, rope_rows, k_rot, attend)
 
     def step(self, q, k, v, rope=None, interleaved=False, rope_rows=None):

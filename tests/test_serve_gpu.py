@@ -220,3 +220,19 @@ def test_the_first_sequences_take_a_step(cuda_ok):
     at.check_status()
     third = at.block_table[3].long()
     assert torch.equal(at.k_cache[third].nan_to_num(7.0), cache[third].nan_to_num(7.0))
+
+
+def test_a_second_prompt_is_reported(cuda_ok):
+    """prompt() attends to its own tokens only: on a sequence that holds some
+    already it says so; sequences without new tokens may hold any."""
+    prob = bsa.SeqProblem.make(4, 2, 64)
+    at = layer(prob, 3, page=4)
+    gen = torch.Generator().manual_seed(5)
+    q, k, v = (torch.randn(9, x, 64, generator=gen).bfloat16().cuda() for x in (4, 2, 2))
+    at.prompt(q[:5], k[:5], v[:5], cu_of([5, 0, 0]))
+    at.prompt(q[:4], k[:4], v[:4], cu_of([0, 4, 0]))  # the first rests
+    at.check_status()
+    assert at.seq_lens.tolist() == [5, 4, 0]
+    at.prompt(q[:3], k[:3], v[:3], cu_of([0, 1, 2]))
+    with pytest.raises(bsa.BSAError, match="INVALID_ARG"):
+        at.check_status()
