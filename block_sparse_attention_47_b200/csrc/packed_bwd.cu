@@ -707,9 +707,10 @@ struct DkdvCfg {
   static constexpr int OFF_STG = 2 * TILE;     // [slot][Q | dO]
   static constexpr int OFF_VEC = OFF_STG + NR * 2 * TILE;  // [slot][lse2 128 | D 128] fp32
   static constexpr int OFF_BAR = OFF_VEC + NR * 1024;
-  // full[NR] s_ready dp_ready dp_read st_issued p_ready ds_ready x_free own
-  // fix_go fixed done drain[2]
-  static constexpr int N_BARS = NR + 13;
+  // full[NR] s_ready dp_ready dp_read st_issued p_ready[2] ds_ready x_free own
+  // fix_go fixed done drain[2].  p_ready has a barrier per region: P^T of step
+  // p+1 may be in before the thread of the sums has looked for step p's.
+  static constexpr int N_BARS = NR + 14;
   static constexpr int OFF_MISC = OFF_BAR + 8 * N_BARS;
   static constexpr int SMEM = OFF_MISC + 64 + 1024;
   static constexpr uint32_t TMEM_COLS = 512;
@@ -739,7 +740,7 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t sK = base + C::OFF_K, sV = base + C::OFF_V;
   const uint32_t full = base + C::OFF_BAR, s_ready = full + 8 * NR, dp_ready = s_ready + 8;
   const uint32_t dp_read = dp_ready + 8, st_issued = dp_read + 8;
-  const uint32_t p_ready = st_issued + 8, ds_ready = p_ready + 8;
+  const uint32_t p_ready = st_issued + 8, ds_ready = p_ready + 16;
   const uint32_t x_free = ds_ready + 8, own = x_free + 8;
   const uint32_t fix_go = own + 8, fixed = fix_go + 8, done = fixed + 8, drain = done + 8;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);
@@ -795,6 +796,7 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(dp_read, 8);
       mbar_init(st_issued, 1);
       mbar_init(p_ready, 8);
+      mbar_init(p_ready + 8, 8);
       mbar_init(ds_ready, 8);
       mbar_init(x_free, 1);
       mbar_init(own, 1);
@@ -954,7 +956,7 @@ __global__ void __launch_bounds__(384, 1)
                       sdesc_sw128(rows + kk * 2048, C::BOX, 1024), idesc_acc,
                       (p > 0 || kk > 0) ? 1u : 0u);
         };
-        ok = mbar_wait(p_ready, p & 1, abort_flag);
+        ok = mbar_wait(p_ready + 8 * (p & 1), (p >> 1) & 1, abort_flag);
         if (!ok) break;
         sums(C::COL_DV, cS, doslot(p));
         // dK is queued behind the next S^T, which the groups wait for first
@@ -1032,7 +1034,7 @@ __global__ void __launch_bounds__(384, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_ready);
+      if (lane == 0) mbar_arrive(p_ready + 8 * (p & 1));
       // dS^T = P^T * (dP^T - D) beside P^T, 32 columns at a time
       ok = __all_sync(0xffffffffu, mbar_wait(dp_ready, p & 1, abort_flag));
       if (!ok) break;
