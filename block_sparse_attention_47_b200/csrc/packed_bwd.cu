@@ -918,8 +918,9 @@ __global__ void __launch_bounds__(384, 1)
           tc_mma_ss(tmem + cS, sdesc_sw128(sK + off, 16, 1024),
                     sdesc_sw128(qslot(p) + off, 16, 1024), idesc_s, kk > 0);
         }
-        tc_commit(s_ready);
+        // before s_ready: whoever has P^T of this step then finds its phase over
         mbar_arrive(st_issued);
+        tc_commit(s_ready);
         // dP^T once the accumulations of step p-1 have read P^T and dS^T from its region
         if (p > 0) ok = mbar_wait(x_free, (p - 1) & 1, abort_flag);
         if (!ok) break;
@@ -959,7 +960,9 @@ __global__ void __launch_bounds__(384, 1)
         ok = mbar_wait(p_ready + 8 * (p & 1), (p >> 1) & 1, abort_flag);
         if (!ok) break;
         sums(C::COL_DV, cS, doslot(p));
-        // dK is queued behind the next S^T, which the groups wait for first
+        // dK is queued behind the next S^T, which the groups wait for first; so
+        // x_free of step p comes only after load p + 1, and the copies cannot
+        // be overtaken at x_free
         ok = (p + 1 == np || mbar_wait(st_issued, (p + 1) & 1, abort_flag)) &&
              mbar_wait(ds_ready, p & 1, abort_flag);
         if (!ok) break;

@@ -8,7 +8,8 @@ Hazard checks: no slot is reloaded before its readers have finished, no product
 reads a slot that does not hold its own tiles, no column of tensor memory is
 overwritten before it was read, every product reads what its own step wrote,
 outputs are read after the last product, and every role finishes.  Planted
-mistakes (a wait left out, one barrier for two regions) are caught.
+mistakes (a wait left out, one barrier for two regions, a signal behind the commit
+that it must precede) are caught.
 """
 import heapq
 import itertools
@@ -184,7 +185,7 @@ def dkdv(sim, n, tails, wrong=None):
     ring = Slots("Q/dO", NR)
     region = [Columns("region %d" % r, 8) for r in range(2)]   # S^T, then P^T; or dP^T
     region_ds = [Columns("dS^T of region %d" % r, 8) for r in range(2)]
-    log = dict(dv=0, dk=0)
+    log = dict(dv=0, dk=0, s=-1)
 
     def p_of(p):  # the barrier of step p's P^T and its parity
         return (p_ready[0], p & 1) if wrong == "one p_ready" else (p_ready[p & 1], (p >> 1) & 1)
@@ -216,9 +217,14 @@ def dkdv(sim, n, tails, wrong=None):
                 yield ("wait", dp_read, (p - 1) & 1)
             ring.use(p, p)
             region[p & 1].put(("S", p))
+            log["s"] = p
             yield ("mma", 512, lambda p=p: ring.free(p, p, "S"))
-            yield ("commit", s_ready)
-            yield ("arrive", st_issued)
+            if wrong == "late st_issued":
+                yield ("commit", s_ready)
+                yield ("arrive", st_issued)
+            else:
+                yield ("arrive", st_issued)
+                yield ("commit", s_ready)
             if p > 0 and wrong != "x_free of dP":
                 yield ("wait", x_free, (p - 1) & 1)
             ring.use(p, p)
@@ -235,6 +241,8 @@ def dkdv(sim, n, tails, wrong=None):
             yield ("mma", 512, lambda p=p: (region[p & 1].take(("P", p)), ring.free(p, p, "dV"), log.update(dv=p + 1)))
             if p + 1 < n and wrong != "no st_issued":
                 yield ("wait", st_issued, (p + 1) & 1)
+                if log["s"] < p + 1:
+                    raise Hazard("dK of step %d queued in front of the next S^T" % p)
             if wrong != "ds_ready":
                 yield ("wait", ds_ready, p & 1)
             region_ds[p & 1].see(("dS", p))
@@ -627,6 +635,7 @@ def test_no_hazard(kernel):
 @pytest.mark.parametrize("kernel,wrong", [
     ("dkdv", "one p_ready"),            # the accumulations may look two phases late
     ("dkdv", "no st_issued"),           # and then so may the copies at x_free
+    ("dkdv", "late st_issued"),         # dK in front of the S^T that the groups wait for
     ("dkdv", "no wait of the copies"), ("dkdv", "dp_read"), ("dkdv", "x_free of dP"), ("dkdv", "ds_ready"),
     ("dq", "kempty"), ("dq", "own"), ("dq", "read"), ("dq", "x_free"),
     ("forward", "empty"), ("forward", "q_free"), ("forward", "info_free"), ("forward", "fixed"), ("forward", "o"),
