@@ -42,9 +42,10 @@
 //
 // fp16.  P and dS enter the accumulations as 16-bit values.  P <= 1 is scaled
 // by 2^13.  dS is scaled by the power of two that puts its largest possible
-// value, 2 max_i |dO_i| max_j |V_j| (2-norms over the rows of a kv head), at
-// 2^15, so that it neither overflows nor sinks below fp16's range whatever
-// the scale of the loss.  bf16 needs neither.
+// value, 2 max_i |dO_i| max_j |V_j| (2-norms over the sequence's rows of a kv
+// head), at 2^15, so that it does not overflow, and loses bits only below
+// 2^-29 of that value, whatever the scale of the loss and of the sequences
+// beside it.  bf16 needs neither.
 #include "seq_internal.cuh"
 
 namespace bsa {
@@ -81,9 +82,17 @@ __device__ __forceinline__ int key_steps(bool causal, int last, int lq, int lk) 
   return ((causal ? min(lk, max(0, last + 1 + lk - lq)) : lk) + 127) >> 7;
 }
 
-// the power of two of dS for one kv head (fp16), from the largest squared norms
-__device__ __forceinline__ float ds_factor(const float* __restrict__ norms, int kvh, int kv_heads) {
-  const float bound = 2.f * sqrtf(__ldcg(norms + kvh)) * sqrtf(__ldcg(norms + kv_heads + kvh));
+// fp16: where a sequence's largest squared norms stand, of dO rows and, behind
+// them, of V rows: kv_heads each
+__device__ __forceinline__ int64_t norms_at(int seq, int kvh, int kv_heads) {
+  return 2 * int64_t(seq) * kv_heads + kvh;
+}
+
+// the power of two of dS for one sequence and kv head (fp16)
+__device__ __forceinline__ float ds_factor(const float* __restrict__ norms, int seq, int kvh,
+                                           int kv_heads) {
+  const float* at = norms + norms_at(seq, kvh, kv_heads);
+  const float bound = 2.f * sqrtf(__ldcg(at)) * sqrtf(__ldcg(at + kv_heads));
   if (!(bound > 0.f) || isinf(bound)) return 1.f;
   return exp2f(fminf(fmaxf(floorf(15.f - log2f(bound)), -60.f), 60.f));
 }
@@ -122,71 +131,42 @@ __device__ __forceinline__ void write_channels(uint32_t stage, uint32_t tcol, T*
 // ============================================================================
 // D = rowsum(dO * O), the statistics' layout, and the norms for fp16
 // ============================================================================
-// largest squared norm of a V row per kv head (fp16): block `part` of `parts`
-template <int D>
-__device__ __forceinline__ void v_norms(const SeqGeo& g, const PackedBwdIO& io, int part, int parts,
-                                        int kvh) {
-  constexpr int TPR = D / 8;
-  const int lane = threadIdx.x & 31;
-  // rows that a sequence owns: from the first offset to the last
-  const int64_t lo = max(0, __ldg(io.cu_k)), hi = min(int64_t(__ldg(io.cu_k + io.n_seqs)), io.total_k);
-  float most = 0.f;
-  for (int64_t r0 = lo + int64_t(part) * (256 / TPR); r0 < hi; r0 += int64_t(parts) * (256 / TPR)) {
-    const int64_t r = r0 + threadIdx.x / TPR;
-    float sq = 0.f;
-    if (r < hi) {
-      const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const __half*>(io.v.p) + r * io.v.sn +
-                                                      int64_t(kvh) * io.v.sh + (threadIdx.x % TPR) * 8);
-      const uint32_t av[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 x = unpack2<__half>(av[i]);
-        sq = fmaf(x.x, x.x, sq);
-        sq = fmaf(x.y, x.y, sq);
-      }
-    }
-#pragma unroll
-    for (int o = TPR / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-    most = fmaxf(most, sq);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-  if (lane == 0)
-    atomicMax(reinterpret_cast<int*>(io.norms) + g.kv_heads + kvh, __float_as_int(most));
-}
-
 template <typename T, int D>
 __global__ void __launch_bounds__(256) bwd_prepare_kernel(SeqGeo g, const PackedBwdIO io,
                                                           int tiles) {
   cudaTriggerProgrammaticLaunchCompletion();  // dQ may set itself up
-  if constexpr (std::is_same<T, __half>::value) {
-    // the blocks behind the tiles' look at V
-    if (int(blockIdx.x) >= tiles) {
-      if (int(blockIdx.y) < g.kv_heads)
-        v_norms<D>(g, io, int(blockIdx.x) - tiles, int(gridDim.x) - tiles, blockIdx.y);
-      return;
-    }
-  }
+  constexpr bool kHalf = std::is_same<T, __half>::value;
   constexpr int TPR = D / 8;  // threads per row, 16 bytes each
-  __shared__ int where[6];    // any, sequence, tile, first row, length, keys
+  __shared__ int where[6];    // any, sequence, tile, first row, length, length of the others
   __shared__ float top[8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // fp16: the blocks behind the tiles' look at V, a key tile and kv head each
+  const bool of_v = kHalf && int(blockIdx.x) >= tiles;
+  int64_t tile = blockIdx.x;
+  int head = blockIdx.y;
+  if (of_v) {
+    const int64_t i = (tile - tiles) * gridDim.y + blockIdx.y;
+    tile = i / g.kv_heads;
+    head = int(i - tile * g.kv_heads);
+  }
   if (warp == 0) {
-    const Tile f = find_tile<kWalkQ>(io.cu_q, io.total_q, io.cu_k, io.total_k, io.n_seqs, g.causal,
-                                     128, blockIdx.x, lane, io.status);
+    const Tile f = find_tile<kWalkQ>(of_v ? io.cu_k : io.cu_q, of_v ? io.total_k : io.total_q,
+                                     of_v ? io.cu_q : io.cu_k, of_v ? io.total_q : io.total_k,
+                                     io.n_seqs, g.causal, 128, tile, lane, io.status);
     if (lane == 0)
       where[0] = f.any, where[1] = f.seq, where[2] = f.tile, where[3] = f.a.start,
       where[4] = f.a.len, where[5] = f.b.len;
   }
   __syncthreads();
   if (!where[0]) return;
-  const int b = where[1], t = where[2], head = blockIdx.y;
-  const Span q{where[3], where[4]};
+  const int b = where[1], t = where[2];
+  const Span q{where[3], where[4]};  // of V: the keys
   // D of tiles of few key steps comes from dQ: there O and (but for its norms
   // in fp16) dO need not be read
   const bool summed =
-      !std::is_same<T, __half>::value &&
+      !kHalf &&
       key_steps(g.causal, min(t * 128 + 128, q.len) - 1, q.len, where[5]) <= kExactSteps;
+  const Rows z_rows = of_v ? io.v : io.dout;
   const int64_t stats = stat_rows(io.total_q, io.n_seqs);
   const int64_t out0 = int64_t(head) * stats + stat_start(q.start, b) + int64_t(t) * 128;
   float most = 0.f;
@@ -197,10 +177,12 @@ __global__ void __launch_bounds__(256) bwd_prepare_kernel(SeqGeo g, const Packed
     if (row < q.len && !summed) {
       const int64_t at = q.start + row;
       const int c = (threadIdx.x % TPR) * 8;
-      const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const T*>(io.o.p) + at * io.o.sn +
-                                                      int64_t(head) * io.o.sh + c);
-      const uint4 z = *reinterpret_cast<const uint4*>(static_cast<const T*>(io.dout.p) +
-                                                      at * io.dout.sn + int64_t(head) * io.dout.sh + c);
+      uint4 a = make_uint4(0u, 0u, 0u, 0u);
+      if (!of_v)
+        a = *reinterpret_cast<const uint4*>(static_cast<const T*>(io.o.p) + at * io.o.sn +
+                                            int64_t(head) * io.o.sh + c);
+      const uint4 z = *reinterpret_cast<const uint4*>(static_cast<const T*>(z_rows.p) +
+                                                      at * z_rows.sn + int64_t(head) * z_rows.sh + c);
       const uint32_t av[4] = {a.x, a.y, a.z, a.w}, zv[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -217,7 +199,7 @@ __global__ void __launch_bounds__(256) bwd_prepare_kernel(SeqGeo g, const Packed
       sq += __shfl_xor_sync(0xffffffffu, sq, o);
     }
     most = fmaxf(most, sq);
-    if (threadIdx.x % TPR == 0) {
+    if (threadIdx.x % TPR == 0 && !of_v) {
       float lse = INFINITY;
       if (row < q.len) {
         lse = __ldg(io.lse + int64_t(head) * io.total_q + q.start + row);
@@ -227,7 +209,7 @@ __global__ void __launch_bounds__(256) bwd_prepare_kernel(SeqGeo g, const Packed
       io.stat_delta[out0 + r] = row < q.len ? acc : 0.f;
     }
   }
-  if constexpr (std::is_same<T, __half>::value) {
+  if constexpr (kHalf) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
     if (lane == 0) top[warp] = most;
@@ -235,7 +217,9 @@ __global__ void __launch_bounds__(256) bwd_prepare_kernel(SeqGeo g, const Packed
     if (threadIdx.x == 0) {
       for (int w = 1; w < 8; ++w) most = fmaxf(most, top[w]);
       // non-negative floats order as their bits; a maximum has no order of arrival
-      atomicMax(reinterpret_cast<int*>(io.norms) + head / g.group, __float_as_int(most));
+      float* to = io.norms + (of_v ? norms_at(b, head, g.kv_heads) + g.kv_heads
+                                   : norms_at(b, head / g.group, g.kv_heads));
+      atomicMax(reinterpret_cast<int*>(to), __float_as_int(most));
     }
   }
 }
@@ -556,7 +540,7 @@ __global__ void __launch_bounds__(384, 1)
       const int64_t at = int64_t(head) * stat_rows(io.total_q, io.n_seqs) + stat_start(q0, seq) + r;
       lse2 = __ldcg(io.stat_lse + at);
       dlt = __ldcg(io.stat_delta + at);
-      if constexpr (kHalf) fac = ds_factor(io.norms, kvh, g.kv_heads);
+      if constexpr (kHalf) fac = ds_factor(io.norms, seq, kvh, g.kv_heads);
     }
     const float sl2 = g.scale * kLog2e;
     const uint32_t tS = tmem + C::COL_S + 64u * grp + lane_base;
@@ -983,7 +967,7 @@ __global__ void __launch_bounds__(384, 1)
     const bool exists = any && kr < Lk;
     const float sl2 = g.scale * kLog2e;
     if (kHalf) cudaGridDependencySynchronize();  // the norms
-    const float fac = kHalf && np > 0 ? ds_factor(io.norms, kvh, g.kv_heads) : 1.f;
+    const float fac = kHalf && np > 0 ? ds_factor(io.norms, seq, kvh, g.kv_heads) : 1.f;
     const float fac_p = kHalf ? fac * exp2f(-kPShift) : 1.f;
     const float shift = kHalf ? kPShift : 0.f;
     bool ok = true;
@@ -1120,7 +1104,7 @@ __global__ void __launch_bounds__(384, 1)
     if (any && !*abort_flag) {
       // rank c writes rows c, c + ranks, .. of both: 16-byte output chunks
       constexpr int CH = D / 8;
-      const float fac = kHalf ? ds_factor(io.norms, kvh, g.kv_heads) : 1.f;
+      const float fac = kHalf ? ds_factor(io.norms, seq, kvh, g.kv_heads) : 1.f;
       for (int i = threadIdx.x; i < 2 * (128 / ranks) * CH; i += C::kThreads) {
         const int ch = i % CH, rr = (i / CH) * ranks + rank, grp = rr >> 7, row = rr & 127;
         if (first + row >= Lk) continue;
@@ -1195,6 +1179,11 @@ cudaError_t launch_after(K kern, unsigned ctas, int ranks, int threads, int smem
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// the norms of every sequence and kv head, dO's and V's
+size_t norm_count(const SeqGeo& g, int64_t n_seqs) {
+  return 2 * size_t(g.kv_heads) * size_t(g.fp16 && n_seqs > 1 ? n_seqs : 1);
+}
+
 template <typename T, int D>
 cudaError_t launch_t(const SeqGeo& g, const CUtensorMap* maps, const PackedBwdIO& io,
                      cudaStream_t st) {
@@ -1204,10 +1193,9 @@ cudaError_t launch_t(const SeqGeo& g, const CUtensorMap* maps, const PackedBwdIO
     const int64_t n_tiles = tiles(io.total_q);
     int64_t v_blocks = 0;
     if (std::is_same<T, __half>::value) {
-      e = cudaMemsetAsync(io.norms, 0, 2 * sizeof(float) * g.kv_heads, st);
+      e = cudaMemsetAsync(io.norms, 0, sizeof(float) * norm_count(g, io.n_seqs), st);
       if (e != cudaSuccess) return e;
-      v_blocks = (io.total_k + 255) / 256;
-      v_blocks = v_blocks < 256 ? v_blocks : 256;
+      if (io.total_k > 0) v_blocks = (tiles(io.total_k) * g.kv_heads + g.heads - 1) / g.heads;
     }
     bwd_prepare_kernel<T, D>
         <<<dim3(unsigned(n_tiles + v_blocks), g.heads), 256, 0, st>>>(g, io, int(n_tiles));
@@ -1243,7 +1231,7 @@ cudaError_t launch_t(const SeqGeo& g, const CUtensorMap* maps, const PackedBwdIO
 
 size_t packed_bwd_workspace_bytes(const SeqGeo& g, int64_t total_q, int64_t n_seqs) {
   // statistics (lse2 and D per head and padded row) and the norms
-  return sizeof(float) * (2 * size_t(g.heads) * stat_rows(total_q, n_seqs) + 2 * size_t(g.kv_heads));
+  return sizeof(float) * (2 * size_t(g.heads) * stat_rows(total_q, n_seqs) + norm_count(g, n_seqs));
 }
 
 void packed_bwd_workspace_split(const SeqGeo& g, PackedBwdIO* io, void* workspace) {

@@ -106,7 +106,7 @@ struct PackedBwdIO {
   Rows o, dout, v, dq, dk, dv;
   const float* lse;    // [heads, total_q] from the forward
   // workspace: statistics per head and padded row, the largest squared norms
-  // of dO and V rows per kv head (fp16)
+  // of dO and V rows per sequence and kv head (fp16)
   float *stat_lse, *stat_delta, *norms;
   int32_t* status;
   int stall;

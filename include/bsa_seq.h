@@ -140,7 +140,7 @@ bsa_status bsa_query_packed_bwd_workspace(const bsa_seq_problem* prob, int32_t n
  * rows no sequence owns are left as they were.  Sums are fp32, in a fixed
  * order without atomics, so gradients do not vary from run to run; P and dS
  * are rounded to the element type for their products (in fp16 with scales
- * that keep them in its range).
+ * that keep them in its range, taken for each sequence from its own rows).
  *   q, k, v, cu_q, cu_k   the forward's
  *   o, lse                its results;  dout the gradient of o, [total_q,
  *                         heads, head_dim], strides not 0

@@ -453,3 +453,48 @@ def test_bwd_binding_refuses(cuda_ok):
     with pytest.raises(bsa.BSAError, match="broadcast"):
         bsa.packed_attn_bwd(*a)
     bsa.packed_attn_bwd(*ok)
+
+
+# fp16 scales dS by a power of two; it has to come from the sequence's own rows
+@pytest.mark.parametrize("H,K,d", [(2, 1, 64), (4, 2, 128), (20, 20, 64)])
+@pytest.mark.parametrize("many", [False, True])
+def test_bwd_fp16_beside_a_large_neighbour(cuda_ok, H, K, d, many):
+    """Rows of sequence 0 grow by 2^15 in dO and V together: the gradients of
+    the others stay bit for bit, within bounds from their own maxima."""
+    lens = [300, 200, 64] + ([3] * 40 if many else [])
+    q, k, v = inputs(lens, lens, H, K, d, FP, tail=0)
+    gen = torch.Generator().manual_seed(21)
+    dout = torch.randn(q.shape, generator=gen)
+    v, dout = v.clone(), dout.cuda()
+    v[300:] *= 2.0 ** -4
+    dout[300:] *= 2.0 ** -6
+    dout = dout.half()
+    prob, cu = bsa.SeqProblem.make(H, K, d, FP), cu_of(lens)
+    a = backward(prob, q, k, v, dout, cu, cu)
+    v[:300] *= 2.0 ** 6
+    dout[:300] *= 2.0 ** 9
+    b = backward(prob, q, k, v, dout, cu, cu)
+    for x, y in zip(a[:3], b[:3]):
+        assert torch.equal(x[300:], y[300:])
+    at = 300
+    for n in lens[1:4]:
+        s = slice(at, at + n)
+        check_bwd(q[s], k[s], v[s], dout[s], [n], [n], True, *(x[s] for x in b[:3]), 1 / math.sqrt(d))
+        at += n
+
+
+@pytest.mark.parametrize("value", [math.inf, math.nan])
+def test_bwd_fp16_one_dead_value_stays_where_it_is(cuda_ok, value):
+    lens = [200, 130, 64]
+    q, k, v = inputs(lens, lens, 2, 1, 64, FP, tail=0)
+    v, dout = v.clone(), torch.randn(q.shape, device="cuda").half()
+    v[:200] *= 2.0 ** -7
+    dout[:200] *= 2.0 ** -7
+    prob, cu = bsa.SeqProblem.make(2, 1, 64, FP), cu_of(lens)
+    a = backward(prob, q, k, v, dout, cu, cu)
+    dout[230, 0, 5] = value
+    b = backward(prob, q, k, v, dout, cu, cu)
+    for x, y in zip(a[:3], b[:3]):
+        for s in (slice(0, 200), slice(330, 394)):
+            assert torch.equal(x[s], y[s])
+    assert not bool(b[0][230, 0].isfinite().any())

@@ -272,3 +272,10 @@ def prob_of():
 def test_rows_of_a_packed_call_are_limited():
     rc = call("bsa_packed_attn_bwd", seq._PACKED, bwd_args(tk=(1 << 30) + 1, n_seqs=1))
     assert rc == SHAPE and b"2^30" in bsa.lib().bsa_last_error()
+
+
+def test_bwd_fp16_workspace_has_the_norms_of_every_sequence():
+    for n in (1, 3, 1000):
+        rows = 128 * (500 // 128 + n + 1)
+        assert bsa.packed_bwd_workspace_bytes(prob(dtype=torch.float16), 500, n) == \
+            4 * (2 * 8 * rows + 2 * 2 * n)
