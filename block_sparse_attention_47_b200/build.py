@@ -10,6 +10,7 @@ is newer than the library.
 import concurrent.futures as cf
 import glob
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -22,6 +23,10 @@ LIB = os.path.join(PKG, "libbsa.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I" + os.path.join(ROOT, "include")]
+
+# Kernels whose warps exchange registers: their split adds up to the threads
+# times this many, and with any other number the exchange would not end
+REGISTERS = {"packed_fwd_kernel": 168}
 
 
 def nvcc():
@@ -47,16 +52,26 @@ def up_to_date():
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def check_registers(log, required=None):
+    """Raises unless every kernel named in `required` is in ptxas' report with
+    that many registers a thread."""
+    required = REGISTERS if required is None else required
+    used = re.findall(r"Compiling entry function '(\w+)'.*?Used (\d+) registers", log, re.S)
+    for kernel, n in required.items():
+        got = [int(r) for name, r in used if kernel in name]
+        if not got or any(r != n for r in got):
+            raise RuntimeError("%s has to take %d registers a thread; the compiler's report has %s"
+                               % (kernel, n, sorted(set(got)) or "none"))
+
+
 def build(verbose=False, force=False, ptxas_verbose=False):
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
-    extra = ["-Xptxas", "-v"] if ptxas_verbose else []
-
     def one(src):
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-        cmd = [cc, *ARCH, *FLAGS, *extra, "-c", src, "-o", obj]
+        cmd = [cc, *ARCH, *FLAGS, "-Xptxas", "-v", "-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, obj, r
 
@@ -71,6 +86,7 @@ def build(verbose=False, force=False, ptxas_verbose=False):
             failed = True
     if failed:
         raise RuntimeError("libbsa.so build failed")
+    check_registers("\n".join(r.stdout + r.stderr for _, _, r in results))
     tmp = LIB + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-o", tmp] + [obj for _, obj, _ in results]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -627,14 +627,20 @@ cudaError_t launch_t(const SeqGeo& g, const CUtensorMap* maps, const PackedIO& i
                      int ranks, cudaStream_t st) {
   using C = FwdCfg<D>;
   auto kern = packed_fwd_kernel<T, D, HEADS, SPLIT>;
-  // the register split waits for ever unless the launch brings 168 a thread
-  static const int regs = [&] {
+  // The register split waits for ever unless the launch brings 168 a thread:
+  // the build checks that, and so does the first launch (an error of the query
+  // itself is the call's and not kept).
+  static std::atomic<bool> fits{false};
+  cudaError_t e;
+  if (!fits.load(std::memory_order_acquire)) {
     cudaFuncAttributes a{};
-    return cudaFuncGetAttributes(&a, kern) == cudaSuccess ? a.numRegs : 0;
-  }();
-  if (regs != 168) return cudaErrorInvalidConfiguration;
+    e = cudaFuncGetAttributes(&a, kern);
+    if (e != cudaSuccess) return e;
+    if (a.numRegs != 168) return cudaErrorInvalidConfiguration;
+    fits.store(true, std::memory_order_release);
+  }
   static std::atomic<uint64_t> seen{0};
-  cudaError_t e = allow_smem(kern, C::SMEM, seen);
+  e = allow_smem(kern, C::SMEM, seen);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   const int sms = device_sms();

@@ -279,3 +279,14 @@ def test_bwd_fp16_workspace_has_the_norms_of_every_sequence():
         rows = 128 * (500 // 128 + n + 1)
         assert bsa.packed_bwd_workspace_bytes(prob(dtype=torch.float16), 500, n) == \
             4 * (2 * 8 * rows + 2 * 2 * n)
+
+
+def test_the_build_checks_the_registers_of_a_split():
+    from block_sparse_attention_47_b200 import build
+    line = ("ptxas info    : Compiling entry function '_Z%s' for 'sm_100a'\n"
+            "    0 bytes stack frame\nptxas info    : Used %d registers, used 1 barriers\n")
+    good = line % ("17packed_fwd_kernelIfE", 168) + line % ("5other", 30)
+    build.check_registers(good)
+    for bad in (good + line % ("17packed_fwd_kernelIhE", 160), line % ("5other", 168), ""):
+        with pytest.raises(RuntimeError, match="registers"):
+            build.check_registers(bad)
