@@ -44,6 +44,8 @@
 // Tensor memory (512 columns): S_u/P_u at 128 u, O_u at 256 + 128 u.
 // Every wait is bounded and reports BSA_ERR_TIMEOUT: 2 s, 20 s where it may last
 // as long as another tile's walk.
+#include <cmath>
+
 #include "seq_internal.cuh"
 
 namespace bsa {
@@ -657,26 +659,39 @@ cudaError_t launch_t(const SeqGeo& g, const CUtensorMap* maps, const PackedIO& i
   return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], g, io, units);
 }
 
-// CTAs that share a tile's keys, where a CTA per tile leaves half of the 148 SMs
-// idle.  us with 1 | 2 | 4 | 8 CTAs a tile (d = 128, bf16; queries x keys):
-//   32 tiles, 512 x 5,000 of 16 heads:     80 |  51 |  37 |  84
-//   64 tiles, 512 x 8,000 of 32/8 heads:  121 |  70 |  88 | 165
-//   12 tiles, 384 x 5,000 of 8/2 heads:    79 |  49 |  33 |  30
-//   16 tiles, 512 x 30,000 of 8 heads:    427 | 218 | 119 | 145
-// so one wave of CTAs for one sequence, and no more than 112 in clusters of
-// eight, of which few find room at a time.  Sequences of several lengths even
-// out over two waves (256, 511 and 64 queries to 5,000, 511 and 2,113 keys: 76 |
-// 45 | 41 | 72).  Short walks: 1 query to 1,000 keys of 8/2 heads 21 us by one, 12
-// by four; 513 to 513 of 16/8 heads 16.6 and 18.5; 384 to 1,500 of 8/2 heads 20.7
-// by four, 23.0 by eight; 130 to 2,000 18.0 and 16.5.
+// CTAs that share a tile's keys, where a CTA per tile leaves half of the SMs
+// idle.  Only the sums of the lengths are known here: a walk is taken to have
+// total_k / 128 / n^0.6 key steps, between those of n equal sequences and the
+// longest of unequal ones.  us with 1 | 2 | 4 | 8 CTAs a tile (bf16):
+//   1 x 1,000 of 8/2 heads, 4 tiles:              20 |  14 |  11 |  11
+//   384 x 5,000 of 8/2 heads, 12 tiles:           79 |  49 |  33 |  31
+//   512 x 5,000 of 16 heads, 32 tiles:            80 |  50 |  37 |  83
+//   600 x 1,200 of 16/8 heads, 40 tiles:          24 |  19 |  30 |  44
+//   512 x 8,000 of 32/8 heads, 64 tiles:         111 |  63 |  75 | 128
+//   8 x (250 x 250) of 4/2 heads:                 11 |  18 |  19 |  47
+//   30 x (1 x 128) of 8/2 heads:                  10 |  20 |  36 |  72
+//   16 x (1 x 4,000) of 8/2 heads:                60 |  35 |  43 |  71
+//   256, 511, 64 x 5,000, 511, 2,113 of 16/2:     73 |  43 |  39 |  65
+// So one wave of CTAs, and clusters of eight, of which few find room at a time,
+// on half of the SMs.  Long walks of several sequences may take two waves of
+// fours, and eights three quarters of the SMs: from 30 steps on 0.63 to 0.74
+// of the time by twos where lengths differ, 1.16 to 1.22 where they are equal.
+// Over 5,330 batches of 1 to 32 sequences, equal or log-uniform up to 20,000
+// keys, this takes 1.09 times the best of the four sizes on average, 1.21 with
+// the batch's keys in place of a walk's, 1.51 without clusters.
 int split_ranks(const PackedIO& io, int64_t rows, int slots) {
+  const int sms = device_sms();
   // the sequences' last tiles are half full on average
   const int64_t units = ((io.total_q + rows - 1) / rows + io.n_seqs / 2) * slots;
-  const int64_t steps = io.total_k / 128;  // of a walk at most
-  if (units > 74 || steps < 6) return 1;
-  int ranks = steps >= 15 && units * 8 <= 112 ? 8 : 4;
-  if (ranks == 4 && units * 4 > (io.n_seqs > 1 ? 300 : 148)) ranks = 2;
-  return ranks;
+  if (2 * units > sms) return 1;
+  const bool one = io.n_seqs == 1;
+  const double steps = double(io.total_k) / 128 / (one ? 1. : std::pow(double(io.n_seqs), 0.6));
+  if (8 * units <= sms / 2 ? steps >= 8 : 8 * units <= sms * 3 / 4 && steps >= (one ? 15 : 25))
+    return 8;
+  if (4 * units <= sms / 2 ? steps >= 3
+                           : 4 * units <= (!one && steps >= 30 ? 2 * sms : sms) && steps >= 5)
+    return 4;
+  return steps >= 6 ? 2 : 1;
 }
 
 template <typename T, int D>

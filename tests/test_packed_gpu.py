@@ -498,3 +498,29 @@ def test_bwd_fp16_one_dead_value_stays_where_it_is(cuda_ok, value):
         for s in (slice(0, 200), slice(330, 394)):
             assert torch.equal(x[s], y[s])
     assert not bool(b[0][230, 0].isfinite().any())
+
+
+# a cluster's size comes from the lengths' sums: batches on both sides of every step
+SPLIT = [
+    ([1] * 30, [128] * 30, 8, 2, 64, BF),          # many walks of a step: none
+    ([250] * 8, [250] * 8, 4, 2, 128, FP),
+    ([1] * 16, [4000] * 16, 8, 2, 64, BF),         # twos, two waves of fours
+    ([1] * 8, [4000] * 8, 8, 2, 128, FP),          # fours
+    ([7, 130, 1], [600, 500, 700], 4, 2, 64, BF),  # eights
+    ([1, 1, 1, 300], [9, 20, 300, 300], 2, 2, 128, BF),
+    ([200, 1], [3000, 4000], 8, 8, 64, FP),
+    ([40] * 5, [2000, 3, 0, 900, 129], 2, 1, 128, BF),
+]
+
+
+@pytest.mark.parametrize("case", SPLIT, ids=[str(i) for i in range(len(SPLIT))])
+def test_fwd_shared_walks_of_several_sequences(cuda_ok, case):
+    lq, lk, H, K, d, dt = case
+    q, k, v = inputs(lq, lk, H, K, d, dt)
+    prob, st = bsa.SeqProblem.make(H, K, d, dt), status_word()
+    out, lse = torch.full_like(q, 5.0), torch.full((H, q.shape[0]), 5.0, device="cuda")
+    bsa.packed_attn_fwd(prob, q, k, v, cu_of(lq), cu_of(lk), out, lse, dev_status=st)
+    assert int(st) == 0
+    check_fwd(q, k, v, lq, lk, True, out, lse, 1 / math.sqrt(d))
+    n = sum(lq)
+    assert bool((out[n:] == 5.0).all()) and bool((lse[:, n:] == 5.0).all())
