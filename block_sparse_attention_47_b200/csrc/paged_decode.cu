@@ -10,7 +10,9 @@
 // uses the whole GPU and a ragged batch leaves no SM idle.  A share that
 // covers a (sequence, set) whole writes its output; the others leave (max,
 // sum, O) in the workspace, two slots per CTA and head group, and a second
-// kernel joins them in position order.  Where no
+// kernel joins them in position order, a CTA per border of two shares (one per
+// sequence and head group cost the square of the batch, as each looks at all
+// lengths: 65,536 sequences of 40 keys 15.1 ms).  Where no
 // sequence can be longer than 512 keys and the (sequence, head group) pairs
 // fit the SMs, each takes a CTA whole and there is nothing to join.
 //
@@ -138,6 +140,53 @@ __device__ __forceinline__ int64_t active_ctas(int64_t total, int64_t n, int hw)
   return a < 1 ? 1 : (a < n ? a : n);
 }
 
+// A CTA's share [s, e) of the `total` units, and where s lies: unit `rem` of
+// the pair (b, set).  All threads of the block; `scratch`: one int64
+// per warp and two more.  Lengths out of range are reported where `status` is given.
+struct Share {
+  int64_t s, e, total, rem;
+  int b, set;
+};
+template <int kThreads>
+__device__ __forceinline__ Share find_share(const Shape& sh, int64_t cta, int64_t n_ctas,
+                                            int64_t* scratch, int32_t* status) {
+  Share f{};
+  const int per = (sh.n_seqs + kThreads - 1) / kThreads;
+  const int b_lo = min(sh.n_seqs, int(threadIdx.x) * per), b_hi = min(sh.n_seqs, b_lo + per);
+  int64_t mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) {
+    mine += int64_t(sh.units(b)) * sh.sets;
+    if (status) {
+      const int n = __ldg(sh.lens + b);
+      if (n < 0 || n > sh.max_len) report_invalid(status);
+    }
+  }
+  const int64_t before = block_scan<kThreads>(mine, scratch, f.total);
+  const int64_t active = active_ctas(f.total, n_ctas, sh.hw);
+  f.s = cta < active ? f.total * cta / active : f.total;
+  f.e = cta < active ? f.total * (cta + 1) / active : f.total;
+  if (f.s >= f.e) return f;
+  int* where = reinterpret_cast<int*>(scratch + kThreads / 32);  // b, then units before it
+  if (before <= f.s && f.s < before + mine) {
+    int64_t at = before;
+    int b = b_lo;
+    for (;; ++b) {
+      const int64_t u = int64_t(sh.units(b)) * sh.sets;
+      if (f.s < at + u) break;
+      at += u;
+    }
+    where[0] = b;
+    *reinterpret_cast<int64_t*>(where + 2) = at;
+  }
+  __syncthreads();
+  f.b = where[0];
+  f.rem = f.s - *reinterpret_cast<int64_t*>(where + 2);
+  const int n = sh.units(f.b);
+  f.set = int(f.rem / n);
+  f.rem -= int64_t(f.set) * n;
+  return f;
+}
+
 // a (sequence, head group) without a key: its output is 0
 template <typename T, int D>
 __device__ __forceinline__ void zero_output(const SeqGeo& g, const DecodeIO& io, int b, int hg) {
@@ -187,40 +236,12 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
       return;
     }
   } else {
-    const int per = (sh.n_seqs + kThreads - 1) / kThreads;
-    const int b_lo = min(sh.n_seqs, int(threadIdx.x) * per), b_hi = min(sh.n_seqs, b_lo + per);
-    int64_t mine = 0;
-    for (int b = b_lo; b < b_hi; ++b) {
-      mine += int64_t(sh.units(b)) * sh.sets;
-      if (blockIdx.x == 0) {
-        const int n = __ldg(sh.lens + b);
-        if (n < 0 || n > sh.max_len) report_invalid(io.status);
-      }
-    }
-    int64_t total;
-    const int64_t before = block_scan<kThreads>(mine, scratch, total);
-    const int64_t active = active_ctas(total, gridDim.x, hw);
-    s = cta < active ? total * cta / active : total;
-    e = cta < active ? total * (cta + 1) / active : total;
+    const Share f = find_share<kThreads>(sh, cta, gridDim.x, scratch,
+                                         blockIdx.x == 0 ? io.status : nullptr);
+    s = f.s, e = f.e;
     if (s >= e) return;
-    int* where = reinterpret_cast<int*>(scratch + kDecWarps);  // b, then units before it
-    if (before <= s && s < before + mine) {
-      int64_t at = before;
-      int b = b_lo;
-      for (;; ++b) {
-        const int64_t u = int64_t(sh.units(b)) * sh.sets;
-        if (s < at + u) break;
-        at += u;
-      }
-      where[0] = b;
-      *reinterpret_cast<int64_t*>(where + 2) = at;
-    }
-    __syncthreads();
-    b0 = where[0];
-    rem0 = s - *reinterpret_cast<int64_t*>(where + 2);
-    const int n = sh.units(b0);
-    hg0 = int(rem0 / n);
-    rem0 -= int64_t(hg0) * n;
+    b0 = f.b, hg0 = f.set;
+    rem0 = f.rem;
   }
 
   // ---- the copies: this warp's units s + pl, s + pl + pw, .. of the list
@@ -481,44 +502,44 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
 }
 
 // The parts of each (sequence, head group) that several CTAs shared, in
-// position order.
+// position order: a CTA per border of two shares and head group of a set.
+// Sequences without a key get their zeros here.
 template <typename T, int D>
 __global__ void __launch_bounds__(128)
     paged_decode_join_kernel(SeqGeo g, const DecodeIO io, Shape sh, int n_ctas) {
   using C = DecCfg<D>;
   constexpr int kThreads = 128;
-  __shared__ int64_t scratch[kThreads / 32 + 1];
+  __shared__ int64_t scratch[kThreads / 32 + 2];
   __shared__ float sml[2][kMaxCtas][kHeadTile];
-  const int b = blockIdx.x / sh.hgroups, hg = blockIdx.x - b * sh.hgroups;
-  int64_t before = 0, all = 0;
-  for (int i = threadIdx.x; i < sh.n_seqs; i += kThreads) {
-    const int64_t u = int64_t(sh.units(i)) * sh.sets;
-    all += u;
-    if (i < b) before += u;
+  const int lane = threadIdx.x & 31;
+  for (int64_t at = (int64_t(blockIdx.x) * kThreads + threadIdx.x) & ~31; at < sh.n_seqs;
+       at += int64_t(gridDim.x) * kThreads) {
+    uint32_t none = __ballot_sync(0xffffffffu, at + lane < sh.n_seqs && sh.len(int(at) + lane) == 0);
+    for (; none; none &= none - 1) {
+      T* out = static_cast<T*>(io.o.p) + (at + __ffs(none) - 1) * io.o.sn;
+      for (int i = lane; i < g.heads * (D / 8); i += 32) {
+        const int h = i / (D / 8);
+        *reinterpret_cast<uint4*>(out + h * io.o.sh + (i - h * (D / 8)) * 8) =
+            make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
   }
-  int64_t total, s0;
-  block_scan<kThreads>(all, scratch, total);
-  __syncthreads();
-  block_scan<kThreads>(before, scratch, s0);
+  const int c = blockIdx.x / sh.hw, hl = blockIdx.x - c * sh.hw;
+  const Share f = find_share<kThreads>(sh, c, n_ctas, scratch, nullptr);
   cudaGridDependencySynchronize();
-  const int n_units = sh.units(b);
+  if (f.s >= f.e || f.rem == 0) return;  // no share, or one that begins with a pair
+  const int b = f.b, hg = f.set * sh.hw + hl;
   const int hsub = (g.group + kHeadTile - 1) / kHeadTile;
   const int kvh = hg / hsub, row0 = (hg - kvh * hsub) * kHeadTile;
   const int rows = min(kHeadTile, g.group - row0);
   T* out = static_cast<T*>(io.o.p) + int64_t(b) * io.o.sn +
            (int64_t(kvh) * g.group + row0) * io.o.sh;
-  if (n_units == 0) {
-    zero_output<T, D>(g, io, b, hg);
-    return;
-  }
-  const int set = hg / sh.hw, hl = hg - set * sh.hw;
-  s0 += int64_t(set) * n_units;
-  const int64_t s1 = s0 + n_units;
-  const int64_t active = active_ctas(total, n_ctas, sh.hw);
+  const int64_t total = f.total, active = active_ctas(total, n_ctas, sh.hw);
+  const int64_t s0 = f.s - f.rem, s1 = s0 + sh.units(b);
   // the CTA whose share holds unit i
   const int c0 = int(((s0 + 1) * active + total - 1) / total) - 1;
   const int c1 = int((s1 * active + total - 1) / total) - 1;
-  if (c0 == c1) return;
+  if (c != c0 + 1) return;  // an earlier border lies in it, too
   const int parts = c1 - c0 + 1;
   const float* ws = static_cast<const float*>(io.workspace);
   auto slot = [&](int i) {
@@ -586,7 +607,7 @@ cudaError_t launch_t(const SeqGeo& g, const PagedCache& c, const DecodeIO& io, c
   if (e != cudaSuccess || whole) return e;
   // the join's launch overlaps the first kernel; it waits for its results itself
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(io.n_seqs) * unsigned(sh.hgroups));
+  cfg.gridDim = dim3(unsigned(ctas) * unsigned(sh.hw));
   cfg.blockDim = dim3(128);
   cfg.stream = st;
   cudaLaunchAttribute attr{};

@@ -319,3 +319,29 @@ def test_binding_refuses(cuda_ok):
     with pytest.raises(ValueError):
         bsa.paged_attn_decode(*ok, dev_status=torch.zeros(1, device="cuda"))
     bsa.paged_attn_decode(*ok)
+
+
+@pytest.mark.parametrize("n,H,K,d,dt", [(5000, 4, 4, 64, BF), (3001, 34, 2, 64, FP), (300000, 1, 1, 64, BF)])
+def test_decode_many_sequences(cuda_ok, n, H, K, d, dt):
+    """Thousands of caches, some empty, some shared by several CTAs."""
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    lens = torch.randint(0, 60, (n,), generator=gen, device="cuda", dtype=torch.int32)
+    lens[::7] = 0
+    lens[n // 2] = 4000
+    page, pages, width = 16, 4096, 250
+    kc, vc = (torch.randn(pages, page, K, d, generator=gen, device="cuda").to(dt) for _ in range(2))
+    table = torch.full((n, width), -1, dtype=torch.int32, device="cuda")
+    reach = torch.arange(width, device="cuda")[None] < ((lens + page - 1) // page)[:, None]
+    table[reach] = torch.randint(0, pages, (int(reach.sum()),), generator=gen, device="cuda", dtype=torch.int32)
+    q = torch.randn(n, H, d, generator=gen, device="cuda").to(dt)
+    prob, out, st = bsa.SeqProblem.make(H, K, d, dt), torch.full_like(q, 5.0), status_word()
+    ws = torch.full((bsa.decode_workspace_bytes(prob),), 255, dtype=torch.uint8, device="cuda")
+    bsa.paged_attn_decode(prob, q, kc, vc, table, lens, out, ws, dev_status=st)
+    assert int(st) == 0
+    assert bool((out[lens == 0] == 0).all())
+    at = torch.cat([torch.tensor([0, 1, 2, n // 2 - 1, n // 2, n // 2 + 1, n - 1]),
+                    torch.randint(0, n, (50,), generator=torch.Generator().manual_seed(7))]).cuda()
+    check_decode(q[at], kc, vc, table[at], lens[at].tolist(), out[at], 1 / math.sqrt(d))
+    again = torch.empty_like(out)
+    bsa.paged_attn_decode(prob, q, kc, vc, table, lens, again, ws)
+    assert torch.equal(again, out)
