@@ -6,7 +6,8 @@
 // the sums over the query heads h of a kv head.
 //
 // Bound by the tensor cores: 10 d flops per (query head, seen pair), 14 with
-// the scores and dP formed in both kernels.  Two kernels rather than one with
+// the scores and dP formed in both kernels, 18 where dQ forms them twice (see
+// D below).  Two kernels rather than one with
 // atomic dQ sums, so that gradients do not vary from run to run:
 //   dQ     CTA = 128 query rows of a head, walking the key tiles they see.
 //   dK/dV  CTA = 128 keys of a kv head, walking the query tiles that see them

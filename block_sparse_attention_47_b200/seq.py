@@ -297,7 +297,8 @@ class PagedAttention:
     word (check_status) and written nowhere.
 
     `seq_lens` holds the cached tokens of each sequence; prompt() and step()
-    add the new tokens to it.  prompt() runs on every sequence of the cache in
+    add the new tokens to it.  Rows of a padded batch, behind the last
+    sequence's, are not set in what the calls return.  prompt() runs on every sequence of the cache in
     order, one without new tokens having length 0 in cu; step() on the first
     ones, as many as it gets tokens."""
 

@@ -28,8 +28,8 @@
  * written and may hold anything, NaN included; rows of a sequence must be
  * finite.  Offsets that descend or leave the tensor are reported as
  * BSA_ERR_INVALID_ARG through the status word and read as an empty sequence;
- * among more than 32 sequences they may leave rows of others unwritten.  At
- * most 2^30 rows a tensor.
+ * where they make sequences overlap, or among more than 32 sequences, they may
+ * leave rows of others unwritten or written twice.  At most 2^30 rows a tensor.
  *
  * Paged cache.  k_cache and v_cache share the strides (stride_page,
  * stride_token, stride_head), element strides that are multiples of 8, of a
@@ -127,7 +127,8 @@ typedef struct bsa_decode_args {
 bsa_status bsa_packed_attn_fwd(const bsa_seq_problem* prob, const bsa_packed_args* args,
                                int32_t* dev_status, void* stream);
 
-/* Bytes of bsa_packed_attn_bwd's workspace (row statistics).  Host only. */
+/* Bytes of bsa_packed_attn_bwd's workspace (row statistics, in fp16 the largest
+ * norms of each sequence).  Host only. */
 bsa_status bsa_query_packed_bwd_workspace(const bsa_seq_problem* prob, int32_t n_seqs,
                                           int64_t total_q, size_t* bytes);
 
@@ -135,8 +136,8 @@ bsa_status bsa_query_packed_bwd_workspace(const bsa_seq_problem* prob, int32_t n
  *   dV = P^T dO,  dP = dO V^T,  D_i = sum_j P_ij dP_ij,  dS = P * (dP - D),
  *   dQ = softmax_scale dS K,  dK = softmax_scale dS^T Q,
  * (D is rowsum(dO * O), and taken as that from the rounded o for query tiles
- * that see more than 1,024 keys), dK and dV summed over the query heads of their kv head; P is recomputed
- * from lse.  Every row of a sequence is written (0 where nothing was seen),
+ * that see more than 1,024 keys), dK and dV summed over the query heads of
+ * their kv head; P is recomputed from lse.  Every row of a sequence is written (0 where nothing was seen),
  * rows no sequence owns are left as they were.  Sums are fp32, in a fixed
  * order without atomics, so gradients do not vary from run to run; P and dS
  * are rounded to the element type for their products (in fp16 with scales
